@@ -419,6 +419,14 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     uint32_t sb[2] = {rs[r][0], rs[r][1]};
                     fetch(ch + kPRing, rw[r], rs[r]);
                     const int hbuf = cc % AB;
+                    // a last chunk that ends before this group's steps: the group writes nothing, but
+                    // arrives for buffer hbuf all the same, so it too waits for the buffer's last use
+                    // (a phase ahead, its arrival would stand in for the other group's)
+                    if (ch * CS + SPG * g >= nk && cc >= AB &&
+                        !mbar_wait(chunk_empty((cc - AB) % XS), (uint32_t)(((cc - AB) / XS) & 1), &abort_s)) {
+                        ok = false;
+                        break;
+                    }
 #pragma unroll
                     for (int e = 0; e < SPG; ++e) {
                         const int st = SPG * g + e;

@@ -85,6 +85,10 @@ extern "C" {
 #define SHERRY_OP_UNPACK 2
 
 #define SHERRY_MAX_K 262144
+#define SHERRY_MAX_RANK 128       /* rank of an adapter */
+#define SHERRY_MAX_ADAPTERS 1024  /* adapters of one call */
+#define SHERRY_MAX_TOP 32         /* likeliest tokens of a row */
+#define SHERRY_MAX_VOCAB 16777216
 
 /* ---- sizes ------------------------------------------------------------- */
 
@@ -256,6 +260,106 @@ int sherry_arenas_linear(const uint16_t* X, int64_t M, int64_t N, int64_t K,
                          const uint32_t* idx, const uint8_t* sgn, const float* scales, int granularity, int group,
                          const uint16_t* Wd, float lambda, void* Y, int y_dtype, void* stream);
 float sherry_arenas_lambda(int64_t step, int64_t total, float lambda0);
+
+/* ---- input gradient of the packed linear -----------------------------------
+ * dX[m][k] = sum_n dY[m][n] t[n][k] alpha(n,k), bf16, for training whatever lies
+ * below a frozen packed weight ("Sherry, Tequila and Fairies in Python" section
+ * 1.1: the layer is F.linear(x, w), whose gradient in x is dY w).
+ *   dY       bf16 [M][N] row-major; read only
+ *   dX       bf16 [M][K]; fully overwritten
+ *   workspace  sherry_linear_backward_workspace_bytes(M, N, K) bytes of scratch
+ *            (no tickets; need not be zero)
+ * Accumulated in fp32.  alpha varies along the sum, so it is rounded to bf16 (in a
+ * unit where the first scale is 1.875, so that a per-tensor scale is exact): each
+ * term carries a relative error of up to 2^-8 of its own, typically below 2^-9.
+ * Any valid shape. */
+int sherry_linear_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K,
+                           const uint32_t* idx, const uint8_t* sgn, const float* scales, int granularity, int group,
+                           uint16_t* dX, void* workspace, size_t workspace_bytes, void* stream);
+size_t sherry_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* ---- low-rank adapters beside the packed linear ------------------------------
+ * Y[m] = X[m] (T alpha)^T + U[m] B_a^T with U[m] = scaling[a] X[m] A_a^T and
+ * a = ids[m], the token's adapter: many requests, each with its own, share one
+ * launch over the frozen packed weight.
+ *   A        bf16 [n_adapters][rank][K], B bf16 [n_adapters][N][rank] (16-byte
+ *            aligned); 1 <= n_adapters <= SHERRY_MAX_ADAPTERS, rank a multiple of 8
+ *            up to SHERRY_MAX_RANK (adapters of lower rank: pad with zeros)
+ *   ids      int32 [M]; any value outside [0, n_adapters) (use -1): no adapter.  In
+ *            any order; tokens of one adapter next to each other are cheapest
+ *   scaling  fp32 [n_adapters], or NULL for 1
+ *   U        fp32 [M][rank] (16-byte aligned), optional (NULL): written, zero for
+ *            tokens of no adapter; the backward pass wants it
+ *   Y        as sherry_linear
+ *   workspace  sherry_linear_lora_workspace_bytes(...) bytes, a linear workspace:
+ *            its first 256 KiB zero before first use, left zero by every call
+ * fp32 accumulation; U enters tensor-core products as bf16 terms that keep 16 (bf16
+ * Y) or 24 (fp32 Y) significant bits. */
+int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K,
+                       const uint32_t* idx, const uint8_t* sgn, const float* scales, int granularity, int group,
+                       const uint16_t* A, const uint16_t* B, const int32_t* ids, const float* scaling,
+                       int n_adapters, int rank, float* U, void* Y, int y_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+size_t sherry_linear_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int granularity, int group,
+                                          int n_adapters, int rank, int y_dtype);
+
+/* Gradients of sherry_linear_lora, with P[m] = scaling[a] dY[m] B_a and sums over the
+ * tokens of adapter a (scaling is a constant; T alpha is frozen):
+ *   dX       bf16 [M][K] = dY (T alpha) + P A_a, as sherry_linear_backward; or NULL
+ *   dA       [n_adapters][rank][K] = sum P[m]^T X[m] (grad_dtype); or NULL
+ *   dB       [n_adapters][N][rank] = sum dY[m]^T U[m] (grad_dtype), U from the forward
+ *            call; or NULL (U may then be NULL)
+ * An adapter without tokens gets zeros.  X may be NULL when dA is.
+ *   workspace  sherry_linear_lora_backward_workspace_bytes(...) bytes of scratch (no
+ *            tickets; need not be zero; 256-byte aligned) */
+int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t N, int64_t K,
+                                const uint32_t* idx, const uint8_t* sgn, const float* scales, int granularity,
+                                int group, const uint16_t* A, const uint16_t* B, const int32_t* ids,
+                                const float* scaling, int n_adapters, int rank, const float* U,
+                                uint16_t* dX, void* dA, void* dB, int grad_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream);
+size_t sherry_linear_lora_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int n_adapters, int rank);
+
+/* ---- log probabilities of tokens ---------------------------------------------
+ * For every row z of logits, p = softmax(z):
+ *   logp     fp32 [M]: log p(targets[m]); 0 for a target outside [0, V) (left out)
+ *   entropy  fp32 [M]: -sum p log p; or NULL
+ *   stats    fp32 [M][2]: the largest logit m and log sum exp(z - m) (their sum is
+ *            the log-sum-exp; apart they keep p exact to fp32 at any offset)
+ *   top_logp, top_ids  [M][top]: the `top` likeliest tokens, best first, ties to the
+ *            lowest index, 0 <= top <= min(V, SHERRY_MAX_TOP) (0: both NULL)
+ *   logits   [M][V] fp32 or bf16, rows ld >= V elements apart, aligned to their
+ *            element; read once.  1 <= V <= SHERRY_MAX_VOCAB
+ *   targets  int32 [M], or NULL (then logp NULL)
+ * -inf (a banned token) has p = 0.  A row of -inf only: logp -inf, entropy 0, stats
+ * (-inf, 0), the lowest indices.  A row with NaN or +inf: NaN everywhere, top_ids -1.
+ * No workspace. */
+int sherry_token_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
+                          int top, float* logp, float* entropy, float* stats, float* top_logp, int32_t* top_ids,
+                          void* stream);
+/* Their gradient: dlogits = g (onehot(target) - p) - h p (log p + entropy), with
+ * g = dlogp[m] (0 where the target is left out) and h = dentropy[m].
+ *   stats, entropy  from sherry_token_logprobs (entropy may be NULL with dentropy)
+ *   dlogp    fp32 [M], or NULL (0); dentropy  fp32 [M], or NULL (0)
+ *   dlogits  [M][V] in the logits' type, rows ldd >= V apart; may be logits itself with
+ *            ldd = ld, otherwise must not overlap it
+ * Exactly 0 where p is 0 (the target apart) and in rows of -inf only. */
+int sherry_token_logprobs_backward(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld,
+                                   const int32_t* targets, const float* stats, const float* entropy,
+                                   const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                                   void* stream);
+
+/* ---- a packed head, scored -----------------------------------------------------
+ * sherry_token_logprobs of the fp32 logits X (T alpha)^T of a packed weight [N][K],
+ * N the vocabulary, computed for chunks of tokens so that only a chunk's logits
+ * exist at a time.
+ *   workspace  sherry_linear_logprobs_workspace_bytes(...) bytes, a linear workspace
+ *            (first 256 KiB zero before first use, left zero by every call) */
+int sherry_linear_logprobs(const uint16_t* X, int64_t M, int64_t N, int64_t K,
+                           const uint32_t* idx, const uint8_t* sgn, const float* scales, int granularity, int group,
+                           const int32_t* targets, int top, float* logp, float* entropy, float* stats,
+                           float* top_logp, int32_t* top_ids, void* workspace, size_t workspace_bytes, void* stream);
+size_t sherry_linear_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t K, int granularity, int group);
 
 /* ---- chained linears (dependent phases) -----------------------------------
  * `count` linears with the same M (e.g. one decode token through a layer

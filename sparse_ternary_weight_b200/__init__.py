@@ -441,3 +441,376 @@ def unpack(P: PackedWeight, out=None):
     check(lib().sherry_unpack(_ptr(P.idx), _ptr(P.sgn), _ptr(P.scales), P.N, P.K, P.granularity, P.group,
                               _ptr(out), _stream(P.idx.device)), "unpack")
     return out
+
+
+# ---- adapters and the input gradient -------------------------------------------------------------------
+
+def _stream_workspace(nbytes: int, device) -> "object":
+    """A zero-filled linear workspace of this stream of ``device``.  Calls on different
+    streams may overlap, so each stream keeps its own; under graph capture each call
+    gets a buffer of its graph's own (zeroed by the graph), since a graph may be
+    replayed beside other graphs and eager calls."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    key = (str(device), "linear", _stream(device))
+    seen = lib().sherry_timeout_count()
+    if seen != _ws_timeouts[0]:
+        _ws_cache.clear()
+        _ws_timeouts[0] = seen
+    buf = _ws_cache.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        _ws_cache[key] = buf
+    return buf
+
+
+def _scratch(nbytes: int, device) -> "object":
+    """Uninitialised scratch of one call, from torch's stream-ordered allocator."""
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
+
+
+def _same_device(device, *ts):
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("tensors must be on one CUDA device")
+
+
+def _activations(X, K, what="X"):
+    import torch
+    _require_cuda(X)
+    if X.dtype != torch.bfloat16 or X.dim() != 2 or X.shape[1] != K:
+        raise ValueError(f"{what} must be a 2D bf16 tensor with {K} columns")
+    return X.contiguous()
+
+
+def _adapters(X, P, A, B, ids, scaling):
+    """Checked and contiguous (A, B, ids, scaling, n_adapters, rank)."""
+    import torch
+    _require_cuda(A, B, ids, scaling)
+    _same_device(X.device, P.idx, A, B, ids, scaling)
+    if A.dtype != torch.bfloat16 or A.dim() != 3 or A.shape[2] != P.K:
+        raise ValueError("A must be bf16 [n_adapters, rank, K]")
+    n, R = A.shape[0], A.shape[1]
+    if B.dtype != torch.bfloat16 or tuple(B.shape) != (n, P.N, R):
+        raise ValueError("B must be bf16 [n_adapters, N, rank]")
+    if not 1 <= n <= _abi.MAX_ADAPTERS:
+        raise ValueError(f"1 to {_abi.MAX_ADAPTERS} adapters per call")
+    if R % 8 or not 8 <= R <= _abi.MAX_RANK:
+        raise ValueError(f"the rank must be a multiple of 8 up to {_abi.MAX_RANK} (pad with zeros)")
+    if ids.dtype not in (torch.int32, torch.int64) or tuple(ids.shape) != (X.shape[0],):
+        raise ValueError("ids must be int32 or int64 [M]")
+    if scaling is not None and (scaling.dtype != torch.float32 or tuple(scaling.shape) != (n,)):
+        raise ValueError("scaling must be fp32 [n_adapters]")
+    if ids.dtype == torch.int64:  # a value int32 cannot hold names no adapter
+        ids = ids.clamp(-1, n).to(torch.int32)
+    return (A.contiguous(), B.contiguous(), ids.contiguous(), None if scaling is None else scaling.contiguous(), n, R)
+
+
+def _result(out, shape, dtype, device):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.dtype != dtype or tuple(out.shape) != tuple(shape) or not out.is_contiguous() or out.device != device:
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def linear_lora(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None, out=None, return_u: bool = False):
+    """The packed linear with a low-rank adapter per token: Y[m] = X[m] (T alpha)^T +
+    U[m] B_a^T with U[m] = scaling[a] X[m] A_a^T and a = ids[m].  A is bf16
+    [n_adapters, rank, K], B bf16 [n_adapters, N, rank] (rank a multiple of 8), ids
+    int32 or int64 [M] in any order (a value outside [0, n_adapters): no adapter),
+    scaling fp32 [n_adapters] or None for 1.  With ``return_u`` returns (Y, U), U fp32
+    [M, rank], which :func:`linear_lora_backward` takes."""
+    import torch
+    X = _activations(X, P.K)
+    A, B, ids, scaling, n, R = _adapters(X, P, A, B, ids, scaling)
+    M = X.shape[0]
+    out_dtype = out_dtype or torch.float32
+    yd = {torch.float32: F32, torch.bfloat16: BF16}[out_dtype]
+    out = _result(out, (M, P.N), out_dtype, X.device)
+    U = torch.empty((M, R), dtype=torch.float32, device=X.device) if return_u else None
+    if return_u and P.N == 0:
+        U.zero_()
+    with torch.cuda.device(X.device):
+        L = lib()
+        wsb = L.sherry_linear_lora_workspace_bytes(M, P.N, P.K, P.granularity, P.group, n, R, yd)
+        ws = _stream_workspace(wsb, X.device) if wsb else None
+        check(L.sherry_linear_lora(_ptr(X), M, P.N, P.K, _ptr(P.idx), _ptr(P.sgn), _ptr(P.scales), P.granularity,
+                                   P.group, _ptr(A), _ptr(B), _ptr(ids), _ptr(scaling), n, R, _ptr(U), _ptr(out), yd,
+                                   _ptr(ws), wsb, _stream(X.device)), "linear_lora")
+    return (out, U) if return_u else out
+
+
+def linear_backward(dY, P: PackedWeight, out=None):
+    """Input gradient of the packed linear: dX [M,K] = dY [M,N] (T alpha), bf16."""
+    import torch
+    dY = _activations(dY, P.N, "dY")
+    _same_device(dY.device, P.idx)
+    M = dY.shape[0]
+    out = _result(out, (M, P.K), torch.bfloat16, dY.device)
+    with torch.cuda.device(dY.device):
+        L = lib()
+        wsb = L.sherry_linear_backward_workspace_bytes(M, P.N, P.K)
+        ws = _scratch(wsb, dY.device)
+        check(L.sherry_linear_backward(_ptr(dY), M, P.N, P.K, _ptr(P.idx), _ptr(P.sgn), _ptr(P.scales), P.granularity,
+                                       P.group, _ptr(out), _ptr(ws), wsb, _stream(dY.device)), "linear_backward")
+    return out
+
+
+def linear_lora_backward(dY, X, P: PackedWeight, A, B, ids, U, scaling=None, grad_dtype=None,
+                         need=(True, True, True)):
+    """Gradients of :func:`linear_lora`: (dX bf16 [M,K], dA, dB) from dY (bf16 [M,N]) and
+    the U that the forward call returned; dA and dB are sums over each adapter's
+    tokens in ``grad_dtype`` (bf16, the default, or fp32).  ``need`` leaves out the
+    gradients that are not wanted (None in their place)."""
+    import torch
+    dY = _activations(dY, P.N, "dY")
+    X = _activations(X, P.K)
+    M = X.shape[0]
+    if dY.shape[0] != M:
+        raise ValueError("dY and X must have the same number of rows")
+    A, B, ids, scaling, n, R = _adapters(X, P, A, B, ids, scaling)
+    _same_device(X.device, dY, U)
+    if U is not None and (U.dtype != torch.float32 or tuple(U.shape) != (M, R)):
+        raise ValueError("U must be fp32 [M, rank]")
+    if need[2] and U is None:
+        raise ValueError("dB needs U of the forward pass")
+    U = None if U is None else U.contiguous()
+    grad_dtype = grad_dtype or torch.bfloat16
+    gd = {torch.float32: F32, torch.bfloat16: BF16}[grad_dtype]
+    dX = torch.empty_like(X) if need[0] else None
+    dA = torch.empty(A.shape, dtype=grad_dtype, device=X.device) if need[1] else None
+    dB = torch.empty(B.shape, dtype=grad_dtype, device=X.device) if need[2] else None
+    with torch.cuda.device(X.device):
+        L = lib()
+        wsb = L.sherry_linear_lora_backward_workspace_bytes(M, P.N, P.K, n, R)
+        ws = _scratch(wsb, X.device)
+        check(L.sherry_linear_lora_backward(_ptr(dY), _ptr(X), M, P.N, P.K, _ptr(P.idx), _ptr(P.sgn), _ptr(P.scales),
+                                            P.granularity, P.group, _ptr(A), _ptr(B), _ptr(ids), _ptr(scaling), n, R,
+                                            _ptr(U), _ptr(dX), _ptr(dA), _ptr(dB), gd, _ptr(ws), wsb,
+                                            _stream(X.device)), "linear_lora_backward")
+    return dX, dA, dB
+
+
+def _refuse_capture(what, explicit):
+    """Autograd's accumulation of a leaf's gradient runs on the stream where an earlier
+    graph of the same leaf was built; under capture that ends the capture, and the
+    process with it.  So the differentiable forms are not captured."""
+    import torch
+    if torch.cuda.is_initialized() and torch.is_grad_enabled() and torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"{what} cannot be captured into a CUDA graph: capture {explicit}")
+
+
+def _lora_function():
+    import torch
+
+    class SherryLinearLora(torch.autograd.Function):
+        """:func:`linear_lora` with :func:`linear_lora_backward`; the packed weight and
+        the scaling are constants."""
+
+        @staticmethod
+        def forward(ctx, X, A, B, P, ids, scaling, out_dtype):
+            Y, U = linear_lora(X, P, A, B, ids, scaling, out_dtype, return_u=True)
+            ctx.save_for_backward(X, A, B, ids, scaling, U)
+            ctx.packed = P
+            return Y
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dY):
+            X, A, B, ids, scaling, U = ctx.saved_tensors
+            need = ctx.needs_input_grad[:3]
+            # an fp32 gradient is rounded to the bf16 that the tensor cores multiply
+            dX, dA, dB = linear_lora_backward(dY.to(torch.bfloat16), X, ctx.packed, A, B, ids, U, scaling, need=need)
+            return dX, dA, dB, None, None, None, None
+
+    return SherryLinearLora
+
+
+_LORA = None
+
+
+def linear_lora_train(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None):
+    """Differentiable :func:`linear_lora`: gradients reach X, A and B (bf16, as the
+    tensors); the packed weight is frozen."""
+    global _LORA
+    _refuse_capture("linear_lora_train", "linear_lora and linear_lora_backward")
+    if _LORA is None:
+        _LORA = _lora_function()
+    return _LORA.apply(X, A, B, P, ids, scaling, out_dtype)
+
+
+# ---- log probabilities of tokens -------------------------------------------------------------------------
+
+@dataclass
+class TokenLogprobs:
+    """Of every row: log p(target) [M] (None without targets), entropy [M], stats [M,2]
+    (the largest logit, log of the sum of exp(z - largest)), and the likeliest
+    tokens' log probabilities and ids [M,top] (None for top = 0)."""
+    logp: "object"
+    entropy: "object"
+    stats: "object"
+    top_logp: "object"
+    top_ids: "object"
+
+    @property
+    def lse(self):
+        """log sum exp of the row's logits."""
+        return self.stats[:, 0] + self.stats[:, 1]
+
+
+def _logits(z):
+    import torch
+    _require_cuda(z)
+    if z.dim() != 2 or z.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be a 2D fp32 or bf16 tensor")
+    M, V = z.shape
+    if not 1 <= V <= _abi.MAX_VOCAB:
+        raise ValueError(f"1 to {_abi.MAX_VOCAB} logits per row")
+    if (V > 1 and z.stride(1) != 1) or (M > 1 and z.stride(0) < V):
+        z = z.contiguous()
+    return z, BF16 if z.dtype == torch.bfloat16 else F32, (z.stride(0) if M > 1 else V)
+
+
+def _targets(t, M, V, device):
+    import torch
+    if t is None:
+        return None
+    _require_cuda(t)
+    _same_device(device, t)
+    if t.dtype not in (torch.int32, torch.int64) or tuple(t.shape) != (M,):
+        raise ValueError("targets must be int32 or int64 [M]")
+    if t.dtype == torch.int64:  # a value int32 cannot hold is outside [0, V) all the same
+        t = t.clamp(-1, V).to(torch.int32)
+    return t.contiguous()
+
+
+def _scores(M, V, targets, top, device):
+    import torch
+    if not 0 <= top <= min(V, _abi.MAX_TOP):
+        raise ValueError(f"top must be 0 to min(V, {_abi.MAX_TOP})")
+    f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)  # noqa: E731
+    return TokenLogprobs(f32(M) if targets is not None else None, f32(M), f32(M, 2), f32(M, top) if top else None,
+                         torch.empty((M, top), dtype=torch.int32, device=device) if top else None)
+
+
+def token_logprobs(logits, targets=None, top: int = 0) -> TokenLogprobs:
+    """Log probabilities of one given token per row, the entropy, and the ``top`` likeliest
+    tokens (ties to the lowest id) of logits [M,V] (fp32 or bf16; rows may be slices of
+    a padded buffer), in one pass.  targets is int32 or int64 [M]; a value outside
+    [0, V) is left out (log p 0, no gradient).  -inf logits have p = 0; a row of -inf
+    only gives -inf and entropy 0, one with NaN or +inf gives NaN and ids -1."""
+    import torch
+    z, dt, ld = _logits(logits)
+    M, V = z.shape
+    targets = _targets(targets, M, V, z.device)
+    r = _scores(M, V, targets, top, z.device)
+    with torch.cuda.device(z.device):
+        check(lib().sherry_token_logprobs(_ptr(z), dt, M, V, ld, _ptr(targets), top, _ptr(r.logp), _ptr(r.entropy),
+                                          _ptr(r.stats), _ptr(r.top_logp), _ptr(r.top_ids), _stream(z.device)),
+              "token_logprobs")
+    return r
+
+
+def token_logprobs_backward(logits, targets, stats, entropy, dlogp=None, dentropy=None, out=None):
+    """Gradient of :func:`token_logprobs` in the logits, [M,V] in their type:
+    dlogp (onehot(target) - p) - dentropy p (log p + entropy).  ``out`` may be the logits
+    themselves (rows in place) or a tensor that does not overlap them."""
+    import torch
+    z, dt, ld = _logits(logits)
+    M, V = z.shape
+    targets = _targets(targets, M, V, z.device)
+    _require_cuda(stats, entropy, dlogp, dentropy, out)
+    _same_device(z.device, stats, entropy, dlogp, dentropy, out)
+    vec = []
+    for t, shape, name in ((stats, (M, 2), "stats"), (entropy, (M,), "entropy"), (dlogp, (M,), "dlogp"),
+                           (dentropy, (M,), "dentropy")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be fp32 {list(shape)}")
+        vec.append(None if t is None else t.contiguous())
+    stats, entropy, dlogp, dentropy = vec
+    if stats is None or (dentropy is not None and entropy is None) or (dlogp is not None and targets is None):
+        raise ValueError("needs stats, targets with dlogp, and entropy with dentropy")
+    if out is None:
+        out = torch.empty((M, V), dtype=z.dtype, device=z.device)
+    elif (out.dtype != z.dtype or tuple(out.shape) != (M, V) or (V > 1 and out.stride(1) != 1)
+          or (M > 1 and out.stride(0) < V)):
+        raise ValueError("out must be [M, V] of the logits' type with rows of unit stride")
+    elif M > 0 and _spans_overlap(z, out) and not (out.data_ptr() == z.data_ptr() and (M == 1 or out.stride(0) == ld)):
+        raise ValueError("out must be the logits themselves or not overlap them")
+    ldd = out.stride(0) if M > 1 else V
+    with torch.cuda.device(z.device):
+        check(lib().sherry_token_logprobs_backward(_ptr(z), dt, M, V, ld, _ptr(targets), _ptr(stats), _ptr(entropy),
+                                                   _ptr(dlogp), _ptr(dentropy), _ptr(out), ldd, _stream(z.device)),
+              "token_logprobs_backward")
+    return out
+
+
+def _spans_overlap(a, b) -> bool:
+    """Whether the address ranges of two row-strided matrices meet."""
+    def span(t):
+        return t.data_ptr(), t.data_ptr() + ((t.shape[0] - 1) * t.stride(0) + t.shape[1]) * t.element_size()
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _logprobs_function():
+    import torch
+
+    class SherryTokenLogprobs(torch.autograd.Function):
+        """log p(target) and entropy with :func:`token_logprobs_backward`."""
+
+        @staticmethod
+        def forward(ctx, logits, targets):
+            r = token_logprobs(logits, targets)
+            ctx.save_for_backward(logits, targets, r.stats, r.entropy)
+            ctx.set_materialize_grads(False)
+            return r.logp, r.entropy
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dlogp, dentropy):
+            if dlogp is None and dentropy is None:
+                return None, None
+            logits, targets, stats, entropy = ctx.saved_tensors
+            return token_logprobs_backward(logits, targets, stats, entropy, dlogp, dentropy), None
+
+    return SherryTokenLogprobs
+
+
+_LOGPROBS = None
+
+
+def token_logprobs_train(logits, targets):
+    """Differentiable (log p(target), entropy) of every row; the loss of a model is, say,
+    ``-logp.mean()``."""
+    global _LOGPROBS
+    _refuse_capture("token_logprobs_train", "token_logprobs and token_logprobs_backward")
+    if _LOGPROBS is None:
+        _LOGPROBS = _logprobs_function()
+    return _LOGPROBS.apply(logits, targets)
+
+
+def linear_logprobs(X, P: PackedWeight, targets=None, top: int = 0) -> TokenLogprobs:
+    """:func:`token_logprobs` of a packed head's logits X (T alpha)^T (P.N is the
+    vocabulary), a chunk of tokens at a time, so that only a chunk's logits exist."""
+    import torch
+    X = _activations(X, P.K)
+    _same_device(X.device, P.idx)
+    M = X.shape[0]
+    if not 1 <= P.N <= _abi.MAX_VOCAB:
+        raise ValueError(f"a head has 1 to {_abi.MAX_VOCAB} rows")
+    targets = _targets(targets, M, P.N, X.device)
+    r = _scores(M, P.N, targets, top, X.device)
+    with torch.cuda.device(X.device):
+        L = lib()
+        wsb = L.sherry_linear_logprobs_workspace_bytes(M, P.N, P.K, P.granularity, P.group)
+        ws = _stream_workspace(wsb, X.device) if wsb else None
+        check(L.sherry_linear_logprobs(_ptr(X), M, P.N, P.K, _ptr(P.idx), _ptr(P.sgn), _ptr(P.scales), P.granularity,
+                                       P.group, _ptr(targets), top, _ptr(r.logp), _ptr(r.entropy), _ptr(r.stats),
+                                       _ptr(r.top_logp), _ptr(r.top_ids), _ptr(ws), wsb, _stream(X.device)),
+              "linear_logprobs")
+    return r

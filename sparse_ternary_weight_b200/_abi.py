@@ -16,6 +16,7 @@ F32, BF16 = 0, 1
 OP_QUANTIZE_PACK, OP_LINEAR, OP_UNPACK = 0, 1, 2
 MAX_K = 262144
 MAX_BATCH = 256
+MAX_RANK, MAX_ADAPTERS, MAX_TOP, MAX_VOCAB = 128, 1024, 32, 16777216
 NOALLOC_SCRATCH_BYTES = 16 << 20
 TEQUILA_ONES, TEQUILA_SIGN = 0, 1
 
@@ -65,6 +66,18 @@ SIGNATURES = {
                                                  i64]),
     "sherry_unpack": (i32, [vp, vp, vp, i64, i64, i32, i32, vp, vp]),
     "sherry_unpack_batched": (i32, [ctypes.POINTER(UnpackDesc), i32, vp]),
+    "sherry_linear_backward": (i32, [vp, i64, i64, i64, vp, vp, vp, i32, i32, vp, vp, sz, vp]),
+    "sherry_linear_backward_workspace_bytes": (sz, [i64, i64, i64]),
+    "sherry_linear_lora": (i32, [vp, i64, i64, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp, i32, vp, sz,
+                                 vp]),
+    "sherry_linear_lora_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, i32, i32]),
+    "sherry_linear_lora_backward": (i32, [vp, vp, i64, i64, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp,
+                                          vp, vp, i32, vp, sz, vp]),
+    "sherry_linear_lora_backward_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
+    "sherry_token_logprobs": (i32, [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp]),
+    "sherry_token_logprobs_backward": (i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp]),
+    "sherry_linear_logprobs": (i32, [vp, i64, i64, i64, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+    "sherry_linear_logprobs_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
     "sherry_linear_noalloc": (i32, [vp, i64, i64, i64, vp, vp, vp, i32, i32, vp, i32, vp]),
     "sherry_status_string": (ctypes.c_char_p, [i32]),
     "sherry_last_cuda_error": (i32, []),

@@ -1,6 +1,7 @@
 // api.cu -- the library's C ABI (declared in include/sherry.h): argument checks
 // on the host, then the launches.  Nothing here allocates device memory.
 #include "common.cuh"
+#include "lora.cuh"
 
 #include <algorithm>
 #include <atomic>
@@ -561,6 +562,329 @@ int sherry_linear_chain(const sherry_linear_desc* descs, int count, const int* p
         const int b = c.begin[ph], e = c.begin[ph + 1];
         if (e > b && (st = linear_launch(c.shapes.data() + b, c.descs.data() + b, e - b, M, y_dtype == SHERRY_BF16,
                                          workspace, sms, s)))
+            return st;
+    }
+    return SHERRY_OK;
+}
+
+// ---- adapters, input gradient, token log probabilities ---------------------------
+
+static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+static int check_ws(const void* workspace, size_t workspace_bytes, size_t need) {
+    if (need > 0 && (!workspace || workspace_bytes < need)) return SHERRY_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256)) return SHERRY_ERR_ALIGN;
+    return SHERRY_OK;
+}
+
+static int check_lora(int64_t M, int n_adapters, int rank) {
+    if (M < 0 || M > 0x3fffffff) return SHERRY_ERR_SHAPE;
+    if (n_adapters < 1 || n_adapters > SHERRY_MAX_ADAPTERS) return SHERRY_ERR_SHAPE;
+    if (rank < 8 || rank > SHERRY_MAX_RANK || rank % 8 != 0) return SHERRY_ERR_SHAPE;
+    return SHERRY_OK;
+}
+
+// Up to this many tokens the product into rank space runs without a plan of tokens by adapter.
+constexpr int64_t kLoraFew = 32;
+
+// The adapters' product is part of the prefill kernel where that is the kernel of the linear
+// and tokens are not so few that a streaming or few-token kernel takes them.
+static bool lora_in_prefill(const ProbShape& s, int64_t M) {
+    return prefill_eligible(s, M) && (M > kLoraFew || !skinny_eligible(s, M));
+}
+
+struct LoraWs {
+    size_t u, plan, y32, total;  // offsets (0: none) and size
+};
+
+// The linear's own workspace comes first and always keeps the ticket region to itself.
+static LoraWs lora_ws(const ProbShape& s, int64_t M, int n_adapters, int rank, int y_dtype) {
+    LoraWs w{};
+    const bool pre = lora_in_prefill(s, M);
+    size_t at = std::max(up256(pre ? 0 : linear_ws_bytes(&s, 1, M, device_sms())), kTicketBytes);
+    w.u = at;
+    at += up256((size_t)M * rank * sizeof(float));
+    if (pre || M > kLoraFew) {
+        w.plan = at;
+        at += lora_plan_bytes(M, n_adapters);
+    }
+    if (!pre && y_dtype == SHERRY_BF16) {
+        w.y32 = at;
+        at += (size_t)(M * s.N) * sizeof(float);
+    }
+    w.total = at;
+    return w;
+}
+
+size_t sherry_linear_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int granularity, int group, int n_adapters,
+                                          int rank, int y_dtype) {
+    if (check_shape(N, K) || check_gran(K, granularity, group) || check_lora(M, n_adapters, rank) || M == 0 || N == 0)
+        return 0;
+    return lora_ws(ProbShape{N, K, granularity, group}, M, n_adapters, rank, y_dtype).total;
+}
+
+int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* idx, const uint8_t* sgn,
+                       const float* scales, int granularity, int group, const uint16_t* A, const uint16_t* B,
+                       const int32_t* ids, const float* scaling, int n_adapters, int rank, float* U, void* Y,
+                       int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_lora(M, n_adapters, rank);
+    if (st) return st;
+    sherry_linear_desc d{X, idx, sgn, scales, Y, N, K, granularity, group};
+    if ((st = check_linear_desc(d, M))) return st;
+    if (y_dtype != SHERRY_F32 && y_dtype != SHERRY_BF16) return SHERRY_ERR_DTYPE;
+    if (M > 0 && N > 0 && (!A || !B || !ids)) return SHERRY_ERR_NULL;
+    if (!aligned(A, 16) || !aligned(B, 16) || !aligned(ids, 4) || !aligned(scaling, 4) || !aligned(U, 16))
+        return SHERRY_ERR_ALIGN;
+    if (M == 0 || N == 0) return SHERRY_OK;
+    const ProbShape s{N, K, granularity, group};
+    const LoraWs w = lora_ws(s, M, n_adapters, rank, y_dtype);
+    if ((st = check_ws(workspace, workspace_bytes, w.total))) return st;
+    char* ws = static_cast<char*>(workspace);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int sms = device_sms();
+    const bool bf16 = y_dtype == SHERRY_BF16;
+    float* u = U ? U : reinterpret_cast<float*>(ws + w.u);
+    LoraPlan plan{};
+    if (w.plan) {
+        plan = lora_plan_in(ws + w.plan, M, n_adapters);
+        if ((st = lora_plan_launch(ids, M, n_adapters, plan, cs))) return st;
+        st = lora_down_launch(X, K, M, K, A, K, rank, ids, scaling, n_adapters, plan, u, sms, cs);
+    } else {
+        st = lora_down_few_launch(X, K, M, K, A, K, rank, ids, scaling, n_adapters, u, cs);
+    }
+    if (st) return st;
+    if (lora_in_prefill(s, M)) return prefill_lora_launch(s, d, M, bf16, LoraArgs{B, u, ids, rank, plan}, cs);
+    float* y32 = bf16 ? reinterpret_cast<float*>(ws + w.y32) : static_cast<float*>(Y);
+    d.Y = y32;
+    if ((st = linear_launch(&s, &d, 1, M, 0, workspace, sms, cs))) return st;
+    return lora_up_launch(y32, M, N, u, B, rank, ids, n_adapters, Y, bf16, cs);
+}
+
+// Rows of dY whose bytes are no multiple of 16 are copied into padded ones: TMA and the vector
+// loads need the alignment.
+static int64_t padded_rows(int64_t N) { return (N + 7) & ~(int64_t)7; }
+
+struct BwdWs {
+    size_t pad, part, bt, p, plan, total;
+};
+
+static BwdWs backward_ws(int64_t M, int64_t N, int64_t K, int n_adapters, int rank) {
+    BwdWs w{};
+    size_t at = 0;
+    const int64_t ld = padded_rows(N);
+    w.pad = at;
+    if (ld != N) at += up256((size_t)(M * ld) * 2);
+    w.part = at;
+    at += up256(dgrad_workspace_bytes(M, N, K, device_sms()));
+    if (n_adapters > 0) {
+        w.bt = at;
+        at += up256((size_t)n_adapters * rank * (size_t)ld * 2);
+        w.p = at;
+        at += up256((size_t)M * rank * sizeof(float));
+        w.plan = at;
+        at += lora_plan_bytes(M, n_adapters);
+    }
+    w.total = at;
+    return w;
+}
+
+static int check_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const uint32_t* idx, const uint8_t* sgn,
+                          const float* scales, int granularity, int group, const uint16_t* dX) {
+    if (M < 0 || M > 0x3fffffff) return SHERRY_ERR_SHAPE;
+    int st = check_shape(N, K);
+    if (st) return st;
+    if (N > 0x3fffffff) return SHERRY_ERR_SHAPE;
+    if ((st = check_gran(K, granularity, group))) return st;
+    if ((st = check_planes(idx, sgn, scales, N))) return st;
+    if (M > 0 && N > 0 && !dY) return SHERRY_ERR_NULL;
+    if (!aligned(dY, 16) || !aligned(dX, 16)) return SHERRY_ERR_ALIGN;
+    return SHERRY_OK;
+}
+
+size_t sherry_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (check_shape(N, K) || M <= 0 || M > 0x3fffffff || N == 0) return 0;
+    return backward_ws(M, N, K, 0, 0).total;
+}
+
+int sherry_linear_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, const uint32_t* idx,
+                           const uint8_t* sgn, const float* scales, int granularity, int group, uint16_t* dX,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_backward(dY, M, N, K, idx, sgn, scales, granularity, group, dX);
+    if (st) return st;
+    if (M > 0 && !dX) return SHERRY_ERR_NULL;
+    if (M == 0) return SHERRY_OK;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (N == 0) {
+        SHERRY_CUDA_CHECK(cudaMemsetAsync(dX, 0, (size_t)(M * K) * 2, cs));
+        return SHERRY_OK;
+    }
+    const BwdWs w = backward_ws(M, N, K, 0, 0);
+    if ((st = check_ws(workspace, workspace_bytes, w.total))) return st;
+    char* ws = static_cast<char*>(workspace);
+    const int64_t ld = padded_rows(N);
+    const uint16_t* G = dY;
+    if (ld != N) {
+        G = reinterpret_cast<uint16_t*>(ws + w.pad);
+        if ((st = lora_pad_launch(dY, M, N, reinterpret_cast<uint16_t*>(ws + w.pad), ld, cs))) return st;
+    }
+    return dgrad_launch(ProbShape{N, K, granularity, group}, idx, sgn, scales, G, ld, M, dX, nullptr, nullptr, nullptr,
+                        nullptr, 0, ws + w.part, device_sms(), cs);
+}
+
+size_t sherry_linear_lora_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int n_adapters, int rank) {
+    if (check_shape(N, K) || check_lora(M, n_adapters, rank) || M == 0 || N == 0) return 0;
+    return backward_ws(M, N, K, n_adapters, rank).total;
+}
+
+int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t N, int64_t K,
+                                const uint32_t* idx, const uint8_t* sgn, const float* scales, int granularity,
+                                int group, const uint16_t* A, const uint16_t* B, const int32_t* ids,
+                                const float* scaling, int n_adapters, int rank, const float* U, uint16_t* dX, void* dA,
+                                void* dB, int grad_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_lora(M, n_adapters, rank);
+    if (st) return st;
+    if ((st = check_backward(dY, M, N, K, idx, sgn, scales, granularity, group, dX))) return st;
+    if (grad_dtype != SHERRY_F32 && grad_dtype != SHERRY_BF16) return SHERRY_ERR_DTYPE;
+    if (M > 0 && N > 0 && (!A || !B || !ids || (dA && !X) || (dB && !U))) return SHERRY_ERR_NULL;
+    if (!aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(ids, 4) || !aligned(scaling, 4) ||
+        !aligned(U, 16) || !aligned(dA, 16) || !aligned(dB, 16))
+        return SHERRY_ERR_ALIGN;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const size_t size = grad_dtype == SHERRY_BF16 ? 2 : 4;
+    if (M == 0 || N == 0) {  // no tokens, or no outputs: every gradient is zero
+        if (dX && M > 0) SHERRY_CUDA_CHECK(cudaMemsetAsync(dX, 0, (size_t)(M * K) * 2, cs));
+        if (dA) SHERRY_CUDA_CHECK(cudaMemsetAsync(dA, 0, (size_t)n_adapters * rank * K * size, cs));
+        if (dB && N > 0) SHERRY_CUDA_CHECK(cudaMemsetAsync(dB, 0, (size_t)n_adapters * rank * N * size, cs));
+        return SHERRY_OK;
+    }
+    if (!dX && !dA && !dB) return SHERRY_OK;
+    const BwdWs w = backward_ws(M, N, K, n_adapters, rank);
+    if ((st = check_ws(workspace, workspace_bytes, w.total))) return st;
+    char* ws = static_cast<char*>(workspace);
+    const int sms = device_sms();
+    const int64_t ld = padded_rows(N);
+    const uint16_t* G = dY;
+    if (ld != N) {
+        G = reinterpret_cast<uint16_t*>(ws + w.pad);
+        if ((st = lora_pad_launch(dY, M, N, reinterpret_cast<uint16_t*>(ws + w.pad), ld, cs))) return st;
+    }
+    const LoraPlan plan = lora_plan_in(ws + w.plan, M, n_adapters);
+    if ((st = lora_plan_launch(ids, M, n_adapters, plan, cs))) return st;
+    float* p = reinterpret_cast<float*>(ws + w.p);
+    if (dX || dA) {
+        uint16_t* bt = reinterpret_cast<uint16_t*>(ws + w.bt);
+        if ((st = lora_transpose_launch(B, n_adapters, N, rank, bt, ld, cs))) return st;
+        if ((st = lora_down_launch(G, ld, M, ld, bt, ld, rank, ids, scaling, n_adapters, plan, p, sms, cs))) return st;
+    }
+    if (dX && (st = dgrad_launch(ProbShape{N, K, granularity, group}, idx, sgn, scales, G, ld, M, dX, &plan, A, p, ids,
+                                 rank, ws + w.part, sms, cs)))
+        return st;
+    LoraGradJob jobs[2];
+    int count = 0;
+    if (dB) jobs[count++] = LoraGradJob{U, G, ld, N, dB, 1};
+    if (dA) jobs[count++] = LoraGradJob{p, X, K, K, dA, 0};
+    if (count == 0) return SHERRY_OK;
+    return lora_grad_launch(jobs, count, rank, n_adapters, M, plan, grad_dtype == SHERRY_BF16, sms, cs);
+}
+
+static int check_logits(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld) {
+    if (dtype != SHERRY_F32 && dtype != SHERRY_BF16) return SHERRY_ERR_DTYPE;
+    if (M < 0 || M > 0x7fffffff || V < 1 || V > SHERRY_MAX_VOCAB || ld < V) return SHERRY_ERR_SHAPE;
+    if (M > 0 && !logits) return SHERRY_ERR_NULL;
+    if (!aligned(logits, dtype == SHERRY_BF16 ? 2 : 4)) return SHERRY_ERR_ALIGN;
+    return SHERRY_OK;
+}
+
+static int check_scores(int64_t M, int64_t V, const int32_t* targets, int top, const float* logp, const float* entropy,
+                        const float* stats, const float* top_logp, const int32_t* top_ids) {
+    if (top < 0 || top > SHERRY_MAX_TOP || top > V) return SHERRY_ERR_SHAPE;
+    if (M > 0 && (!stats || (logp && !targets) || (top > 0 && (!top_logp || !top_ids)))) return SHERRY_ERR_NULL;
+    if (!aligned(targets, 4) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(stats, 4) ||
+        !aligned(top_logp, 4) || !aligned(top_ids, 4))
+        return SHERRY_ERR_ALIGN;
+    return SHERRY_OK;
+}
+
+int sherry_token_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
+                          int top, float* logp, float* entropy, float* stats, float* top_logp, int32_t* top_ids,
+                          void* stream) {
+    int st = check_logits(logits, dtype, M, V, ld);
+    if (st) return st;
+    if ((st = check_scores(M, V, targets, top, logp, entropy, stats, top_logp, top_ids))) return st;
+    if (M == 0) return SHERRY_OK;
+    return token_logprobs_launch(logits, dtype, M, V, ld, targets, top, logp, entropy, stats, top_logp, top_ids,
+                                 device_sms(), static_cast<cudaStream_t>(stream));
+}
+
+int sherry_token_logprobs_backward(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld,
+                                   const int32_t* targets, const float* stats, const float* entropy,
+                                   const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                                   void* stream) {
+    int st = check_logits(logits, dtype, M, V, ld);
+    if (st) return st;
+    if (ldd < V || (dlogits == logits && ldd != ld)) return SHERRY_ERR_SHAPE;
+    if (M > 0 && (!stats || !dlogits || (dlogp && !targets) || (dentropy && !entropy))) return SHERRY_ERR_NULL;
+    if (!aligned(dlogits, dtype == SHERRY_BF16 ? 2 : 4) || !aligned(targets, 4) || !aligned(stats, 4) ||
+        !aligned(entropy, 4) || !aligned(dlogp, 4) || !aligned(dentropy, 4))
+        return SHERRY_ERR_ALIGN;
+    if (M == 0) return SHERRY_OK;
+    return token_logprobs_bwd_launch(logits, dtype, M, V, ld, dlogp ? targets : nullptr, stats, entropy, dlogp,
+                                     dentropy, dlogits, ldd, static_cast<cudaStream_t>(stream));
+}
+
+// Tokens per chunk of a scored head: the chunk's fp32 logits within 128 MB, about what L2 holds,
+// in whole 128-token tiles.
+static int64_t head_chunk(int64_t M, int64_t N) {
+    const int64_t rows = std::max<int64_t>(128, ((int64_t)32 << 20) / N / 128 * 128);
+    return std::min(M, rows);
+}
+
+// The largest of the chunks' linear workspaces (the last chunk may take another kernel).
+static size_t head_linear_ws(const ProbShape& s, int64_t M) {
+    const int64_t c = head_chunk(M, s.N);
+    size_t lw = linear_ws_bytes(&s, 1, c, device_sms());
+    if (M % c) lw = std::max(lw, linear_ws_bytes(&s, 1, M % c, device_sms()));
+    return std::max(up256(lw), kTicketBytes);
+}
+
+size_t sherry_linear_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t K, int granularity, int group) {
+    if (check_shape(N, K) || check_gran(K, granularity, group) || M <= 0 || M > 0x7fffffff || N < 1 ||
+        N > SHERRY_MAX_VOCAB)
+        return 0;
+    return head_linear_ws(ProbShape{N, K, granularity, group}, M) + (size_t)(head_chunk(M, N) * N) * sizeof(float);
+}
+
+int sherry_linear_logprobs(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* idx, const uint8_t* sgn,
+                           const float* scales, int granularity, int group, const int32_t* targets, int top,
+                           float* logp, float* entropy, float* stats, float* top_logp, int32_t* top_ids,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    if (M < 0 || M > 0x7fffffff) return SHERRY_ERR_SHAPE;
+    sherry_linear_desc d{X, idx, sgn, scales, workspace, N, K, granularity, group};
+    int st = check_shape(N, K);
+    if (st) return st;
+    if (N < 1 || N > SHERRY_MAX_VOCAB) return SHERRY_ERR_SHAPE;
+    if ((st = check_gran(K, granularity, group))) return st;
+    if ((st = check_planes(idx, sgn, scales, N))) return st;
+    if (M > 0 && !X) return SHERRY_ERR_NULL;
+    if (!aligned(X, 16)) return SHERRY_ERR_ALIGN;
+    if ((st = check_scores(M, N, targets, top, logp, entropy, stats, top_logp, top_ids))) return st;
+    if (M == 0) return SHERRY_OK;
+    const ProbShape s{N, K, granularity, group};
+    const int64_t c = head_chunk(M, N);
+    const size_t lw = head_linear_ws(s, M);
+    if ((st = check_ws(workspace, workspace_bytes, lw + (size_t)(c * N) * sizeof(float)))) return st;
+    float* z = reinterpret_cast<float*>(static_cast<char*>(workspace) + lw);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int sms = device_sms();
+    for (int64_t m = 0; m < M; m += c) {
+        const int64_t rows = std::min(c, M - m);
+        d.X = X + m * K;
+        d.Y = z;
+        if ((st = linear_launch(&s, &d, 1, rows, 0, workspace, sms, cs))) return st;
+        if ((st = token_logprobs_launch(z, SHERRY_F32, rows, N, N, targets ? targets + m : nullptr, top,
+                                        logp ? logp + m : nullptr, entropy ? entropy + m : nullptr, stats + 2 * m,
+                                        top > 0 ? top_logp + m * top : nullptr, top > 0 ? top_ids + m * top : nullptr,
+                                        sms, cs)))
             return st;
     }
     return SHERRY_OK;

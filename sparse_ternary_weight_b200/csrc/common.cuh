@@ -206,6 +206,14 @@ int stream_linear_launch(const ProbShape* shapes, const sherry_linear_desc* desc
 // mode 0 Y = Yin + bias[n], mode 1 Y = Yin + sign(X) D^T
 int tequila_term_launch(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* idx, const uint16_t* D,
                         const float* bias, int mode, const float* Yin, void* Y, int y_bf16, cudaStream_t stream);
+int dgrad_status_take();                    // input-gradient kernel (dgrad.cu), as stream_status_take
+// log probabilities of tokens and their gradient (logprobs.cu)
+int token_logprobs_launch(const void* z, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets, int top,
+                          float* logp, float* entropy, float* stats, float* top_logp, int32_t* top_ids, int sms,
+                          cudaStream_t stream);
+int token_logprobs_bwd_launch(const void* z, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
+                              const float* stats, const float* entropy, const float* dlogp, const float* dentropy,
+                              void* out, int64_t ldo, cudaStream_t stream);
 // chained phases on the streaming kernel (cooperative launch, one CTA per SM)
 bool chain_eligible(const ProbShape& s, int64_t M);
 bool chain_launch_ok(const ProbShape* shapes, int count, int n_phases, int64_t M);

@@ -1,0 +1,560 @@
+// dgrad.cu -- input gradient of the packed linear, with the adapters' share:
+//
+//   dX[m][k] = sum_n dY[m][n] t[n][k] alpha(n,k)  +  sum_r P[m][r] A_a[r][k]
+//
+// (the layer is Y = X (T alpha)^T, "Sherry, Tequila and Fairies in Python" section
+// 1.1: F.linear; a = ids[m] is the token's adapter and P = s_a dY B_a, lora.cu).
+//
+// The sum runs over weight rows n, whose scale changes with every n: unlike in the
+// forward pass alpha cannot be taken out of a group's sum, so it enters the bf16
+// operand, t * bf16(alpha * c).  The factor c = 1.875 / alpha(0,0) is undone in
+// fp32 at the end: the scales of a weight are close to each other, and c puts them
+// at the top of a binade, where bf16's half step is 2^-9 of the value instead of up
+// to 2^-8 (a per-tensor scale becomes 1.875 exactly).  Rounding alpha, not splitting
+// it in two bf16 terms, halves the tensor work; its error averages out over the n of
+// a sum and stays below that of the bf16 dX.
+//
+// CTA tile: 128 TM tokens x 256 k (TM = 1 or 2 MMAs of 128 x 256 that share the
+// decoded operand); n runs in stages of 64 rows.  dY is operand A, K-major, by TMA.
+// The weights are operand B in the layout they unpack to, k contiguous (MN-major,
+// 128-byte swizzle): a decode thread owns 64 consecutive k of a row, looks each
+// block of 4 up in the 32 patterns, scales it with one packed multiply per pair and
+// stores 16 bytes at a time, conflict-free (eight lanes take the eight rows of a
+// swizzle atom).  After the last rows the same warps append the adapters' stages:
+// operand B is A_a as it is stored, operand A is P of the tile's tokens, zero for
+// tokens of other adapters, split into 2 bf16 terms (16 significant bits).
+//   warps 0..7   epilogue: TMEM -> registers -> dX (bf16) or, where n is split over
+//                CTAs, fp32 partial sums that k_dgrad_join adds in order
+//   warps 8..15  decode
+//   warp 16      TMA, warp 17 MMA issue
+// n is split where there are fewer tiles than SMs.
+#include "common.cuh"
+#include "lora.cuh"
+#include "lut.cuh"
+#include "tc.cuh"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+namespace sherry {
+
+constexpr int kGThreads = 32 * 18;
+constexpr int kGTmaWarp = 16, kGMmaWarp = 17;
+constexpr int kGK = 256;                     // k columns per tile
+constexpr int kGN = 64;                      // weight rows per stage
+constexpr int kGBBytes = kGN * kGK * 2;      // 32 KB of decoded weights per stage
+constexpr int kGABytes = 128 * kGN * 2;      // 16 KB of dY per 128 tokens and stage
+constexpr int kGStageSum = 192 * 1024;       // 3 stages of 64 KB (TM = 2) or 4 of 48 KB (TM = 1)
+constexpr int kGSmem = kGStageSum + 256 + 1024;
+constexpr int kGMaxStages = 4;
+constexpr float kGTop = 1.875f;              // what alpha(0,0) becomes: exact in bf16
+
+// bf16 x bf16 -> fp32, M = 128, N = 256, A K-major, B MN-major (bit 16)
+constexpr uint32_t kGIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(kGK >> 3) << 17) |
+                             ((uint32_t)(128 >> 4) << 24);
+
+struct GParams {
+    const uint32_t* idx;
+    const uint8_t* sgn;
+    const float* scales;
+    void* out;             // dX bf16 [M][K], or fp32 partial sums [splits][M][K]
+    int M, N, K, words;
+    int gran, group, spr;
+    int mtiles, ktiles, splits, nstages;
+    // adapters (LORA)
+    const uint16_t* A;     // bf16 [n_adapters][R][K]
+    const float* Pm;       // fp32 [M][R]
+    const int32_t* ids;
+    const int32_t* tile_n; // adapters present in each 128-token tile
+    const int32_t* tile_a; // [tiles][kLoraTile]
+    int R;
+};
+
+// MN-major, 128-byte swizzle: atoms of 64 elements x 8 rows (1024 B); the next 64
+// elements are kGN * 128 bytes on (leading offset), the next 8 rows 1024 (stride)
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3fff);
+    d |= (uint64_t)((kGN * 128) >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// the unit that alpha is held in: alpha(0,0) / 1.875, or 1 where that is no ordinary number
+__device__ __forceinline__ float dgrad_unit(const float* scales) {
+    const float a = __ldg(scales);
+    return (a > 1e-30f && a < 1e30f) ? a / kGTop : 1.0f;
+}
+
+template <int TM, bool LORA>
+__global__ void __launch_bounds__(kGThreads, 1)
+k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParams P) {
+    constexpr int ST = TM == 2 ? 3 : 4;                // stages
+    constexpr int SB = TM * kGABytes + kGBBytes;       // bytes per stage
+    constexpr int AC = 2 / TM;                         // accumulators of TM x 256 columns in TMEM
+    static_assert(ST * SB <= kGStageSum && ST <= kGMaxStages, "stage plan");
+    extern __shared__ __align__(1024) unsigned char gsmem[];
+    __shared__ uint64_t bars[3 * kGMaxStages + 5];
+    __shared__ uint32_t tmem_base_s;
+    __shared__ volatile int abort_s;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_u32(gsmem) + 1023u) & ~1023u;
+    const uint32_t table = base + kGStageSum;  // 256-aligned
+    const uint32_t bar0 = smem_u32(&bars[0]);
+    auto full_a = [&](int s) { return bar0 + 8u * s; };
+    auto full_b = [&](int s) { return bar0 + 8u * (ST + s); };
+    auto empty = [&](int s) { return bar0 + 8u * (2 * ST + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (3 * ST + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (3 * ST + 2 + b); };
+    const uint32_t drain = bar0 + 8u * (3 * ST + 4);
+
+    const int items = P.mtiles * P.ktiles * P.splits;
+    // item -> token tile, k tile, stages [st0, st1) of the rows and, in the last split, the adapters' stages
+    struct Item {
+        int mt, kt, sp, st0, st1, nl;
+    };
+    const int rb = LORA ? (P.R + 15) / 16 : 0;
+    auto item = [&](int w) {
+        Item it;
+        it.kt = w % P.ktiles;
+        const int q = w / P.ktiles;
+        it.mt = q % P.mtiles;
+        it.sp = q / P.mtiles;
+        it.st0 = (int)((int64_t)P.nstages * it.sp / P.splits);
+        it.st1 = (int)((int64_t)P.nstages * (it.sp + 1) / P.splits);
+        it.nl = 0;
+        if constexpr (LORA) {
+            if (it.sp == P.splits - 1) {
+                int slots = 0;
+#pragma unroll
+                for (int h = 0; h < TM; ++h) {
+                    const int t = it.mt * TM + h;
+                    if (t * kLoraTile < P.M) slots += __ldg(P.tile_n + t);
+                }
+                it.nl = (slots * rb * 2 + 3) / 4;
+            }
+        }
+        return it;
+    };
+
+    if (threadIdx.x == 0) {
+        abort_s = 0;
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(full_a(s), 1);
+            mbar_init(full_b(s), 256);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_empty(b), 256);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x < 32) {
+        // the 32 patterns: low halves (weights 0, 1), then high halves, conflict-free
+        const uint2 e = decode_block_bf16((uint32_t)threadIdx.x & 15u, (uint32_t)threadIdx.x >> 4);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(table + 4u * threadIdx.x), "r"(e.x) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(table + 128u + 4u * threadIdx.x), "r"(e.y) : "memory");
+    }
+    if (warp == kGMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_s)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+
+    if (warp < 8) {
+        // ---------------- epilogue: lane = token; the two groups of four warps take the two
+        // token halves (TM = 2) or the two halves of the columns (TM = 1) ----------------
+        const int q = warp & 3, half = warp >> 2;
+        constexpr int COLS = TM == 2 ? kGK : kGK / 2;
+        const float unit = P.splits == 1 ? dgrad_unit(P.scales) : 1.0f;
+        int b = 0;
+        uint32_t bph = 0;
+        for (int w = blockIdx.x; w < items; w += gridDim.x) {
+            const Item it = item(w);
+            if (!mbar_wait(acc_full(b), bph, &abort_s)) break;
+            tc_fence_after();
+            const int64_t m = (int64_t)it.mt * (TM * 128) + (TM == 2 ? half * 128 : 0) + q * 32 + lane;
+            const int kc = it.kt * kGK + (TM == 2 ? 0 : half * COLS);
+            const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kGK + half * COLS);
+#pragma unroll 1
+            for (int c = 0; c < COLS / 32; ++c) {
+                uint32_t v[32];
+                SHERRY_TMEM_LD32(t_row + 32 * c, v);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                const int k = kc + 32 * c;
+                if (m < P.M && k < P.K) {
+                    if (P.splits == 1) {
+                        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(P.out) + m * P.K + k);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const __nv_bfloat162 p =
+                                    __floats2bfloat162_rn(__uint_as_float(v[8 * j + 2 * i]) * unit,
+                                                          __uint_as_float(v[8 * j + 2 * i + 1]) * unit);
+                                h[i] = *reinterpret_cast<const uint32_t*>(&p);
+                            }
+                            dst[j] = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<float*>(P.out) +
+                                                              ((int64_t)it.sp * P.M + m) * P.K + k);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(acc_empty(b));
+            if (++b == AC) { b = 0; bph ^= 1u; }
+        }
+    } else if (warp < kGTmaWarp) {
+        // ---------------- decode: 64 rows x four blocks of 64 k; eight lanes = the eight rows
+        // of one swizzle atom, so their 16-byte stores cover all banks ----------------
+        const int dt = threadIdx.x - 256;
+        const int r = (dt >> 5) * 8 + (lane & 7), blk = lane >> 3;
+        const uint32_t brow = (uint32_t)(TM * kGABytes + blk * (kGN * 128) + (r >> 3) * 1024 + (r & 7) * 128);
+        const float inv = 1.0f / dgrad_unit(P.scales);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+            const Item it = item(w);
+            const int kw = it.kt * (kGK / 32) + 2 * blk;  // first of this thread's two words
+            int sc0 = 0, sc1 = 0;                          // their scales' places within a row
+            if (P.gran == SHERRY_PER_GROUP) {
+                sc0 = 32 * kw / P.group;
+                sc1 = 32 * (kw + 1) / P.group;
+            }
+            auto fetch = [&](int st, uint32_t* wd, uint32_t* sg, float* al) {
+                const int64_t n = (int64_t)st * kGN + r;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    wd[h] = 0u;
+                    sg[h] = 0u;
+                    al[h] = 0.0f;
+                    if (st < it.st1 && n < P.N && kw + h < P.words) {
+                        wd[h] = __ldg(P.idx + n * P.words + kw + h);
+                        sg[h] = __ldg(P.sgn + n * P.words + kw + h);
+                        al[h] = __ldg(P.scales + (P.gran == SHERRY_PER_TENSOR ? 0 : n * P.spr + (h ? sc1 : sc0)));
+                    }
+                }
+            };
+            uint32_t wd[2], sg[2];
+            float al[2];
+            fetch(it.st0, wd, sg, al);
+            for (int st = it.st0; st < it.st1; ++st) {
+                uint32_t nwd[2], nsg[2];
+                float nal[2];
+                fetch(st + 1, nwd, nsg, nal);
+                if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
+                const uint32_t dst = base + (uint32_t)(s * SB) + brow;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t ev, od;
+                    spread_word(wd[h], sg[h], ev, od);
+                    const __nv_bfloat162 a2 = __float2bfloat162_rn(al[h] * inv);
+                    const uint32_t a = *reinterpret_cast<const uint32_t*>(&a2);
+                    uint32_t v[16];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t at = __byte_perm((j & 1) ? od : ev, table, (uint32_t)(j >> 1) | 0x7650u);
+                        uint32_t lo, hi;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo) : "r"(at));
+                        asm volatile("ld.shared.u32 %0, [%1+128];" : "=r"(hi) : "r"(at));
+                        v[2 * j] = mul_bf16x2(lo, a);
+                        v[2 * j + 1] = mul_bf16x2(hi, a);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        sts128(dst + (uint32_t)(((4 * h + c) ^ (r & 7)) * 16),
+                               make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
+                }
+                fence_proxy_async();
+                mbar_arrive(full_b(s));
+                if (++s == ST) { s = 0; ph ^= 1u; }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    wd[h] = nwd[h];
+                    sg[h] = nsg[h];
+                    al[h] = nal[h];
+                }
+            }
+            if constexpr (LORA) {
+                // adapters: four entries of 16 ranks per stage; entry = (slot, block of 16 ranks, split term)
+                int slots0 = 0, slots = 0;
+                if (it.nl > 0) {
+                    slots0 = __ldg(P.tile_n + it.mt * TM);
+                    slots = slots0;
+                    if (TM == 2 && (it.mt * TM + 1) * kLoraTile < P.M) slots += __ldg(P.tile_n + it.mt * TM + 1);
+                }
+                const int entries = slots * rb * 2;
+                auto adapter = [&](int slot) {
+                    const int t = it.mt * TM + (slot >= slots0 ? 1 : 0);
+                    return __ldg(P.tile_a + (int64_t)t * kLoraTile + (slot >= slots0 ? slot - slots0 : slot));
+                };
+                for (int ls = 0; ls < it.nl && ok; ++ls) {
+                    if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
+                    const uint32_t stage = base + (uint32_t)(s * SB);
+                    {  // operand B: row r of the stage = a rank's row of A_a, 64 of its k
+                        const int e = ls * 4 + (r >> 4), q = e >> 1;
+                        const int rr = (q % (rb > 0 ? rb : 1)) * 16 + (r & 15);
+                        const bool in = e < entries && rr < P.R;
+                        const uint16_t* src = P.A;
+                        const int k = it.kt * kGK + blk * 64;
+                        if (in) src += ((int64_t)adapter(q / rb) * P.R + rr) * P.K + k;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (in && k + 8 * c < P.K) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                            sts128(stage + brow + (uint32_t)((c ^ (r & 7)) * 16), v);
+                        }
+                    }
+                    // operand A: a token's P for each entry, zero where the token has another adapter
+                    constexpr int EPT = TM == 2 ? 4 : 2;  // entries per thread
+                    const int row = TM == 2 ? dt : (dt & 127);
+                    const int ebase = TM == 2 ? 0 : 2 * (dt >> 7);
+                    const int64_t m = (int64_t)it.mt * (TM * 128) + row;
+                    const int my = m < P.M ? __ldg(P.ids + m) : -1;
+#pragma unroll 1
+                    for (int i = 0; i < EPT; ++i) {
+                        const int el = ebase + i, e = ls * 4 + el, q = e >> 1;
+                        uint32_t h[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) h[j] = 0u;
+                        if (e < entries && my >= 0) {
+                            const int slot = q / rb, r0 = (q % rb) * 16;
+                            if (adapter(slot) == my && (slot >= slots0) == (row >= 128)) {
+                                const float* src = P.Pm + m * P.R + r0;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    if (r0 + 4 * j < P.R) {
+                                        const float4 f = __ldg(reinterpret_cast<const float4*>(src) + j);
+                                        h[2 * j] = split_pair(f.x * inv, f.y * inv, e & 1);
+                                        h[2 * j + 1] = split_pair(f.z * inv, f.w * inv, e & 1);
+                                    }
+                                }
+                            }
+                        }
+                        const uint32_t arow =
+                            stage + (uint32_t)((row >> 7) * kGABytes + ((row & 127) >> 3) * 1024 + (row & 7) * 128);
+                        sts128(arow + (uint32_t)(((2 * el) ^ (row & 7)) * 16), make_uint4(h[0], h[1], h[2], h[3]));
+                        sts128(arow + (uint32_t)(((2 * el + 1) ^ (row & 7)) * 16), make_uint4(h[4], h[5], h[6], h[7]));
+                    }
+                    fence_proxy_async();
+                    mbar_arrive(full_b(s));
+                    if (++s == ST) { s = 0; ph ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == kGTmaWarp) {
+        // ---------------- TMA: dY tiles; in an adapters' stage the decode warps write both operands ----------------
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            int issued[ST] = {};  // phases of full_a started per stage
+            bool ok = true;
+            for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+                const Item it = item(w);
+                for (int st = it.st0; st < it.st1 + it.nl; ++st) {
+                    if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
+                    if (st < it.st1) {
+                        mbar_expect_tx(full_a(s), TM * kGABytes);
+#pragma unroll
+                        for (int h = 0; h < TM; ++h)
+                            tma_load_2d(base + (uint32_t)(s * SB + h * kGABytes), &ymap, st * kGN,
+                                        (it.mt * TM + h) * 128, full_a(s));
+                    } else {
+                        mbar_arrive(full_a(s));
+                    }
+                    ++issued[s];
+                    if (++s == ST) { s = 0; ph ^= 1u; }
+                }
+            }
+            // every load lands before the CTA's shared memory goes away
+            for (int i = 0; i < ST; ++i)
+                if (issued[i] > 0) mbar_drain(full_a(i), (uint32_t)((issued[i] - 1) & 1));
+        }
+    } else {
+        // ---------------- MMA issue ----------------
+        if (lane == 0) {
+            int s = 0, b = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true;
+            for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+                const Item it = item(w);
+                if (!mbar_wait(acc_empty(b), bph ^ 1u, &abort_s)) break;
+                tc_fence_after();
+                for (int st = it.st0; st < it.st1 + it.nl; ++st) {
+                    if (!mbar_wait(full_a(s), ph, &abort_s) || !mbar_wait(full_b(s), ph, &abort_s)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = smem_desc(base + (uint32_t)(s * SB));
+                    const uint64_t db = smem_desc_mn(base + (uint32_t)(s * SB + TM * kGABytes));
+#pragma unroll
+                    for (int kk = 0; kk < kGN / 16; ++kk)  // 16 rows: +32 bytes in A's row, two 8-row atoms of B
+#pragma unroll
+                        for (int h = 0; h < TM; ++h)
+                            mma_bf16_ss(tmem + (uint32_t)((TM == 2 ? h : b) * kGK),
+                                        da + (uint64_t)((h * kGABytes) >> 4) + (uint64_t)(2 * kk),
+                                        db + (uint64_t)(2 * kk * (1024 >> 4)), kGIdesc,
+                                        (st == it.st0 && kk == 0) ? 0u : 1u);
+                    mma_commit(empty(s));
+                    if (++s == ST) { s = 0; ph ^= 1u; }
+                }
+                if (!ok) break;
+                mma_commit(acc_full(b));
+                if (++b == AC) { b = 0; bph ^= 1u; }
+            }
+            mma_commit(drain);
+            mbar_drain(drain, 0u);
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kGMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// dX = (the splits' partial sums, in order) * unit, bf16
+__global__ void __launch_bounds__(256) k_dgrad_join(const float* part, int splits, int64_t total, const float* scales,
+                                                    uint16_t* out) {
+    const float unit = dgrad_unit(scales);
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= total) return;  // total = M * K, a multiple of 32
+    float4 a = *reinterpret_cast<const float4*>(part + i);
+    for (int s = 1; s < splits; ++s) {
+        const float4 b = *reinterpret_cast<const float4*>(part + (int64_t)s * total + i);
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * unit, a.y * unit), hi = __floats2bfloat162_rn(a.z * unit, a.w * unit);
+    *reinterpret_cast<uint2*>(out + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// ---- host -------------------------------------------------------------------------
+
+struct GPlan {
+    int tm, mtiles, ktiles, splits, nstages;
+};
+
+// Two 128-token MMAs per CTA once that still gives every SM a tile (the decoded operand is then used
+// twice); rows split over CTAs where there are fewer tiles than SMs, at least 4 stages each.
+static GPlan dgrad_plan(int64_t M, int64_t N, int64_t K, int sms) {
+    GPlan g;
+    g.ktiles = (int)((K + kGK - 1) / kGK);
+    g.nstages = (int)((N + kGN - 1) / kGN);
+    g.tm = ((M + 255) / 256) * g.ktiles * 10 >= (int64_t)sms * 7 ? 2 : 1;
+    g.mtiles = (int)((M + 128 * g.tm - 1) / (128 * g.tm));
+    const int64_t tiles = (int64_t)g.mtiles * g.ktiles;
+    g.splits = 1;
+    if (g.tm == 1 && tiles * 2 <= sms)
+        g.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / tiles, g.nstages / 4));
+    return g;
+}
+
+size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int sms) {
+    const GPlan g = dgrad_plan(M, N, K, sms);
+    return g.splits > 1 ? (size_t)g.splits * (size_t)(M * K) * sizeof(float) : 0;
+}
+
+int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, const float* scales, const uint16_t* dY,
+                 int64_t ldy, int64_t M, uint16_t* dX, const LoraPlan* lora, const uint16_t* A, const float* Pm,
+                 const int32_t* ids, int R, void* workspace, int sms, cudaStream_t stream) {
+    const GPlan g = dgrad_plan(M, s.N, s.K, sms);
+    CUtensorMap map;
+    int st = encode_2d(&map, dY, ldy, M, 128);
+    if (st) return st;
+    GParams P{};
+    P.idx = idx;
+    P.sgn = sgn;
+    P.scales = scales;
+    P.out = g.splits > 1 ? workspace : dX;
+    P.M = (int)M;
+    P.N = (int)s.N;
+    P.K = (int)s.K;
+    P.words = (int)(s.K / 32);
+    P.gran = s.granularity;
+    P.group = s.granularity == SHERRY_PER_GROUP ? s.group : 32;
+    P.spr = s.granularity == SHERRY_PER_GROUP ? (int)(s.K / s.group) : 1;
+    P.mtiles = g.mtiles;
+    P.ktiles = g.ktiles;
+    P.splits = g.splits;
+    P.nstages = g.nstages;
+    if (lora) {
+        P.A = A;
+        P.Pm = Pm;
+        P.ids = ids;
+        P.tile_n = lora->tile_n;
+        P.tile_a = lora->tile_a;
+        P.R = R;
+    }
+    static PerDevice once;
+    int v = 0;
+    st = per_device(once, &v, [](int& x) {
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_dgrad<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_dgrad<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_dgrad<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_dgrad<2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
+        x = 1;
+        return SHERRY_OK;
+    });
+    if (st) return st;
+    const int64_t items = (int64_t)g.mtiles * g.ktiles * g.splits;
+    if (items > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)std::min<int64_t>(items, sms);
+    if (g.tm == 2) {
+        if (lora)
+            k_dgrad<2, true><<<grid, kGThreads, kGSmem, stream>>>(map, P);
+        else
+            k_dgrad<2, false><<<grid, kGThreads, kGSmem, stream>>>(map, P);
+    } else {
+        if (lora)
+            k_dgrad<1, true><<<grid, kGThreads, kGSmem, stream>>>(map, P);
+        else
+            k_dgrad<1, false><<<grid, kGThreads, kGSmem, stream>>>(map, P);
+    }
+    SHERRY_LAUNCH_CHECK();
+    if (g.splits > 1) {
+        const int64_t total = M * s.K;
+        k_dgrad_join<<<(unsigned)((total / 4 + 255) / 256), 256, 0, stream>>>(static_cast<const float*>(workspace),
+                                                                            g.splits, total, scales, dX);
+        SHERRY_LAUNCH_CHECK();
+    }
+    return SHERRY_OK;
+}
+
+int dgrad_status_take() { return tc_status_take(); }
+
+}  // namespace sherry

@@ -1,0 +1,574 @@
+// logprobs.cu -- log probabilities of given tokens, entropy and the likeliest
+// tokens of every row of logits in one pass over them, and their gradient.
+//
+// With z the row, m = max z, S = sum exp(z - m):
+//   log p(t) = (z_t - m) - log S        entropy H = log S - sum (z - m) exp(z - m) / S
+//   d logits = g (onehot(t) - p) - h p (log p + H)   for d log p(t) = g, d H = h
+//
+// Forward (k_logprobs): a cluster of 1 to 8 CTAs per row, each reading a
+// contiguous share of the row's 16-byte vectors once.  A thread keeps a running
+// maximum, S and the weighted sum in fp32 in base 2: with L = log2(e) and
+// r = rn(m L), e = 2^(z L - r) is one fused multiply-add and one exponential;
+// that r is a rounded m L scales every e by the same 2^(m L - r), which the
+// row's end takes back out.  The likeliest tokens come from the same pass: keys
+// (value, ~index) at or above a threshold are appended to a list in shared
+// memory; the threshold starts at the smallest of 32 disjoint groups' maxima (a
+// lower bound of the 32nd largest) and rises to the k-th best key whenever the
+// list is cut back.  A key's place in the answer is the number of larger keys,
+// so ties go to the lowest index and the order of the appends does not matter.
+//
+// Rows whose maximum is beyond +-1e38 (masks of the type's lowest value
+// everywhere) would overflow m L and take a second pass with z - m first.  All
+// -inf: log p = -inf, H = 0.  NaN or +inf in a row: NaN, and no tokens (-1).
+//
+// Backward (k_logprobs_bwd): elementwise, one read and one write; the rows of
+// the output may be aligned differently from those of the input, in which case a
+// thread joins two aligned vectors of the input into one of the output.
+// Both are bound by HBM.
+#include "common.cuh"
+#include "lut.cuh"
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+namespace cg = cooperative_groups;
+
+namespace sherry {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpVecs = 4;       // 16-byte vectors per thread and iteration
+constexpr int kLpCap = 1024;     // candidate keys held
+constexpr int kLpRefine = 96;    // keys beyond the wanted ones that make a cut worth its pass
+constexpr int kLpMaxTop = SHERRY_MAX_TOP;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kEdge = 1e38f;   // row maxima beyond this overflow m * log2(e) or come near it
+static_assert(kLpMaxTop <= 32, "the first threshold is a bound of the 32nd largest");
+
+struct LpParams {
+    const void* z;
+    int64_t ld;
+    const int32_t* targets;
+    float* logp;
+    float* entropy;
+    float* stats;
+    float* top_logp;
+    int32_t* top_ids;
+    int V, top;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <typename T>
+struct LpVec;
+template <>
+struct LpVec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(uint4 v, float* f) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16lo(w[i]);
+            f[2 * i + 1] = bf16hi(w[i]);
+        }
+    }
+    static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ __nv_bfloat16 round(float f) { return __float2bfloat16_rn(f); }
+    static __device__ __forceinline__ uint32_t pad() { return 0xff80ff80u; }  // two -inf
+};
+template <>
+struct LpVec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(uint4 v, float* f) {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ float one(const float* p) { return *p; }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    static __device__ __forceinline__ float round(float f) { return f; }
+    static __device__ __forceinline__ uint32_t pad() { return 0xff800000u; }
+};
+
+// order-preserving bits of a float; -0 and +0 are one value
+__device__ __forceinline__ uint32_t lp_order(float z) {
+    const uint32_t u = __float_as_uint(z + 0.0f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float lp_unorder(uint32_t u) {
+    return __uint_as_float((u & 0x80000000u) ? (u ^ 0x80000000u) : ~u);
+}
+__device__ __forceinline__ uint64_t lp_key(float z, int i) { return ((uint64_t)lp_order(z) << 32) | (uint32_t)~i; }
+
+// One vector of the row whose first element is `e0` (may be negative, or reach past
+// the row: those elements read as -inf).
+template <typename T>
+__device__ __forceinline__ uint4 lp_load(const T* row, int e0, int V) {
+    constexpr int N = LpVec<T>::N;
+    if (e0 >= 0 && e0 + N <= V) return *reinterpret_cast<const uint4*>(row + e0);
+    float f[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = (e0 + j >= 0 && e0 + j < V) ? LpVec<T>::one(row + e0 + j) : -INFINITY;
+    return LpVec<T>::pack(f);
+}
+
+struct LpTop {  // shared state of the likeliest tokens
+    uint64_t buf[kLpCap];
+    uint64_t best[kLpMaxTop];
+    float group[32];
+    uint64_t thr;
+    int cnt;
+};
+
+// The `k` largest of buf[0..n), in order, into best (0 where there are fewer).
+__device__ __forceinline__ void lp_rank(LpTop& s, int n, int k) {
+    if ((int)threadIdx.x < k) s.best[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kLpThreads) {
+        const uint64_t me = s.buf[i];
+        int r = 0;
+        for (int j = 0; j < n; ++j) r += s.buf[j] > me;
+        if (r < k) s.best[r] = me;
+    }
+    __syncthreads();
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLpThreads) k_logprobs(const LpParams P) {
+    constexpr int N = LpVec<T>::N;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int64_t rowi = blockIdx.x / C;
+    const T* row = reinterpret_cast<const T*>(P.z) + rowi * P.ld;
+    const int V = P.V, top = TOP ? P.top : 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    __shared__ typename std::conditional<TOP, LpTop, int>::type top_s;
+    __shared__ float red[3][kLpThreads / 32];
+    __shared__ float part[3];  // this CTA's maximum, S, weighted sum
+
+    // the row's 16-byte vectors: vector v holds elements off + N v ..; this CTA's share is [v0, v1)
+    const int off = -(int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    const int nv = (V - off + N - 1) / N;
+    const int share = (nv + C - 1) / C;
+    const int v0 = min(rank * share, nv), v1 = min(v0 + share, nv);
+    const int iters = (v1 - v0 + kLpThreads * kLpVecs - 1) / (kLpThreads * kLpVecs);
+
+    auto fetch = [&](int it, uint4* x) {
+#pragma unroll
+        for (int u = 0; u < kLpVecs; ++u) {
+            const int v = v0 + (it * kLpVecs + u) * kLpThreads + tid;
+            x[u] = v < v1 ? lp_load(row, off + N * v, V)
+                          : make_uint4(LpVec<T>::pad(), LpVec<T>::pad(), LpVec<T>::pad(), LpVec<T>::pad());
+        }
+    };
+
+    float m = -INFINITY, r = -kEdge * kLog2e, s1 = 0.0f, s2 = 0.0f;
+    if constexpr (TOP) {
+        if (tid == 0) {
+            top_s.cnt = 0;
+            top_s.thr = 0;
+        }
+    }
+    uint4 x[kLpVecs];
+    fetch(0, x);
+    for (int it = 0; it < iters; ++it) {
+        uint4 nx[kLpVecs];
+        if (it + 1 < iters) fetch(it + 1, nx);
+        float vm[kLpVecs];
+        float bm = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kLpVecs; ++u) {
+            float f[N];
+            LpVec<T>::unpack(x[u], f);
+            vm[u] = f[0];
+#pragma unroll
+            for (int j = 1; j < N; ++j) vm[u] = fmaxf(vm[u], f[j]);
+            bm = fmaxf(bm, vm[u]);
+        }
+        if (bm > m) {
+            const float nr = fmaxf(bm, -kEdge) * kLog2e;
+            const float d = fmaxf(r - nr, -1e4f), f = ex2(d);
+            s2 = f * fmaf(d, s1, s2);
+            s1 *= f;
+            m = bm;
+            r = nr;
+        }
+#pragma unroll
+        for (int u = 0; u < kLpVecs; ++u) {
+            float f[N];
+            LpVec<T>::unpack(x[u], f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float y = fmaf(f[j], kLog2e, -r);
+                const float e = ex2(y);
+                s1 += e;
+                s2 = fmaf(e, fmaxf(y, -1e4f), s2);  // e = 0 there: 0 * -inf would be NaN
+            }
+        }
+        if constexpr (TOP) {
+            if (it == 0) {
+                // 32 groups of 8 threads: the smallest of their maxima has 32 elements at or above it
+                float g = bm;
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) g = fmaxf(g, __shfl_xor_sync(kFull, g, o));
+                if ((tid & 7) == 0) top_s.group[tid >> 3] = g;
+                __syncthreads();
+                g = top_s.group[lane];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) g = fminf(g, __shfl_xor_sync(kFull, g, o));
+                if (tid == 0) top_s.thr = (uint64_t)lp_order(g) << 32;
+                __syncthreads();
+            }
+            const int held = top_s.cnt;  // nothing is appended between the last barrier and the next
+            __syncthreads();
+            while (true) {
+                const uint64_t thr = top_s.thr;
+                const float tv = lp_unorder((uint32_t)(thr >> 32));
+#pragma unroll
+                for (int u = 0; u < kLpVecs; ++u) {
+                    if (vm[u] >= tv) {
+                        float f[N];
+                        LpVec<T>::unpack(x[u], f);
+                        const int e0 = off + N * (v0 + (it * kLpVecs + u) * kLpThreads + tid);
+#pragma unroll
+                        for (int j = 0; j < N; ++j) {
+                            if (f[j] >= tv) {
+                                const int e = e0 + j;
+                                const uint64_t key = lp_key(f[j], e);
+                                if (key >= thr && e >= 0 && e < V && v0 + (it * kLpVecs + u) * kLpThreads + tid < v1) {
+                                    const int at = atomicAdd(&top_s.cnt, 1);
+                                    if (at < kLpCap) top_s.buf[at] = key;
+                                }
+                            }
+                        }
+                    }
+                }
+                __syncthreads();
+                const int n = top_s.cnt;
+                if (n <= kLpCap) {
+                    if (n > top + kLpRefine) {  // cut back to the best, raise the threshold
+                        lp_rank(top_s, n, top);
+                        if (tid < top) top_s.buf[tid] = top_s.best[tid];
+                        if (tid == 0) {
+                            top_s.cnt = top;
+                            top_s.thr = max(top_s.thr, top_s.best[top - 1]);
+                        }
+                        __syncthreads();
+                    }
+                    break;
+                }
+                // more keys than the list holds: raise the threshold to the k-th best of those
+                // held (each is in the row, so it is a bound) and append this iteration's again
+                lp_rank(top_s, kLpCap, top);
+                if (tid == 0) {
+                    top_s.thr = max(top_s.thr, top_s.best[top - 1]);
+                    top_s.cnt = held;
+                }
+                __syncthreads();
+            }
+        }
+        if (it + 1 < iters) {
+#pragma unroll
+            for (int u = 0; u < kLpVecs; ++u) x[u] = nx[u];
+        }
+    }
+    if constexpr (TOP) {
+        __syncthreads();
+        lp_rank(top_s, min(top_s.cnt, kLpCap), top);
+    }
+
+    // the row's maximum
+    float bmax = m;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) bmax = fmaxf(bmax, __shfl_xor_sync(kFull, bmax, o));
+    if (lane == 0) red[0][warp] = bmax;
+    __syncthreads();
+    bmax = red[0][lane & (kLpThreads / 32 - 1)];
+#pragma unroll
+    for (int o = kLpThreads / 64; o >= 1; o >>= 1) bmax = fmaxf(bmax, __shfl_xor_sync(kFull, bmax, o));
+    if (C > 1) {
+        if (tid == 0) part[0] = bmax;
+        cluster.sync();
+        for (int c = 0; c < C; ++c) bmax = fmaxf(bmax, *cluster.map_shared_rank(&part[0], c));
+    }
+    float ref = fmaxf(bmax, -kEdge) * kLog2e;
+    const bool edge = bmax > kEdge || (bmax < -kEdge && bmax != -INFINITY);
+    if (edge) {
+        // m log2(e) overflows: this row again, with z - m first
+        s1 = 0.0f;
+        s2 = 0.0f;
+        for (int v = v0 + tid; v < v1; v += kLpThreads) {
+            float f[N];
+            LpVec<T>::unpack(lp_load(row, off + N * v, V), f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float y = (f[j] - bmax) * kLog2e;
+                const float e = ex2(y);
+                s1 += e;
+                s2 = fmaf(e, fmaxf(y, -1e4f), s2);
+            }
+        }
+        ref = 0.0f;
+    } else {
+        const float d = fmaxf(r - ref, -1e4f), f = ex2(d);
+        s2 = f * fmaf(d, s1, s2);
+        s1 *= f;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        s1 += __shfl_xor_sync(kFull, s1, o);
+        s2 += __shfl_xor_sync(kFull, s2, o);
+    }
+    if (lane == 0) {
+        red[1][warp] = s1;
+        red[2][warp] = s2;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        s1 = s2 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kLpThreads / 32; ++w) {
+            s1 += red[1][w];
+            s2 += red[2][w];
+        }
+        part[1] = s1;
+        part[2] = s2;
+    }
+    if (C > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+    if (rank == 0) {
+        s1 = s2 = 0.0f;
+        for (int c = 0; c < C; ++c) {
+            s1 += *cluster.map_shared_rank(&part[1], c);
+            s2 += *cluster.map_shared_rank(&part[2], c);
+        }
+        // log S relative to the true maximum: S was summed relative to ref = rn(m L)
+        const bool dead = bmax == -INFINITY, bad = !(s1 < INFINITY);
+        float lsum = logf(s1) + (edge ? 0.0f : fmaf(-bmax, kLog2e, ref) * kLn2);
+        if (dead) lsum = 0.0f;
+        if (bad) lsum = NAN;
+        if (tid == 0) {
+            if (P.logp) {
+                const int t = P.targets[rowi];
+                float lp = 0.0f;
+                if (t >= 0 && t < V) {
+                    const float zt = LpVec<T>::one(row + t);
+                    lp = bad ? NAN : (dead || zt == -INFINITY) ? -INFINITY : (zt - bmax) - lsum;
+                }
+                P.logp[rowi] = lp;
+            }
+            if (P.entropy)
+                P.entropy[rowi] = bad ? NAN : dead ? 0.0f : fmaxf(logf(s1) - s2 / s1 * kLn2, 0.0f);
+            P.stats[2 * rowi] = bad ? NAN : bmax;
+            P.stats[2 * rowi + 1] = lsum;
+        }
+        if constexpr (TOP) {
+            // every CTA's best are in its shared memory; a key's place is the number of larger ones
+            for (int i = tid; i < C * top; i += kLpThreads) {
+                const uint64_t me = cluster.map_shared_rank(&top_s.best[0], i / top)[i % top];
+                int place = 0;
+                for (int c = 0; c < C; ++c) {
+                    const uint64_t* other = cluster.map_shared_rank(&top_s.best[0], c);
+                    for (int j = 0; j < top; ++j) place += other[j] > me;
+                }
+                if (me != 0 && place < top && !bad) {
+                    const float zt = lp_unorder((uint32_t)(me >> 32));
+                    P.top_ids[rowi * top + place] = (int32_t)~(uint32_t)me;
+                    P.top_logp[rowi * top + place] = (dead || zt == -INFINITY) ? -INFINITY : (zt - bmax) - lsum;
+                }
+            }
+            if (bad) {
+                for (int i = tid; i < top; i += kLpThreads) {
+                    P.top_ids[rowi * top + i] = -1;
+                    P.top_logp[rowi * top + i] = NAN;
+                }
+            }
+        }
+    }
+    if (C > 1) cluster.sync();  // the others' shared memory is read until here
+}
+
+// ---- backward --------------------------------------------------------------------
+
+struct LpBwdParams {
+    const void* z;
+    int64_t ld;
+    const int32_t* targets;
+    const float* stats;
+    const float* entropy;
+    const float* dlogp;
+    const float* dentropy;
+    void* out;
+    int64_t ldo;
+    int V, segs;
+};
+
+constexpr int kLpBwdVecs = 4;
+
+// the 16 bytes that start `shift` bytes into the 32 bytes (a, b); shift is the same for the whole row
+__device__ __forceinline__ uint4 lp_join(uint4 a, uint4 b, int shift) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const int bits = (shift & 3) * 8;
+    uint32_t o[5];
+    switch (shift >> 2) {
+        case 0:
+#pragma unroll
+            for (int i = 0; i < 5; ++i) o[i] = w[i];
+            break;
+        case 1:
+#pragma unroll
+            for (int i = 0; i < 5; ++i) o[i] = w[i + 1];
+            break;
+        case 2:
+#pragma unroll
+            for (int i = 0; i < 5; ++i) o[i] = w[i + 2];
+            break;
+        default:
+#pragma unroll
+            for (int i = 0; i < 5; ++i) o[i] = w[i + 3];
+            break;
+    }
+    return make_uint4(__funnelshift_r(o[0], o[1], bits), __funnelshift_r(o[1], o[2], bits),
+                      __funnelshift_r(o[2], o[3], bits), __funnelshift_r(o[3], o[4], bits));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads) k_logprobs_bwd(const LpBwdParams P) {
+    constexpr int N = LpVec<T>::N;
+    const int64_t rowi = blockIdx.x / P.segs;
+    const int seg = (int)(blockIdx.x % P.segs);
+    const T* row = reinterpret_cast<const T*>(P.z) + rowi * P.ld;
+    T* out = reinterpret_cast<T*>(P.out) + rowi * P.ldo;
+    const int V = P.V;
+    // vectors of the output: vector v holds elements off + N v ..; in the input they
+    // start `shift` bytes past an aligned vector
+    const int off = -(int)((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T));
+    const int shift = (int)(((reinterpret_cast<uintptr_t>(row) & 15u) + 16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u);
+    const int nv = (V - off + N - 1) / N;
+    const int vb = seg * (kLpThreads * kLpBwdVecs) + threadIdx.x;
+
+    uint4 x[kLpBwdVecs];
+#pragma unroll
+    for (int u = 0; u < kLpBwdVecs; ++u) {
+        const int v = vb + u * kLpThreads;
+        const int e0 = off + N * v;
+        const int lead = shift / (int)sizeof(T);
+        if (v < nv) {
+            if (shift == 0) {
+                x[u] = lp_load(row, e0, V);
+            } else if (e0 - lead >= 0 && e0 - lead + 2 * N <= V) {
+                const uint4* p = reinterpret_cast<const uint4*>(row + e0 - lead);
+                x[u] = lp_join(p[0], p[1], shift);
+            } else {
+                float f[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    f[j] = (e0 + j >= 0 && e0 + j < V) ? LpVec<T>::one(row + e0 + j) : -INFINITY;
+                x[u] = LpVec<T>::pack(f);
+            }
+        }
+    }
+    const float m = P.stats[2 * rowi], lsum = P.stats[2 * rowi + 1];
+    const int t0 = P.targets ? P.targets[rowi] : -1;
+    const int t = (t0 >= 0 && t0 < V) ? t0 : -1;
+    const bool dead = m == -INFINITY;
+    const float g = (t < 0 || dead) ? 0.0f : P.dlogp[rowi];
+    const float h = P.dentropy ? P.dentropy[rowi] : 0.0f;
+    const float H = P.dentropy ? P.entropy[rowi] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < kLpBwdVecs; ++u) {
+        const int v = vb + u * kLpThreads;
+        if (v >= nv) break;
+        const int e0 = off + N * v;
+        float f[N];
+        LpVec<T>::unpack(x[u], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float lp = (f[j] - m) - lsum;
+            const float p = dead ? 0.0f : ex2(lp * kLog2e);
+            // p = 0 where z = -inf: its log p would make 0 * -inf
+            f[j] = p == 0.0f ? 0.0f : -p * fmaf(h, lp + H, g);
+            if (e0 + j == t) f[j] += g;
+        }
+        if (e0 >= 0 && e0 + N <= V) {
+            *reinterpret_cast<uint4*>(out + e0) = LpVec<T>::pack(f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (e0 + j >= 0 && e0 + j < V) out[e0 + j] = LpVec<T>::round(f[j]);
+        }
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------
+
+template <typename T>
+static int lp_launch(const LpParams& P, int64_t M, int sms, cudaStream_t stream) {
+    // CTAs per row: enough to give every SM four of them (their resident number), as long as each
+    // still has a full iteration of vectors
+    const int64_t iters = (P.V / LpVec<T>::N + kLpThreads * kLpVecs - 1) / (kLpThreads * kLpVecs);
+    int c = 1;
+    while (c < 8 && M * c < 2 * (int64_t)sms && c < iters) c *= 2;
+    if (M * c > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(M * c));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)c;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (P.top > 0)
+        SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, true>, P));
+    else
+        SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, false>, P));
+    return SHERRY_OK;
+}
+
+int token_logprobs_launch(const void* z, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets, int top,
+                          float* logp, float* entropy, float* stats, float* top_logp, int32_t* top_ids, int sms,
+                          cudaStream_t stream) {
+    const LpParams P{z, ld, targets, logp, entropy, stats, top_logp, top_ids, (int)V, top};
+    return dtype == SHERRY_BF16 ? lp_launch<__nv_bfloat16>(P, M, sms, stream) : lp_launch<float>(P, M, sms, stream);
+}
+
+int token_logprobs_bwd_launch(const void* z, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
+                              const float* stats, const float* entropy, const float* dlogp, const float* dentropy,
+                              void* out, int64_t ldo, cudaStream_t stream) {
+    const int n = dtype == SHERRY_BF16 ? 8 : 4;
+    // a row that starts inside a vector has one more of them
+    const int64_t segs = (V / n + 2 + kLpThreads * kLpBwdVecs - 1) / (kLpThreads * kLpBwdVecs);
+    if (M * segs > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
+    const LpBwdParams P{z, ld, targets, stats, entropy, dlogp, dentropy, out, ldo, (int)V, (int)segs};
+    if (dtype == SHERRY_BF16)
+        k_logprobs_bwd<__nv_bfloat16><<<(unsigned)(M * segs), kLpThreads, 0, stream>>>(P);
+    else
+        k_logprobs_bwd<float><<<(unsigned)(M * segs), kLpThreads, 0, stream>>>(P);
+    SHERRY_LAUNCH_CHECK();
+    return SHERRY_OK;
+}
+
+}  // namespace sherry

@@ -28,12 +28,11 @@
 //   next warp    TMA: the chunk's four X tiles [128 tokens x 64 K], SWIZZLE_128B
 //   last warp    TMEM allocation; one elected thread issues tcgen05.mma
 #include "common.cuh"
+#include "lora.cuh"
 #include "lut.cuh"
+#include "tc.cuh"
 
-#include <cuda.h>
 #include <cuda_bf16.h>
-
-#include <mutex>
 
 namespace sherry {
 
@@ -64,13 +63,14 @@ constexpr int kPAcc = 2;                         // group accumulators in flight
 constexpr int kPTmemCols = 512;                  // 2 x 128 accumulator columns + the A buffers
 constexpr int kPAcol = kPAcc * kPBN;             // first TMEM column of the A stages (256)
 constexpr int kPAcols = kPBK / 2;                // 32 columns (64 bf16) per A stage
-constexpr long long kPWaitCycles = 4000000000LL;  // ~2 s at 2 GHz
 constexpr int kPMaxSlots = kPXSlots > kPArnSlots ? kPXSlots : kPArnSlots;
 constexpr int kPMaxABuf = kPABuf > 2 ? kPABuf : 2;
 static_assert(kPAcol + kPABuf * kPChunkSteps * kPAcols <= kPTmemCols, "TMEM plan");
 static_assert(kPXSlots >= kPABuf + 1, "the decode's A-buffer wait reads the slot barrier of chunk cc - kPABuf");
 
-__device__ int g_device_status = 0;
+// bf16 x bf16 -> fp32, both K-major, M = 128, N = 128
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kPBN >> 3) << 17) |
+                            ((uint32_t)(kPBM >> 4) << 24);
 
 struct PParams {
     const uint32_t* idx;
@@ -82,139 +82,14 @@ struct PParams {
     int row_scale, per_tensor, spr;
     int group_steps;  // K-steps per scale group (per-row: all of K)
     float lambda;     // Arenas: weight of the dense product
+    // adapters (PMode::kLora)
+    const uint16_t* B;      // bf16 [n_adapters][N][R]
+    const float* U;         // fp32 [M][R]
+    const int32_t* ids;
+    const int32_t* tile_n;  // adapters present in each 128-token tile
+    const int32_t* tile_a;  // [tiles][kLoraTile]
+    int R, terms;           // rank; bf16 terms that U is split into
 };
-
-// ---- PTX wrappers -------------------------------------------------------------
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
-                 "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// bounded wait: false if it gave up (or another thread of the CTA did)
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    if (mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (true) {
-        if (mbar_try(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (clock64() - t0 > kPWaitCycles) {
-            *abort_flag = 1;
-            atomicExch(&g_device_status, SHERRY_ERR_TIMEOUT);
-            return false;
-        }
-    }
-}
-// Bounded wait used on the way out of the kernel, after a normal finish or an
-// abort: it ignores the abort flag, so that the CTA's own asynchronous work (its
-// committed MMAs, its TMA loads in flight) lands before TMEM is freed and the
-// CTA's shared memory is released.  On timeout it records the error and returns.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-    const long long t0 = clock64();
-    while (!mbar_try(bar, parity)) {
-        if (clock64() - t0 > kPWaitCycles) {
-            atomicExch(&g_device_status, SHERRY_ERR_TIMEOUT);
-            return;
-        }
-    }
-}
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void fence_mbar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-// K-major, 128-byte swizzled operand: 8-row atoms of 1024 bytes
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr >> 4) & 0x3fff);        // start address
-    d |= (uint64_t)1 << 16;                       // leading byte offset (unused for swizzled K-major)
-    d |= (uint64_t)(1024 >> 4) << 32;             // stride byte offset: 8 rows x 128 B
-    d |= (uint64_t)1 << 46;                       // descriptor version (sm_100)
-    d |= (uint64_t)2 << 61;                       // SWIZZLE_128B
-    return d;
-}
-
-// bf16 x bf16 -> fp32, both K-major, M = 128, N = 128
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kPBN >> 3) << 17) |
-                            ((uint32_t)(kPBM >> 4) << 24);
-
-// D (TMEM) += A (TMEM, lane = row, 2 bf16 per column) x B (shared, descriptor)
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(kIdesc), "r"(accumulate)
-        : "memory");
-}
-
-// D (TMEM) += A (shared, descriptor) x B (shared, descriptor), both K-major
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(kIdesc), "r"(accumulate)
-        : "memory");
-}
-
-#define SHERRY_TMEM_ST32(taddr, v)                                                                               \
-    asm volatile(                                                                                                \
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16," \
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),                        \
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),      \
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),          \
-        "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),         \
-        "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])                      \
-        : "memory")
-
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-#define SHERRY_TMEM_LD16(taddr, v)                                                                       \
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14," \
-                 "%15}, [%16];"                                                                          \
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),    \
-                   "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), \
-                   "=r"(v[14]), "=r"(v[15])                                                               \
-                 : "r"(taddr))
-
-#define SHERRY_TMEM_LD32(taddr, v)                                                                               \
-    asm volatile(                                                                                                \
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17," \
-        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"                                       \
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),        \
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),  \
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]),             \
-          "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),             \
-          "=r"(v[30]), "=r"(v[31])                                                                               \
-        : "r"(taddr))
 
 // Arenas (ARN): the same kernel also accumulates X W^T for a dense bf16 latent
 // weight W in a third TMEM accumulator and writes Y = (the promoted ternary sum)
@@ -222,10 +97,21 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 // same slots as X: a chunk is then two K-steps of X and two of W (64 KB), and the
 // ternary A stages shrink to 2 x 2 steps so that the dense accumulator fits in
 // TMEM (columns 384..511).
-template <int EPI, bool ARN>
+//
+// Adapters (kLora): after a tile's last K-chunk come chunks whose operand A is B_a
+// (the rank columns of the tile's weight rows, straight from its rows into TMEM) and
+// whose X slot holds U of the tile's tokens, zero for tokens of other adapters.  The
+// decode warps write both; each different adapter of the tile and each 16 ranks is
+// one K = 16 entry per bf16 term of U, four entries a step.  They form one more
+// group, with scale 1.  A tile of one adapter of rank 16 adds 3 K = 16 products to
+// K / 16, and a tile whose tokens all differ stays right, at 128 entries a term.
+enum class PMode { kPlain, kArenas, kLora };
+
+template <int EPI, PMode MODE>
 __global__ void __launch_bounds__(PRoles<EPI>::kThreads, 1)
 k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
           const __grid_constant__ PParams P) {
+    constexpr bool ARN = MODE == PMode::kArenas, LORA = MODE == PMode::kLora;
     constexpr int kPTmaWarp = PRoles<EPI>::kTmaWarp, kPMmaWarp = PRoles<EPI>::kMmaWarp;
     constexpr int CS = ARN ? kPArnSteps : kPChunkSteps;   // K-steps per chunk
     constexpr int XS = ARN ? kPArnSlots : kPXSlots;       // chunk slots
@@ -263,6 +149,10 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     const int nchunks = (nk + CS - 1) / CS;  // the last one may hold fewer steps
     const int gs = P.group_steps;
     const int ngroups = nk / gs;
+    // LORA: K = 16 entries of tile t's adapters, and their steps of four
+    const int rb = LORA ? (P.R + 15) / 16 : 1;
+    auto lora_entries = [&](int t) -> int { return LORA ? __ldg(P.tile_n + t / ntn) * rb * P.terms : 0; };
+    auto lora_steps = [&](int t) -> int { return LORA ? (lora_entries(t) + 3) / 4 : 0; };
 
     if (threadIdx.x == 0) {
         abort_s = 0;
@@ -348,6 +238,25 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             if (P.row_scale && row_ok) a = __ldg(P.scales + (P.per_tensor ? 0 : n));
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] *= a;
+            if constexpr (LORA) {
+                if (lora_steps(t) > 0) {
+                    ok = mbar_wait(acc_full(b), bph, &abort_s);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kPBN + half * kCols);
+#pragma unroll
+                    for (int c = 0; c < kCols / 16; ++c) {
+                        uint32_t v[16];
+                        SHERRY_TMEM_LD16(t_row + 16 * c, v);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[16 * c + j] += __uint_as_float(v[j]);
+                    }
+                    tc_fence_before();
+                    mbar_arrive(acc_empty(b));
+                    if (++b == kPAcc) { b = 0; bph ^= 1u; }
+                }
+            }
             if constexpr (ARN) {
                 // Y = the ternary sum + lambda * the dense product
                 ok = mbar_wait(dense_full, dph, &abort_s);
@@ -464,6 +373,70 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     ++cc;
                 }
             }
+            if constexpr (LORA) {
+                // the adapters' chunks: thread i writes row i of both operands
+                const int entries = lora_entries(t), lsteps = lora_steps(t);
+                const int64_t m = (int64_t)(t / ntn) * kPBN + i;
+                const int my = m < P.M ? __ldg(P.ids + m) : -1;
+                for (int st0 = 0; st0 < lsteps && ok; st0 += CS, ++cc) {
+                    const int hbuf = cc % AB;
+                    // chunk cc - AB done: A buffer hbuf is free, and so is X slot cc % XS (XS > AB)
+                    if (cc >= AB &&
+                        !mbar_wait(chunk_empty((cc - AB) % XS), (uint32_t)(((cc - AB) / XS) & 1), &abort_s)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int e = 0; e < SPG; ++e) {
+                        const int st = SPG * g + e;
+                        if (st0 + st >= lsteps) break;
+                        uint32_t v[32];
+                        const uint32_t xrow = stX + (uint32_t)((cc % XS) * SLOTB + st * kPStepB + (i >> 3) * 1024 +
+                                                               (i & 7) * 128);
+#pragma unroll
+                        for (int el = 0; el < 4; ++el) {
+                            const int en = (st0 + st) * 4 + el, qq = en / P.terms, term = en - qq * P.terms;
+                            const int r0 = (qq % rb) * 16;
+                            const bool in = en < entries;
+                            const int a = in ? __ldg(P.tile_a + (int64_t)(t / ntn) * kLoraTile + qq / rb) : -1;
+                            uint4 b0 = make_uint4(0u, 0u, 0u, 0u), b1 = b0;
+                            if (in && row_ok) {
+                                const uint4* src =
+                                    reinterpret_cast<const uint4*>(P.B + ((int64_t)a * P.N + n) * P.R + r0);
+                                b0 = __ldg(src);
+                                if (r0 + 8 < P.R) b1 = __ldg(src + 1);
+                            }
+                            v[8 * el] = b0.x, v[8 * el + 1] = b0.y, v[8 * el + 2] = b0.z, v[8 * el + 3] = b0.w;
+                            v[8 * el + 4] = b1.x, v[8 * el + 5] = b1.y, v[8 * el + 6] = b1.z, v[8 * el + 7] = b1.w;
+                            uint32_t h[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) h[j] = 0u;
+                            if (in && a == my) {
+                                const float4* src = reinterpret_cast<const float4*>(P.U + m * P.R + r0);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    if (r0 + 4 * j < P.R) {
+                                        const float4 f = __ldg(src + j);
+                                        h[2 * j] = split_pair(f.x, f.y, term);
+                                        h[2 * j + 1] = split_pair(f.z, f.w, term);
+                                    }
+                            }
+#pragma unroll
+                            for (int hh = 0; hh < 2; ++hh)
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                                 xrow + (uint32_t)(((2 * el + hh) ^ (i & 7)) * 16)),
+                                             "r"(h[4 * hh]), "r"(h[4 * hh + 1]), "r"(h[4 * hh + 2]), "r"(h[4 * hh + 3])
+                                             : "memory");
+                        }
+                        SHERRY_TMEM_ST32(t_lane + (uint32_t)((hbuf * CS + st) * kPAcols), v);
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    fence_proxy_async();
+                    mbar_arrive(full_a(hbuf));
+                }
+            }
         }
     } else if (warp == kPTmaWarp) {
         // ---------------- TMA producer for X (and, ARN, the latent-weight tiles) ----------------
@@ -491,6 +464,18 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     ++issued[c];
                     if (++c == XS) { c = 0; cph ^= 1u; }
                 }
+                if constexpr (LORA) {
+                    // the decode warps fill these slots themselves
+                    for (int st0 = 0; st0 < lora_steps(t) && ok; st0 += CS) {
+                        if (!mbar_wait(chunk_empty(c), cph ^ 1u, &abort_s)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive(full_x(c));
+                        ++issued[c];
+                        if (++c == XS) { c = 0; cph ^= 1u; }
+                    }
+                }
             }
             // every load issued must land before the CTA's shared memory goes away
             // (after an abort the MMA thread may not have waited for the last ones)
@@ -516,10 +501,10 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     tc_fence_after();
                 }
                 const uint32_t td = tmem + (uint32_t)(b * kPBN);
-                mma_bf16_ts(td, ta, db, first ? 0u : 1u);
+                mma_bf16_ts(td, ta, db, kIdesc, first ? 0u : 1u);
 #pragma unroll
                 for (int kk = 1; kk < kPBK / 16; ++kk)  // K = 16 per MMA: 8 A columns, +32 bytes in the B row
-                    mma_bf16_ts(td, ta + (uint32_t)(8 * kk), db + (uint64_t)(2 * kk), 1u);
+                    mma_bf16_ts(td, ta + (uint32_t)(8 * kk), db + (uint64_t)(2 * kk), kIdesc, 1u);
                 if constexpr (ARN) {
                     if (ks == 0) {
                         if (!mbar_wait(dense_empty, dph ^ 1u, &abort_s)) return false;
@@ -528,7 +513,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     const uint32_t tdd = tmem + (uint32_t)kDenseCol;
 #pragma unroll
                     for (int kk = 0; kk < kPBK / 16; ++kk)
-                        mma_bf16_ss(tdd, dw + (uint64_t)(2 * kk), db + (uint64_t)(2 * kk),
+                        mma_bf16_ss(tdd, dw + (uint64_t)(2 * kk), db + (uint64_t)(2 * kk), kIdesc,
                                     (ks == 0 && kk == 0) ? 0u : 1u);
                     if (ks == nk - 1) {
                         mma_commit(dense_full);
@@ -573,6 +558,36 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     mma_commit(chunk_empty(c));
                     if (++c == XS) { c = 0; cph ^= 1u; }
                 }
+                if constexpr (LORA) {
+                    const int lsteps = lora_steps(t);
+                    if (ok && lsteps > 0) {
+                        if (!mbar_wait(acc_empty(b), bph ^ 1u, &abort_s)) break;
+                        const uint32_t td = tmem + (uint32_t)(b * kPBN);
+                        for (int st0 = 0; st0 < lsteps; st0 += CS, ++cc) {
+                            const int hbuf = cc % AB;
+                            if (!mbar_wait(full_a(hbuf), (uint32_t)((cc / AB) & 1), &abort_s) ||
+                                !mbar_wait(full_x(c), cph, &abort_s)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint64_t db0 = smem_desc(stX + c * SLOTB);
+                            const uint32_t ta0 = tmem + (uint32_t)(kPAcol + hbuf * CS * kPAcols);
+                            const int steps = min(CS, lsteps - st0);
+                            for (int st = 0; st < steps; ++st)
+#pragma unroll
+                                for (int kk = 0; kk < kPBK / 16; ++kk)
+                                    mma_bf16_ts(td, ta0 + (uint32_t)(st * kPAcols + 8 * kk),
+                                                db0 + (uint64_t)((st * kPStepB) >> 4) + (uint64_t)(2 * kk), kIdesc,
+                                                (st0 + st + kk) == 0 ? 0u : 1u);
+                            mma_commit(chunk_empty(c));
+                            if (++c == XS) { c = 0; cph ^= 1u; }
+                        }
+                        if (!ok) break;
+                        mma_commit(acc_full(b));
+                        if (++b == kPAcc) { b = 0; bph ^= 1u; }
+                    }
+                }
             }
             // all MMAs this thread issued complete before TMEM is freed (after an abort
             // no epilogue has waited for them)
@@ -592,23 +607,6 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
 
 // ---- host side -------------------------------------------------------------------
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiled encode_fn() {
-    static EncodeTiled fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(p);
-    });
-    return fn;
-}
-
 bool prefill_eligible(const ProbShape& s, int64_t M) {
     if (M < 17 || s.N == 0) return false;
     if (s.K % kPBK != 0) return false;
@@ -617,22 +615,9 @@ bool prefill_eligible(const ProbShape& s, int64_t M) {
     return true;
 }
 
-static int encode_2d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int box_rows) {
-    EncodeTiled enc = encode_fn();
-    if (!enc) return SHERRY_ERR_UNSUPPORTED;
-    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kPBK, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? SHERRY_OK : SHERRY_ERR_UNSUPPORTED;
-}
-
-// Wd: the latent bf16 weight for Arenas (null: the plain linear)
+// Wd: the latent bf16 weight for Arenas; lora: the adapters' part of P (null: the plain linear)
 static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16,
-                              const uint16_t* Wd, float lambda, cudaStream_t stream) {
+                              const uint16_t* Wd, float lambda, const LoraArgs* lora, cudaStream_t stream) {
     CUtensorMap map, wmap;
     int st = encode_2d(&map, d.X, s.K, M, kPBN);
     if (st) return st;
@@ -653,14 +638,25 @@ static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, i
     P.spr = s.granularity == SHERRY_PER_GROUP ? (int)(s.K / s.group) : 1;
     P.group_steps = s.granularity == SHERRY_PER_GROUP ? s.group / kPBK : (int)(s.K / kPBK);
     P.lambda = lambda;
+    if (lora) {
+        P.B = lora->B;
+        P.U = lora->U;
+        P.ids = lora->ids;
+        P.tile_n = lora->plan.tile_n;
+        P.tile_a = lora->plan.tile_a;
+        P.R = lora->R;
+        P.terms = y_bf16 ? 2 : 3;  // 16 bits of U under a bf16 result, all 24 under an fp32 one
+    }
     // per device: the shared-memory opt-in of every instantiation, and the SM count
     static PerDevice dev_sms;
     int sms = 0;
     st = per_device(dev_sms, &sms, [](int& v) {
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<8, PMode::kPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<16, PMode::kPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<8, PMode::kArenas>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<16, PMode::kArenas>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<8, PMode::kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_prefill<16, PMode::kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem));
         int dev = 0;
         SHERRY_CUDA_CHECK(cudaGetDevice(&dev));
         SHERRY_CUDA_CHECK(cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev));
@@ -674,23 +670,28 @@ static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, i
     // 3B shapes that pays for group scales up to K = 4096 (+6%) and costs at K = 8192 (-15%) and
     // for per-row scales (one drain per tile; -1.5% at 2048 and 4096 tokens)
     const bool epi16 = s.granularity == SHERRY_PER_GROUP && s.K <= 4096;
-    if (Wd) {
+    if (lora) {
         if (epi16)
-            k_prefill<16, true><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            k_prefill<16, PMode::kLora><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, P);
         else
-            k_prefill<8, true><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            k_prefill<8, PMode::kLora><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, P);
+    } else if (Wd) {
+        if (epi16)
+            k_prefill<16, PMode::kArenas><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, P);
+        else
+            k_prefill<8, PMode::kArenas><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, P);
     } else {
         if (epi16)
-            k_prefill<16, false><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            k_prefill<16, PMode::kPlain><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, P);
         else
-            k_prefill<8, false><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            k_prefill<8, PMode::kPlain><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, P);
     }
     SHERRY_LAUNCH_CHECK();
     return SHERRY_OK;
 }
 
 int prefill_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16, cudaStream_t stream) {
-    return prefill_launch_any(s, d, M, y_bf16, nullptr, 0.0f, stream);
+    return prefill_launch_any(s, d, M, y_bf16, nullptr, 0.0f, nullptr, stream);
 }
 
 bool arenas_eligible(const ProbShape& s, int64_t M) {
@@ -701,20 +702,21 @@ bool arenas_eligible(const ProbShape& s, int64_t M) {
 
 int arenas_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16, const uint16_t* Wd,
                   float lambda, cudaStream_t stream) {
-    return prefill_launch_any(s, d, M, y_bf16, Wd, lambda, stream);
+    return prefill_launch_any(s, d, M, y_bf16, Wd, lambda, nullptr, stream);
+}
+
+int prefill_lora_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16, const LoraArgs& lora,
+                        cudaStream_t stream) {
+    return prefill_launch_any(s, d, M, y_bf16, nullptr, 0.0f, &lora, stream);
 }
 
 int device_status_take(cudaStream_t stream) {
     SHERRY_CUDA_CHECK(cudaStreamSynchronize(stream));
-    int v = 0;
-    SHERRY_CUDA_CHECK(cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int)));
-    if (v) {
-        const int zero = 0;
-        SHERRY_CUDA_CHECK(cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)));
-    }
+    const int v = tc_status_take();
     const int w = skinny_status_take();
     const int x = stream_status_take();
-    return v ? v : w ? w : x;
+    const int y = dgrad_status_take();
+    return v ? v : w ? w : x ? x : y;
 }
 
 }  // namespace sherry

@@ -10,12 +10,14 @@
 // maximum, S and the weighted sum in fp32 in base 2: with L = log2(e) and
 // r = rn(m L), e = 2^(z L - r) is one fused multiply-add and one exponential;
 // that r is a rounded m L scales every e by the same 2^(m L - r), which the
-// row's end takes back out.  The likeliest tokens come from the same pass: keys
-// (value, ~index) at or above a threshold are appended to a list in shared
-// memory; the threshold starts at the smallest of 32 disjoint groups' maxima (a
-// lower bound of the 32nd largest) and rises to the k-th best key whenever the
-// list is cut back.  A key's place in the answer is the number of larger keys,
-// so ties go to the lowest index and the order of the appends does not matter.
+// row's end takes back out.  The likeliest tokens cost the pass nothing: the
+// k-th largest of the threads' maxima is a lower bound of the k-th largest element,
+// and only the (about k of 256) threads whose maximum reaches it hold elements that
+// do.  Their elements alone are read again (out of L2) and those at or above the
+// bound are listed as keys (value, ~index).  A key's place in the answer is the
+// number of larger keys, so ties go to the lowest index and the order of the list
+// does not matter.  Rows of many equal values overflow the list and are gone through
+// once more with a rising threshold.
 //
 // Rows whose maximum is beyond +-1e38 (masks of the type's lowest value
 // everywhere) would overflow m L and take a second pass with z - m first.  All
@@ -130,12 +132,24 @@ __device__ __forceinline__ uint4 lp_load(const T* row, int e0, int V) {
     return LpVec<T>::pack(f);
 }
 
+// the largest element of a vector
+template <typename T>
+__device__ __forceinline__ float lp_max(uint4 v) {
+    float f[LpVec<T>::N];
+    LpVec<T>::unpack(v, f);
+    float m = f[0];
+#pragma unroll
+    for (int j = 1; j < LpVec<T>::N; ++j) m = fmaxf(m, f[j]);
+    return m;
+}
+
 struct LpTop {  // shared state of the likeliest tokens
+    float tmax[kLpThreads];    // the threads' maxima
     uint64_t buf[kLpCap];
     uint64_t best[kLpMaxTop];
-    float group[32];
     uint64_t thr;
-    int cnt;
+    uint8_t list[kLpThreads];  // threads that hold candidates
+    int cnt, listed;
 };
 
 // The `k` largest of buf[0..n), in order, into best (0 where there are fewer).
@@ -151,8 +165,56 @@ __device__ __forceinline__ void lp_rank(LpTop& s, int n, int k) {
     __syncthreads();
 }
 
+// Append a vector's keys at or above the threshold; elements [0, hi) of the row count.
+template <typename T>
+__device__ __forceinline__ void lp_push(LpTop& s, uint4 x, int e0, int hi, uint64_t thr, float tv) {
+    float f[LpVec<T>::N];
+    LpVec<T>::unpack(x, f);
+#pragma unroll
+    for (int j = 0; j < LpVec<T>::N; ++j) {
+        const int e = e0 + j;
+        if (f[j] >= tv && e >= 0 && e < hi) {
+            const uint64_t key = lp_key(f[j], e);
+            if (key >= thr) {
+                const int at = atomicAdd(&s.cnt, 1);
+                if (at < kLpCap) s.buf[at] = key;
+            }
+        }
+    }
+}
+
+// Append one iteration's keys, after which the list is whole: where more keys pass than it holds,
+// the threshold rises to the k-th best of those held (each is in the row, so that is a bound) and
+// the iteration's are appended again.  A long list is cut back to its best.  Called by all threads.
+template <typename T>
+__device__ __noinline__ void lp_collect(LpTop& s, const uint4 (&xs)[kLpVecs], int v, int v1, int off, int V, int k) {
+    constexpr int N = LpVec<T>::N;
+    const int held = s.cnt;
+    __syncthreads();
+    while (true) {
+        const uint64_t thr = s.thr;
+        const float tv = lp_unorder((uint32_t)(thr >> 32));
+        for (int u = 0; u < kLpVecs; ++u)
+            if (v + u * kLpThreads < v1 && lp_max<T>(xs[u]) >= tv)
+                lp_push<T>(s, xs[u], off + N * (v + u * kLpThreads), V, thr, tv);
+        __syncthreads();
+        const int n = s.cnt;
+        const bool over = n > kLpCap;
+        if (over || n > k + kLpRefine) {
+            lp_rank(s, min(n, kLpCap), k);
+            if (threadIdx.x == 0) {
+                s.thr = max(s.thr, s.best[k - 1]);
+                s.cnt = over ? held : k;
+            }
+            if (!over && (int)threadIdx.x < k) s.buf[threadIdx.x] = s.best[threadIdx.x];
+        }
+        __syncthreads();
+        if (!over) return;
+    }
+}
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) k_logprobs(const LpParams P) {
+__global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
     constexpr int N = LpVec<T>::N;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -182,28 +244,12 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LpParams P) {
     };
 
     float m = -INFINITY, r = -kEdge * kLog2e, s1 = 0.0f, s2 = 0.0f;
-    if constexpr (TOP) {
-        if (tid == 0) {
-            top_s.cnt = 0;
-            top_s.thr = 0;
-        }
-    }
     uint4 x[kLpVecs];
-    fetch(0, x);
     for (int it = 0; it < iters; ++it) {
-        uint4 nx[kLpVecs];
-        if (it + 1 < iters) fetch(it + 1, nx);
-        float vm[kLpVecs];
+        fetch(it, x);
         float bm = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kLpVecs; ++u) {
-            float f[N];
-            LpVec<T>::unpack(x[u], f);
-            vm[u] = f[0];
-#pragma unroll
-            for (int j = 1; j < N; ++j) vm[u] = fmaxf(vm[u], f[j]);
-            bm = fmaxf(bm, vm[u]);
-        }
+        for (int u = 0; u < kLpVecs; ++u) bm = fmaxf(bm, lp_max<T>(x[u]));
         if (bm > m) {
             const float nr = fmaxf(bm, -kEdge) * kLog2e;
             const float d = fmaxf(r - nr, -1e4f), f = ex2(d);
@@ -224,76 +270,53 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LpParams P) {
                 s2 = fmaf(e, fmaxf(y, -1e4f), s2);  // e = 0 there: 0 * -inf would be NaN
             }
         }
-        if constexpr (TOP) {
-            if (it == 0) {
-                // 32 groups of 8 threads: the smallest of their maxima has 32 elements at or above it
-                float g = bm;
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) g = fmaxf(g, __shfl_xor_sync(kFull, g, o));
-                if ((tid & 7) == 0) top_s.group[tid >> 3] = g;
-                __syncthreads();
-                g = top_s.group[lane];
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) g = fminf(g, __shfl_xor_sync(kFull, g, o));
-                if (tid == 0) top_s.thr = (uint64_t)lp_order(g) << 32;
-                __syncthreads();
-            }
-            const int held = top_s.cnt;  // nothing is appended between the last barrier and the next
-            __syncthreads();
-            while (true) {
-                const uint64_t thr = top_s.thr;
-                const float tv = lp_unorder((uint32_t)(thr >> 32));
-#pragma unroll
-                for (int u = 0; u < kLpVecs; ++u) {
-                    if (vm[u] >= tv) {
-                        float f[N];
-                        LpVec<T>::unpack(x[u], f);
-                        const int e0 = off + N * (v0 + (it * kLpVecs + u) * kLpThreads + tid);
-#pragma unroll
-                        for (int j = 0; j < N; ++j) {
-                            if (f[j] >= tv) {
-                                const int e = e0 + j;
-                                const uint64_t key = lp_key(f[j], e);
-                                if (key >= thr && e >= 0 && e < V && v0 + (it * kLpVecs + u) * kLpThreads + tid < v1) {
-                                    const int at = atomicAdd(&top_s.cnt, 1);
-                                    if (at < kLpCap) top_s.buf[at] = key;
-                                }
-                            }
-                        }
-                    }
-                }
-                __syncthreads();
-                const int n = top_s.cnt;
-                if (n <= kLpCap) {
-                    if (n > top + kLpRefine) {  // cut back to the best, raise the threshold
-                        lp_rank(top_s, n, top);
-                        if (tid < top) top_s.buf[tid] = top_s.best[tid];
-                        if (tid == 0) {
-                            top_s.cnt = top;
-                            top_s.thr = max(top_s.thr, top_s.best[top - 1]);
-                        }
-                        __syncthreads();
-                    }
-                    break;
-                }
-                // more keys than the list holds: raise the threshold to the k-th best of those
-                // held (each is in the row, so it is a bound) and append this iteration's again
-                lp_rank(top_s, kLpCap, top);
-                if (tid == 0) {
-                    top_s.thr = max(top_s.thr, top_s.best[top - 1]);
-                    top_s.cnt = held;
-                }
-                __syncthreads();
-            }
-        }
-        if (it + 1 < iters) {
-#pragma unroll
-            for (int u = 0; u < kLpVecs; ++u) x[u] = nx[u];
-        }
     }
     if constexpr (TOP) {
+        // a value that k of the threads' maxima reach bounds the k-th largest element from below, and
+        // only threads whose maximum reaches it hold an element that does
+        top_s.tmax[tid] = m;
+        if (tid == 0) top_s.cnt = top_s.listed = 0;
         __syncthreads();
-        lp_rank(top_s, min(top_s.cnt, kLpCap), top);
+        if (warp == 0) {
+            // the largest value of 16 leading bits that at least k of the maxima reach, bit by bit
+            uint32_t o[8], t = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = lp_order(top_s.tmax[lane + 32 * j]);
+#pragma unroll
+            for (int bit = 31; bit >= 16; --bit) {
+                const uint32_t want = t | (1u << bit);
+                int n = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) n += o[j] >= want;
+                if (__reduce_add_sync(kFull, n) >= top) t = want;
+            }
+            if (lane == 0) top_s.thr = (uint64_t)max(t, lp_order(-INFINITY)) << 32;  // (below -inf: NaNs)
+        }
+        __syncthreads();
+        const uint64_t thr = top_s.thr;
+        const float tv = lp_unorder((uint32_t)(thr >> 32));
+        if (m >= tv) top_s.list[atomicAdd(&top_s.listed, 1)] = (uint8_t)tid;
+        __syncthreads();
+        const int per = iters * kLpVecs, total = top_s.listed * per;
+        for (int i = tid; i < total; i += kLpThreads) {
+            const int v = v0 + (i % per) * kLpThreads + top_s.list[i / per];
+            if (v < v1) {
+                const uint4 y = lp_load(row, off + N * v, V);
+                if (lp_max<T>(y) >= tv) lp_push<T>(top_s, y, off + N * v, V, thr, tv);
+            }
+        }
+        __syncthreads();
+        if (top_s.cnt > kLpCap) {  // (uniform) many equal values: again, with the threshold rising
+            __syncthreads();
+            if (tid == 0) top_s.cnt = 0;
+            __syncthreads();
+            for (int it = 0; it < iters; ++it) {
+                uint4 cx[kLpVecs];  // (not x: what a call takes by address leaves the registers)
+                fetch(it, cx);
+                lp_collect<T>(top_s, cx, v0 + it * kLpVecs * kLpThreads + tid, v1, off, V, top);
+            }
+        }
+        lp_rank(top_s, top_s.cnt, top);
     }
 
     // the row's maximum

@@ -67,6 +67,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// r = rn(m L): the product must be rounded by itself everywhere, never inside a fused multiply-add
+__device__ __forceinline__ float ref_of(float m) { return __fmul_rn(fmaxf(m, -kEdge), kLog2e); }
+
 template <typename T>
 struct LpVec;
 template <>
@@ -224,8 +227,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     __shared__ typename std::conditional<TOP, LpTop, int>::type top_s;
-    __shared__ float red[3][kLpThreads / 32];
-    __shared__ float part[3];  // this CTA's maximum, S, weighted sum
+    __shared__ float4 red[kLpThreads / 32];  // the warps' maxima, S, weighted sums
+    __shared__ float4 part;                  // this CTA's
 
     // the row's 16-byte vectors: vector v holds elements off + N v ..; this CTA's share is [v0, v1)
     const int off = -(int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
@@ -243,7 +246,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
         }
     };
 
-    float m = -INFINITY, r = -kEdge * kLog2e, s1 = 0.0f, s2 = 0.0f;
+    // the target's logit is fetched beside the pass
+    int target = -1;
+    float zt = 0.0f;
+    if (tid == 0 && rank == 0 && P.logp) {
+        target = P.targets[rowi];
+        if (target >= 0 && target < V) zt = LpVec<T>::one(row + target);
+    }
+    float m = -INFINITY, r = ref_of(-INFINITY), s1 = 0.0f, s2 = 0.0f;
     uint4 x[kLpVecs];
     for (int it = 0; it < iters; ++it) {
         fetch(it, x);
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
 #pragma unroll
         for (int u = 0; u < kLpVecs; ++u) bm = fmaxf(bm, lp_max<T>(x[u]));
         if (bm > m) {
-            const float nr = fmaxf(bm, -kEdge) * kLog2e;
+            const float nr = ref_of(bm);
             const float d = fmaxf(r - nr, -1e4f), f = ex2(d);
             s2 = f * fmaf(d, s1, s2);
             s1 *= f;
@@ -319,26 +329,46 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
         lp_rank(top_s, top_s.cnt, top);
     }
 
-    // the row's maximum
+    // the row's sums: threads of a warp, warps of the CTA, CTAs of the cluster, in order
+    auto rebase = [](float& a, float& b, float from, float to) {  // sums relative to `from`, now to `to`
+        const float d = fmaxf(from - to, -1e4f), f = ex2(d);
+        b = f * fmaf(d, a, b);
+        a *= f;
+    };
     float bmax = m;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) bmax = fmaxf(bmax, __shfl_xor_sync(kFull, bmax, o));
-    if (lane == 0) red[0][warp] = bmax;
-    __syncthreads();
-    bmax = red[0][lane & (kLpThreads / 32 - 1)];
+    rebase(s1, s2, r, ref_of(bmax));
 #pragma unroll
-    for (int o = kLpThreads / 64; o >= 1; o >>= 1) bmax = fmaxf(bmax, __shfl_xor_sync(kFull, bmax, o));
-    if (C > 1) {
-        if (tid == 0) part[0] = bmax;
-        cluster.sync();
-        for (int c = 0; c < C; ++c) bmax = fmaxf(bmax, *cluster.map_shared_rank(&part[0], c));
+    for (int o = 16; o >= 1; o >>= 1) {
+        s1 += __shfl_xor_sync(kFull, s1, o);
+        s2 += __shfl_xor_sync(kFull, s2, o);
     }
-    float ref = fmaxf(bmax, -kEdge) * kLog2e;
+    if (lane == 0) red[warp] = make_float4(bmax, s1, s2, 0.0f);
+    __syncthreads();
+    auto join = [&](auto get, int n) {  // (maximum, sums) of n parts
+        float4 q = get(0);
+        bmax = q.x;
+        for (int i = 1; i < n; ++i) bmax = fmaxf(bmax, get(i).x);
+        s1 = s2 = 0.0f;
+        for (int i = 0; i < n; ++i) {
+            q = get(i);
+            rebase(q.y, q.z, ref_of(q.x), ref_of(bmax));
+            s1 += q.y;
+            s2 += q.z;
+        }
+    };
+    join([&](int i) { return red[i]; }, kLpThreads / 32);
+    if (C > 1) {
+        if (tid == 0) part = make_float4(bmax, s1, s2, 0.0f);
+        cluster.sync();
+        join([&](int i) { return *cluster.map_shared_rank(&part, i); }, C);
+    }
+    float ref = ref_of(bmax);
     const bool edge = bmax > kEdge || (bmax < -kEdge && bmax != -INFINITY);
     if (edge) {
         // m log2(e) overflows: this row again, with z - m first
-        s1 = 0.0f;
-        s2 = 0.0f;
+        s1 = s2 = 0.0f;
         for (int v = v0 + tid; v < v1; v += kLpThreads) {
             float f[N];
             LpVec<T>::unpack(lp_load(row, off + N * v, V), f);
@@ -350,42 +380,32 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
                 s2 = fmaf(e, fmaxf(y, -1e4f), s2);
             }
         }
-        ref = 0.0f;
-    } else {
-        const float d = fmaxf(r - ref, -1e4f), f = ex2(d);
-        s2 = f * fmaf(d, s1, s2);
-        s1 *= f;
-    }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        s1 += __shfl_xor_sync(kFull, s1, o);
-        s2 += __shfl_xor_sync(kFull, s2, o);
-    }
-    if (lane == 0) {
-        red[1][warp] = s1;
-        red[2][warp] = s2;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        s1 = s2 = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kLpThreads / 32; ++w) {
-            s1 += red[1][w];
-            s2 += red[2][w];
+        for (int o = 16; o >= 1; o >>= 1) {
+            s1 += __shfl_xor_sync(kFull, s1, o);
+            s2 += __shfl_xor_sync(kFull, s2, o);
         }
-        part[1] = s1;
-        part[2] = s2;
-    }
-    if (C > 1)
-        cluster.sync();
-    else
         __syncthreads();
-    if (rank == 0) {
+        if (lane == 0) red[warp] = make_float4(0.0f, s1, s2, 0.0f);
+        __syncthreads();
         s1 = s2 = 0.0f;
-        for (int c = 0; c < C; ++c) {
-            s1 += *cluster.map_shared_rank(&part[1], c);
-            s2 += *cluster.map_shared_rank(&part[2], c);
+        for (int w = 0; w < kLpThreads / 32; ++w) {
+            s1 += red[w].y;
+            s2 += red[w].z;
         }
+        if (C > 1) {
+            cluster.sync();
+            if (tid == 0) part = make_float4(0.0f, s1, s2, 0.0f);
+            cluster.sync();
+            s1 = s2 = 0.0f;
+            for (int c = 0; c < C; ++c) {
+                const float4 q = *cluster.map_shared_rank(&part, c);
+                s1 += q.y;
+                s2 += q.z;
+            }
+        }
+    }
+    if (rank == 0) {
         // log S relative to the true maximum: S was summed relative to ref = rn(m L)
         const bool dead = bmax == -INFINITY, bad = !(s1 < INFINITY);
         float lsum = logf(s1) + (edge ? 0.0f : fmaf(-bmax, kLog2e, ref) * kLn2);
@@ -393,12 +413,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
         if (bad) lsum = NAN;
         if (tid == 0) {
             if (P.logp) {
-                const int t = P.targets[rowi];
                 float lp = 0.0f;
-                if (t >= 0 && t < V) {
-                    const float zt = LpVec<T>::one(row + t);
+                if (target >= 0 && target < V)
                     lp = bad ? NAN : (dead || zt == -INFINITY) ? -INFINITY : (zt - bmax) - lsum;
-                }
                 P.logp[rowi] = lp;
             }
             if (P.entropy)
@@ -548,11 +565,12 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs_bwd(const LpBwdParams P
 
 template <typename T>
 static int lp_launch(const LpParams& P, int64_t M, int sms, cudaStream_t stream) {
-    // CTAs per row: enough to give every SM four of them (their resident number), as long as each
-    // still has a full iteration of vectors
+    // CTAs per row: several while there are fewer rows than SMs to share them, as long as each CTA
+    // has a full iteration of vectors.  A cluster's launch and joins cost more than an idle slot:
+    // 128256 bf16, top 8: 64 rows 18.5 / 11.5 / 13.0 us with 1 / 4 / 8 CTAs, 600 rows 52 / 55 with 1 / 2
     const int64_t iters = (P.V / LpVec<T>::N + kLpThreads * kLpVecs - 1) / (kLpThreads * kLpVecs);
     int c = 1;
-    while (c < 8 && M * c < 2 * (int64_t)sms && c < iters) c *= 2;
+    while (c < 8 && 2 * M * c < 3 * (int64_t)sms && c < iters) c *= 2;
     if (M * c > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(M * c));
@@ -563,7 +581,7 @@ static int lp_launch(const LpParams& P, int64_t M, int sms, cudaStream_t stream)
     at.val.clusterDim.x = (unsigned)c;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = c > 1;
     if (P.top > 0)
         SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, true>, P));
     else

@@ -578,7 +578,7 @@ static int check_ws(const void* workspace, size_t workspace_bytes, size_t need) 
 }
 
 static int check_lora(int64_t M, int n_adapters, int rank) {
-    if (M < 0 || M > 0x3fffffff) return SHERRY_ERR_SHAPE;
+    if (M < 0 || M > 0x3f000000) return SHERRY_ERR_SHAPE;
     if (n_adapters < 1 || n_adapters > SHERRY_MAX_ADAPTERS) return SHERRY_ERR_SHAPE;
     if (rank < 8 || rank > SHERRY_MAX_RANK || rank % 8 != 0) return SHERRY_ERR_SHAPE;
     return SHERRY_OK;
@@ -594,23 +594,35 @@ static bool lora_in_prefill(const ProbShape& s, int64_t M) {
 }
 
 struct LoraWs {
-    size_t u, plan, y32, total;  // offsets (0: none) and size
+    size_t u, plan, img, xp, y32, total;  // offsets (0: none) and size
 };
+
+// bf16 terms of U or P: 16 bits under a bf16 result, all 24 under an fp32 one
+static int lora_terms(int dtype) { return dtype == SHERRY_BF16 ? 2 : 3; }
 
 // The linear's own workspace comes first and always keeps the ticket region to itself.
 static LoraWs lora_ws(const ProbShape& s, int64_t M, int n_adapters, int rank, int y_dtype) {
     LoraWs w{};
     const bool pre = lora_in_prefill(s, M);
     size_t at = std::max(up256(pre ? 0 : linear_ws_bytes(&s, 1, M, device_sms())), kTicketBytes);
-    w.u = at;
-    at += up256((size_t)M * rank * sizeof(float));
     if (pre || M > kLoraFew) {
         w.plan = at;
         at += lora_plan_bytes(M, n_adapters);
+        if (lora_may_permute(M, n_adapters)) {
+            w.xp = at;
+            at += up256((size_t)(M * s.K) * 2);
+        }
     }
-    if (!pre && y_dtype == SHERRY_BF16) {
-        w.y32 = at;
-        at += (size_t)(M * s.N) * sizeof(float);
+    if (pre) {
+        w.img = at;
+        at += lora_image_bytes(M, n_adapters, rank, lora_terms(y_dtype));
+    } else {
+        w.u = at;
+        at += up256((size_t)M * rank * sizeof(float));
+        if (y_dtype == SHERRY_BF16) {
+            w.y32 = at;
+            at += (size_t)(M * s.N) * sizeof(float);
+        }
     }
     w.total = at;
     return w;
@@ -643,17 +655,32 @@ int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int sms = device_sms();
     const bool bf16 = y_dtype == SHERRY_BF16;
-    float* u = U ? U : reinterpret_cast<float*>(ws + w.u);
+    const bool pre = lora_in_prefill(s, M);
+    float* u = U || pre ? U : reinterpret_cast<float*>(ws + w.u);
     LoraPlan plan{};
+    LoraDown down{};
     if (w.plan) {
         plan = lora_plan_in(ws + w.plan, M, n_adapters);
         if ((st = lora_plan_launch(ids, M, n_adapters, plan, cs))) return st;
-        st = lora_down_launch(X, K, M, K, A, K, rank, ids, scaling, n_adapters, plan, u, sms, cs);
+        down.G = X;
+        if (w.xp) {
+            const LoraRows rows{X, reinterpret_cast<uint16_t*>(ws + w.xp), K, K, 0};
+            if ((st = lora_rows_launch(&rows, 1, M, plan, cs))) return st;
+            down.Gp = rows.dst;
+        }
+        down.ldg = down.C = K;
+        down.W = A;
+        down.ids = ids;
+        down.scaling = scaling;
+        down.V = u;
+        if (pre) down.img = LoraImage{reinterpret_cast<uint16_t*>(ws + w.img), lora_rp(rank), lora_terms(y_dtype)};
+        st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs);
     } else {
         st = lora_down_few_launch(X, K, M, K, A, K, rank, ids, scaling, n_adapters, u, cs);
     }
     if (st) return st;
-    if (lora_in_prefill(s, M)) return prefill_lora_launch(s, d, M, bf16, LoraArgs{B, u, ids, rank, plan}, cs);
+    if (pre)
+        return prefill_lora_launch(s, d, M, bf16, LoraArgs{B, down.img, down.Gp, rank, n_adapters, plan}, cs);
     float* y32 = bf16 ? reinterpret_cast<float*>(ws + w.y32) : static_cast<float*>(Y);
     d.Y = y32;
     if ((st = linear_launch(&s, &d, 1, M, 0, workspace, sms, cs))) return st;
@@ -665,22 +692,25 @@ int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const
 static int64_t padded_rows(int64_t N) { return (N + 7) & ~(int64_t)7; }
 
 struct BwdWs {
-    size_t pad, part, bt, p, plan, total;
+    size_t g, part, xp, imgp, imgu, plan, total;
 };
 
 static BwdWs backward_ws(int64_t M, int64_t N, int64_t K, int n_adapters, int rank) {
     BwdWs w{};
     size_t at = 0;
     const int64_t ld = padded_rows(N);
-    w.pad = at;
-    if (ld != N) at += up256((size_t)(M * ld) * 2);
+    const bool permute = n_adapters > 0 && lora_may_permute(M, n_adapters);
+    w.g = at;
+    if (ld != N || permute) at += up256((size_t)(M * ld) * 2);
     w.part = at;
     at += up256(dgrad_workspace_bytes(M, N, K, device_sms()));
     if (n_adapters > 0) {
-        w.bt = at;
-        at += up256((size_t)n_adapters * rank * (size_t)ld * 2);
-        w.p = at;
-        at += up256((size_t)M * rank * sizeof(float));
+        w.xp = at;
+        if (permute) at += up256((size_t)(M * K) * 2);
+        w.imgp = at;
+        at += lora_image_bytes(M, n_adapters, rank, 3);
+        w.imgu = at;
+        at += lora_image_bytes(M, n_adapters, rank, 3);
         w.plan = at;
         at += lora_plan_bytes(M, n_adapters);
     }
@@ -724,11 +754,12 @@ int sherry_linear_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, 
     const int64_t ld = padded_rows(N);
     const uint16_t* G = dY;
     if (ld != N) {
-        G = reinterpret_cast<uint16_t*>(ws + w.pad);
-        if ((st = lora_pad_launch(dY, M, N, reinterpret_cast<uint16_t*>(ws + w.pad), ld, cs))) return st;
+        const LoraRows rows{dY, reinterpret_cast<uint16_t*>(ws + w.g), N, ld, 1};
+        if ((st = lora_rows_launch(&rows, 1, M, LoraPlan{}, cs))) return st;
+        G = rows.dst;
     }
-    return dgrad_launch(ProbShape{N, K, granularity, group}, idx, sgn, scales, G, ld, M, dX, nullptr, nullptr, nullptr,
-                        nullptr, 0, ws + w.part, device_sms(), cs);
+    return dgrad_launch(ProbShape{N, K, granularity, group}, idx, sgn, scales, G, ld, M, dX, nullptr, ws + w.part,
+                        device_sms(), cs);
 }
 
 size_t sherry_linear_lora_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int n_adapters, int rank) {
@@ -763,26 +794,47 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     char* ws = static_cast<char*>(workspace);
     const int sms = device_sms();
     const int64_t ld = padded_rows(N);
-    const uint16_t* G = dY;
-    if (ld != N) {
-        G = reinterpret_cast<uint16_t*>(ws + w.pad);
-        if ((st = lora_pad_launch(dY, M, N, reinterpret_cast<uint16_t*>(ws + w.pad), ld, cs))) return st;
-    }
+    const int terms = lora_terms(grad_dtype);
     const LoraPlan plan = lora_plan_in(ws + w.plan, M, n_adapters);
     if ((st = lora_plan_launch(ids, M, n_adapters, plan, cs))) return st;
-    float* p = reinterpret_cast<float*>(ws + w.p);
+    // padded rows are in the plan's order whatever that is; others have a copy in case it permutes
+    LoraRows rows[2];
+    int copies = 0;
+    uint16_t* g = reinterpret_cast<uint16_t*>(ws + w.g);
+    uint16_t* xp = reinterpret_cast<uint16_t*>(ws + w.xp);
+    if (ld != N || plan.may_permute) rows[copies++] = LoraRows{dY, g, N, ld, ld != N};
+    if (dA && plan.may_permute) rows[copies++] = LoraRows{X, xp, K, K, 0};
+    if (copies && (st = lora_rows_launch(rows, copies, M, plan, cs))) return st;
+    const uint16_t* G = ld != N ? g : dY;
+    const uint16_t* Gp = plan.may_permute ? g : nullptr;
+    const LoraImage imgp{reinterpret_cast<uint16_t*>(ws + w.imgp), lora_rp(rank), terms};
+    const LoraImage imgu{reinterpret_cast<uint16_t*>(ws + w.imgu), lora_rp(rank), terms};
+    LoraDown down{};
+    down.ids = ids;
     if (dX || dA) {
-        uint16_t* bt = reinterpret_cast<uint16_t*>(ws + w.bt);
-        if ((st = lora_transpose_launch(B, n_adapters, N, rank, bt, ld, cs))) return st;
-        if ((st = lora_down_launch(G, ld, M, ld, bt, ld, rank, ids, scaling, n_adapters, plan, p, sms, cs))) return st;
+        down.G = G;
+        down.Gp = Gp;
+        down.ldg = ld;
+        down.C = N;
+        down.W = B;
+        down.by_row = 1;
+        down.scaling = scaling;
+        down.unit = scales;
+        down.img = imgp;
     }
-    if (dX && (st = dgrad_launch(ProbShape{N, K, granularity, group}, idx, sgn, scales, G, ld, M, dX, &plan, A, p, ids,
-                                 rank, ws + w.part, sms, cs)))
+    if (dB) {
+        down.V2 = U;
+        down.img2 = imgu;
+    }
+    if ((st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs))) return st;
+    const LoraGradArgs args{A, imgp, Gp, rank, n_adapters, plan};
+    if (dX && (st = dgrad_launch(ProbShape{N, K, granularity, group}, idx, sgn, scales, G, ld, M, dX, &args, ws + w.part,
+                                 sms, cs)))
         return st;
     LoraGradJob jobs[2];
     int count = 0;
-    if (dB) jobs[count++] = LoraGradJob{U, G, ld, N, dB, 1};
-    if (dA) jobs[count++] = LoraGradJob{p, X, K, K, dA, 0};
+    if (dB) jobs[count++] = LoraGradJob{imgu, G, Gp, ld, N, dB, nullptr, 1};
+    if (dA) jobs[count++] = LoraGradJob{imgp, X, plan.may_permute ? xp : nullptr, K, K, dA, scales, 0};
     if (count == 0) return SHERRY_OK;
     return lora_grad_launch(jobs, count, rank, n_adapters, M, plan, grad_dtype == SHERRY_BF16, sms, cs);
 }

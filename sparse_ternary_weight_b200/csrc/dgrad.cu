@@ -19,10 +19,10 @@
 // The weights are operand B in the layout they unpack to, k contiguous (MN-major,
 // 128-byte swizzle): a decode thread owns 64 consecutive k of a row, looks each
 // block of 4 up in the 32 patterns, scales it with one packed multiply per pair and
-// stores 16 bytes at a time, conflict-free (eight lanes take the eight rows of a
-// swizzle atom).  After the last rows the same warps append the adapters' stages:
-// operand B is A_a as it is stored, operand A is P of the tile's tokens, zero for
-// tokens of other adapters, split into 2 bf16 terms (16 significant bits).
+// stores 16 bytes at a time, conflict-free (eight lanes take the eight rows of a swizzle
+// atom).  After the last rows come the adapters' stages, one or two per slot and 64
+// ranks, all by TMA: operand B is A_a as it is stored, operand A is P of the tile's
+// tokens, zero for tokens of other adapters, in 2 bf16 terms (16 significant bits).
 //   warps 0..7   epilogue: TMEM -> registers -> dX (bf16) or, where n is split over
 //                CTAs, fp32 partial sums that k_dgrad_join adds in order
 //   warps 8..15  decode
@@ -48,7 +48,6 @@ constexpr int kGABytes = 128 * kGN * 2;      // 16 KB of dY per 128 tokens and s
 constexpr int kGStageSum = 192 * 1024;       // 3 stages of 64 KB (TM = 2) or 4 of 48 KB (TM = 1)
 constexpr int kGSmem = kGStageSum + 256 + 1024;
 constexpr int kGMaxStages = 4;
-constexpr float kGTop = 1.875f;              // what alpha(0,0) becomes: exact in bf16
 
 // bf16 x bf16 -> fp32, M = 128, N = 256, A K-major, B MN-major (bit 16)
 constexpr uint32_t kGIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(kGK >> 3) << 17) |
@@ -63,25 +62,11 @@ struct GParams {
     int gran, group, spr;
     int mtiles, ktiles, splits, nstages;
     // adapters (LORA)
-    const uint16_t* A;     // bf16 [n_adapters][R][K]
-    const float* Pm;       // fp32 [M][R]
-    const int32_t* ids;
-    const int32_t* tile_n; // adapters present in each 128-token tile
-    const int32_t* tile_a; // [tiles][kLoraTile]
-    int R;
+    LoraPlan plan;
+    int rp;
+    int terms_box;  // terms of P in one tile of 64 columns: 2, or 1
+    int rows_box;   // rows of A_a per load
 };
-
-// MN-major, 128-byte swizzle: atoms of 64 elements x 8 rows (1024 B); the next 64
-// elements are kGN * 128 bytes on (leading offset), the next 8 rows 1024 (stride)
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr >> 4) & 0x3fff);
-    d |= (uint64_t)((kGN * 128) >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
 
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -93,15 +78,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
-// the unit that alpha is held in: alpha(0,0) / 1.875, or 1 where that is no ordinary number
-__device__ __forceinline__ float dgrad_unit(const float* scales) {
-    const float a = __ldg(scales);
-    return (a > 1e-30f && a < 1e30f) ? a / kGTop : 1.0f;
-}
-
 template <int TM, bool LORA>
 __global__ void __launch_bounds__(kGThreads, 1)
-k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParams P) {
+k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap ypmap,
+        const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap amap,
+        const __grid_constant__ GParams P) {
     constexpr int ST = TM == 2 ? 3 : 4;                // stages
     constexpr int SB = TM * kGABytes + kGBBytes;       // bytes per stage
     constexpr int AC = 2 / TM;                         // accumulators of TM x 256 columns in TMEM
@@ -123,11 +104,14 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
     const uint32_t drain = bar0 + 8u * (3 * ST + 4);
 
     const int items = P.mtiles * P.ktiles * P.splits;
-    // item -> token tile, k tile, stages [st0, st1) of the rows and, in the last split, the adapters' stages
+    // item -> token tile, k tile, stages [st0, st1) of the rows and, in the last split, the
+    // slots [sl0, sl1) of its one or two token tiles (from slh on those of the second)
     struct Item {
-        int mt, kt, sp, st0, st1, nl;
+        int mt, kt, sp, st0, st1, sl0, slh, sl1;
     };
-    const int rb = LORA ? (P.R + 15) / 16 : 0;
+    const int rblocks = LORA ? (P.rp + 63) / 64 : 0;
+    // stages per slot and 64 ranks: P's terms in one stage (as one tile or TM = 2 of them), or one after the other
+    const int tstages = LORA && TM == 1 && P.terms_box == 1 ? 2 : 1;
     auto item = [&](int w) {
         Item it;
         it.kt = w % P.ktiles;
@@ -136,16 +120,12 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
         it.sp = q / P.mtiles;
         it.st0 = (int)((int64_t)P.nstages * it.sp / P.splits);
         it.st1 = (int)((int64_t)P.nstages * (it.sp + 1) / P.splits);
-        it.nl = 0;
+        it.sl0 = it.slh = it.sl1 = 0;
         if constexpr (LORA) {
             if (it.sp == P.splits - 1) {
-                int slots = 0;
-#pragma unroll
-                for (int h = 0; h < TM; ++h) {
-                    const int t = it.mt * TM + h;
-                    if (t * kLoraTile < P.M) slots += __ldg(P.tile_n + t);
-                }
-                it.nl = (slots * rb * 2 + 3) / 4;
+                it.sl0 = P.plan.tile_b[it.mt * TM];
+                it.slh = it.sl1 = P.plan.tile_b[it.mt * TM + 1];
+                if (TM == 2 && it.mt * TM + 2 <= P.plan.tiles) it.sl1 = P.plan.tile_b[it.mt * TM + 2];
             }
         }
         return it;
@@ -180,6 +160,11 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
+    if constexpr (LORA) {
+        pdl_trigger();
+        pdl_wait();
+    }
+    const bool permuted = LORA && P.plan.may_permute && P.plan.head[0] != 0;
 
     if (warp < 8) {
         // ---------------- epilogue: lane = token; the two groups of four warps take the two
@@ -193,7 +178,8 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
             const Item it = item(w);
             if (!mbar_wait(acc_full(b), bph, &abort_s)) break;
             tc_fence_after();
-            const int64_t m = (int64_t)it.mt * (TM * 128) + (TM == 2 ? half * 128 : 0) + q * 32 + lane;
+            int64_t m = (int64_t)it.mt * (TM * 128) + (TM == 2 ? half * 128 : 0) + q * 32 + lane;
+            if (LORA && permuted && m < P.M) m = P.plan.perm[m];
             const int kc = it.kt * kGK + (TM == 2 ? 0 : half * COLS);
             const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kGK + half * COLS);
 #pragma unroll 1
@@ -303,68 +289,10 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
                 }
             }
             if constexpr (LORA) {
-                // adapters: four entries of 16 ranks per stage; entry = (slot, block of 16 ranks, split term)
-                int slots0 = 0, slots = 0;
-                if (it.nl > 0) {
-                    slots0 = __ldg(P.tile_n + it.mt * TM);
-                    slots = slots0;
-                    if (TM == 2 && (it.mt * TM + 1) * kLoraTile < P.M) slots += __ldg(P.tile_n + it.mt * TM + 1);
-                }
-                const int entries = slots * rb * 2;
-                auto adapter = [&](int slot) {
-                    const int t = it.mt * TM + (slot >= slots0 ? 1 : 0);
-                    return __ldg(P.tile_a + (int64_t)t * kLoraTile + (slot >= slots0 ? slot - slots0 : slot));
-                };
-                for (int ls = 0; ls < it.nl && ok; ++ls) {
-                    if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
-                    const uint32_t stage = base + (uint32_t)(s * SB);
-                    {  // operand B: row r of the stage = a rank's row of A_a, 64 of its k
-                        const int e = ls * 4 + (r >> 4), q = e >> 1;
-                        const int rr = (q % (rb > 0 ? rb : 1)) * 16 + (r & 15);
-                        const bool in = e < entries && rr < P.R;
-                        const uint16_t* src = P.A;
-                        const int k = it.kt * kGK + blk * 64;
-                        if (in) src += ((int64_t)adapter(q / rb) * P.R + rr) * P.K + k;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (in && k + 8 * c < P.K) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-                            sts128(stage + brow + (uint32_t)((c ^ (r & 7)) * 16), v);
-                        }
-                    }
-                    // operand A: a token's P for each entry, zero where the token has another adapter
-                    constexpr int EPT = TM == 2 ? 4 : 2;  // entries per thread
-                    const int row = TM == 2 ? dt : (dt & 127);
-                    const int ebase = TM == 2 ? 0 : 2 * (dt >> 7);
-                    const int64_t m = (int64_t)it.mt * (TM * 128) + row;
-                    const int my = m < P.M ? __ldg(P.ids + m) : -1;
-#pragma unroll 1
-                    for (int i = 0; i < EPT; ++i) {
-                        const int el = ebase + i, e = ls * 4 + el, q = e >> 1;
-                        uint32_t h[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) h[j] = 0u;
-                        if (e < entries && my >= 0) {
-                            const int slot = q / rb, r0 = (q % rb) * 16;
-                            if (adapter(slot) == my && (slot >= slots0) == (row >= 128)) {
-                                const float* src = P.Pm + m * P.R + r0;
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    if (r0 + 4 * j < P.R) {
-                                        const float4 f = __ldg(reinterpret_cast<const float4*>(src) + j);
-                                        h[2 * j] = split_pair(f.x * inv, f.y * inv, e & 1);
-                                        h[2 * j + 1] = split_pair(f.z * inv, f.w * inv, e & 1);
-                                    }
-                                }
-                            }
-                        }
-                        const uint32_t arow =
-                            stage + (uint32_t)((row >> 7) * kGABytes + ((row & 127) >> 3) * 1024 + (row & 7) * 128);
-                        sts128(arow + (uint32_t)(((2 * el) ^ (row & 7)) * 16), make_uint4(h[0], h[1], h[2], h[3]));
-                        sts128(arow + (uint32_t)(((2 * el + 1) ^ (row & 7)) * 16), make_uint4(h[4], h[5], h[6], h[7]));
-                    }
-                    fence_proxy_async();
-                    mbar_arrive(full_b(s));
+                // the adapters' stages take their turns without this warp, which waits for them all
+                // the same: no barrier gets two phases ahead of it
+                for (int i = (it.sl1 - it.sl0) * rblocks * tstages; i > 0 && ok; --i) {
+                    ok = mbar_wait(empty(s), ph ^ 1u, &abort_s);
                     if (++s == ST) { s = 0; ph ^= 1u; }
                 }
             }
@@ -378,19 +306,35 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
             bool ok = true;
             for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
                 const Item it = item(w);
-                for (int st = it.st0; st < it.st1 + it.nl; ++st) {
+                for (int st = it.st0; st < it.st1; ++st) {
                     if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
-                    if (st < it.st1) {
-                        mbar_expect_tx(full_a(s), TM * kGABytes);
+                    mbar_expect_tx(full_a(s), TM * kGABytes);
 #pragma unroll
-                        for (int h = 0; h < TM; ++h)
-                            tma_load_2d(base + (uint32_t)(s * SB + h * kGABytes), &ymap, st * kGN,
-                                        (it.mt * TM + h) * 128, full_a(s));
-                    } else {
-                        mbar_arrive(full_a(s));
-                    }
+                    for (int h = 0; h < TM; ++h)
+                        tma_load_2d(base + (uint32_t)(s * SB + h * kGABytes), LORA && permuted ? &ypmap : &ymap, st * kGN,
+                                    (it.mt * TM + h) * 128, full_a(s));
                     ++issued[s];
                     if (++s == ST) { s = 0; ph ^= 1u; }
+                }
+                if constexpr (LORA) {
+                    for (int sl = it.sl0; sl < it.sl1 && ok; ++sl) {
+                        const int a = P.plan.slot_a[sl];
+                        for (int u = 0; u < rblocks * tstages; ++u) {
+                            if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
+                            const int r0 = 64 * (u / tstages), t0 = u % tstages;
+                            const int boxes = 2 / (P.terms_box * tstages);
+                            const uint32_t dst = base + (uint32_t)(s * SB);
+                            mbar_expect_tx(full_a(s), (uint32_t)(boxes * kGABytes + 4 * P.rows_box * 128));
+                            for (int i = 0; i < boxes; ++i)
+                                tma_load_2d(dst + (uint32_t)(i * kGABytes), &pmap, (t0 + i) * P.rp + r0, sl * kLoraTile,
+                                            full_a(s));
+                            for (int c = 0; c < kGK / 64; ++c)
+                                tma_load_3d(dst + (uint32_t)(TM * kGABytes + c * kGN * 128), &amap, it.kt * kGK + 64 * c,
+                                            r0, a, full_a(s));
+                            ++issued[s];
+                            if (++s == ST) { s = 0; ph ^= 1u; }
+                        }
+                    }
                 }
             }
             // every load lands before the CTA's shared memory goes away
@@ -402,19 +346,21 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
         if (lane == 0) {
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 0;
+            uint32_t bmask = 0;  // phase parities of full_b per stage (the adapters' stages do not use it)
             bool ok = true;
             for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
                 const Item it = item(w);
                 if (!mbar_wait(acc_empty(b), bph ^ 1u, &abort_s)) break;
                 tc_fence_after();
-                for (int st = it.st0; st < it.st1 + it.nl; ++st) {
-                    if (!mbar_wait(full_a(s), ph, &abort_s) || !mbar_wait(full_b(s), ph, &abort_s)) {
+                for (int st = it.st0; st < it.st1; ++st) {
+                    if (!mbar_wait(full_a(s), ph, &abort_s) || !mbar_wait(full_b(s), (bmask >> s) & 1u, &abort_s)) {
                         ok = false;
                         break;
                     }
+                    bmask ^= 1u << s;
                     tc_fence_after();
                     const uint64_t da = smem_desc(base + (uint32_t)(s * SB));
-                    const uint64_t db = smem_desc_mn(base + (uint32_t)(s * SB + TM * kGABytes));
+                    const uint64_t db = smem_desc_mn(base + (uint32_t)(s * SB + TM * kGABytes), kGN * 128);
 #pragma unroll
                     for (int kk = 0; kk < kGN / 16; ++kk)  // 16 rows: +32 bytes in A's row, two 8-row atoms of B
 #pragma unroll
@@ -425,6 +371,26 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
                                         (st == it.st0 && kk == 0) ? 0u : 1u);
                     mma_commit(empty(s));
                     if (++s == ST) { s = 0; ph ^= 1u; }
+                }
+                if constexpr (LORA) {
+                    for (int sl = it.sl0; sl < it.sl1 && ok; ++sl) {
+                        const uint32_t td = tmem + (uint32_t)((TM == 2 ? (sl >= it.slh) : b) * kGK);
+                        for (int u = 0; u < rblocks * tstages; ++u) {
+                            if (!mbar_wait(full_a(s), ph, &abort_s)) { ok = false; break; }
+                            tc_fence_after();
+                            const uint64_t dp = smem_desc(base + (uint32_t)(s * SB));
+                            const uint64_t da = smem_desc_mn(base + (uint32_t)(s * SB + TM * kGABytes), kGN * 128);
+                            const int n16 = min(4, (P.rp - 64 * (u / tstages)) / 16);
+                            for (int i = 0; i < 2 / tstages; ++i) {  // the stage's terms: in one tile, or one tile each
+                                const uint64_t term = (uint64_t)(P.terms_box == 2 ? i * P.rp / 8 : (i * kGABytes) >> 4);
+                                for (int kk = 0; kk < n16; ++kk)
+                                    mma_bf16_ss(td, dp + term + (uint64_t)(2 * kk), da + (uint64_t)(2 * kk * (1024 >> 4)),
+                                                kGIdesc, 1u);
+                            }
+                            mma_commit(empty(s));
+                            if (++s == ST) { s = 0; ph ^= 1u; }
+                        }
+                    }
                 }
                 if (!ok) break;
                 mma_commit(acc_full(b));
@@ -447,6 +413,8 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ GParam
 // dX = (the splits' partial sums, in order) * unit, bf16
 __global__ void __launch_bounds__(256) k_dgrad_join(const float* part, int splits, int64_t total, const float* scales,
                                                     uint16_t* out) {
+    pdl_trigger();
+    pdl_wait();
     const float unit = dgrad_unit(scales);
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= total) return;  // total = M * K, a multiple of 32
@@ -490,8 +458,8 @@ size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int sms) {
 }
 
 int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, const float* scales, const uint16_t* dY,
-                 int64_t ldy, int64_t M, uint16_t* dX, const LoraPlan* lora, const uint16_t* A, const float* Pm,
-                 const int32_t* ids, int R, void* workspace, int sms, cudaStream_t stream) {
+                 int64_t ldy, int64_t M, uint16_t* dX, const LoraGradArgs* lora, void* workspace, int sms,
+                 cudaStream_t stream) {
     const GPlan g = dgrad_plan(M, s.N, s.K, sms);
     CUtensorMap map;
     int st = encode_2d(&map, dY, ldy, M, 128);
@@ -512,13 +480,16 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
     P.ktiles = g.ktiles;
     P.splits = g.splits;
     P.nstages = g.nstages;
+    CUtensorMap ypmap = map, pmap = map, amap = map;
     if (lora) {
-        P.A = A;
-        P.Pm = Pm;
-        P.ids = ids;
-        P.tile_n = lora->tile_n;
-        P.tile_a = lora->tile_a;
-        P.R = R;
+        P.plan = lora->plan;
+        P.rp = lora->P.rp;
+        P.terms_box = 2 * P.rp <= 64 ? 2 : 1;
+        P.rows_box = std::min(P.rp, 64);
+        if (lora->Gp && (st = encode_2d(&ypmap, lora->Gp, ldy, M, 128))) return st;
+        st = encode_2d(&pmap, lora->P.data, lora->P.terms * P.rp, (int64_t)lora->plan.max_slots * kLoraTile, 128);
+        if (!st) st = encode_3d(&amap, lora->A, s.K, lora->R, lora->n_adapters, P.rows_box);
+        if (st) return st;
     }
     static PerDevice once;
     int v = 0;
@@ -534,23 +505,13 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
     const int64_t items = (int64_t)g.mtiles * g.ktiles * g.splits;
     if (items > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)std::min<int64_t>(items, sms);
-    if (g.tm == 2) {
-        if (lora)
-            k_dgrad<2, true><<<grid, kGThreads, kGSmem, stream>>>(map, P);
-        else
-            k_dgrad<2, false><<<grid, kGThreads, kGSmem, stream>>>(map, P);
-    } else {
-        if (lora)
-            k_dgrad<1, true><<<grid, kGThreads, kGSmem, stream>>>(map, P);
-        else
-            k_dgrad<1, false><<<grid, kGThreads, kGSmem, stream>>>(map, P);
-    }
-    SHERRY_LAUNCH_CHECK();
+    auto kernel = g.tm == 2 ? (lora ? k_dgrad<2, true> : k_dgrad<2, false>) : (lora ? k_dgrad<1, true> : k_dgrad<1, false>);
+    st = launch_after(kernel, grid, kGThreads, kGSmem, stream, 1, lora != nullptr, map, ypmap, pmap, amap, P);
+    if (st) return st;
     if (g.splits > 1) {
         const int64_t total = M * s.K;
-        k_dgrad_join<<<(unsigned)((total / 4 + 255) / 256), 256, 0, stream>>>(static_cast<const float*>(workspace),
-                                                                            g.splits, total, scales, dX);
-        SHERRY_LAUNCH_CHECK();
+        return launch_after(k_dgrad_join, (unsigned)((total / 4 + 255) / 256), 256, 0, stream, 1, true,
+                            static_cast<const float*>(workspace), g.splits, total, scales, dX);
     }
     return SHERRY_OK;
 }

@@ -11,10 +11,11 @@
 // A (dX) are extra steps of the base kernels (prefill.cu, dgrad.cu).  Here are the
 // rest: the plan of tokens by adapter, the products into rank space, the product
 // out of it for few tokens, and the adapters' gradients.  U and P are fp32; where
-// one is a tensor-core operand it is split into bf16 terms whose sum is the value to
-// 16 (bf16 results) or 24 bits (fp32 results).
+// one is a tensor-core operand it is split into bf16 terms (LoraImage) whose sum is
+// the value to 16 (bf16 results) or 24 bits (fp32 results).
 #include "lora.cuh"
 #include "lut.cuh"
+#include "tc.cuh"
 
 #include <cooperative_groups.h>
 
@@ -25,276 +26,539 @@ namespace cg = cooperative_groups;
 namespace sherry {
 
 static inline int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
+static inline int64_t lora_tiles(int64_t M) { return (M + kLoraTile - 1) / kLoraTile; }
+// Slots that a call has room for.  One adapter after the other they are at most tiles + n_adapters;
+// tokens stay in place while they make no more than this: a slot too many costs each product a
+// masked pass over its tile, taking tokens in another order a copy of X or dY.
+static inline int64_t lora_max_slots(int64_t M, int n_adapters) {
+    const int64_t t = lora_tiles(M);
+    return std::min<int64_t>(2 * t + n_adapters, t * n_adapters);
+}
+
+bool lora_may_permute(int64_t M, int n_adapters) {
+    return lora_tiles(M) * n_adapters > lora_max_slots(M, n_adapters);
+}
+
+size_t lora_image_bytes(int64_t M, int n_adapters, int R, int terms) {
+    return (size_t)up256(lora_max_slots(M, n_adapters) * kLoraTile * terms * lora_rp(R) * 2);
+}
 
 size_t lora_plan_bytes(int64_t M, int n_adapters) {
-    const int64_t tiles = (M + kLoraTile - 1) / kLoraTile;
-    return (size_t)(up256(4 * M) + up256(4 * (n_adapters + 2)) + up256(4 * tiles) + up256(4 * tiles * kLoraTile));
+    const int64_t s = lora_max_slots(M, n_adapters);
+    return (size_t)(256 + up256(4 * M) + up256(4 * (lora_tiles(M) + 1)) + 3 * up256(4 * s) + up256(4 * (n_adapters + 1)) +
+                    up256(16 * s));
 }
 
 LoraPlan lora_plan_in(void* mem, int64_t M, int n_adapters) {
-    const int64_t tiles = (M + kLoraTile - 1) / kLoraTile;
+    const int64_t s = lora_max_slots(M, n_adapters);
     char* p = static_cast<char*>(mem);
+    auto take = [&](int64_t bytes) {
+        int32_t* at = reinterpret_cast<int32_t*>(p);
+        p += up256(bytes);
+        return at;
+    };
     LoraPlan plan;
-    plan.perm = reinterpret_cast<int32_t*>(p);
-    p += up256(4 * M);
-    plan.offs = reinterpret_cast<int32_t*>(p);
-    p += up256(4 * (n_adapters + 2));
-    plan.tile_n = reinterpret_cast<int32_t*>(p);
-    p += up256(4 * tiles);
-    plan.tile_a = reinterpret_cast<int32_t*>(p);
+    plan.head = take(8);
+    plan.perm = take(4 * M);
+    plan.tiles = lora_tiles(M);
+    plan.tile_b = take(4 * (plan.tiles + 1));
+    plan.slot_a = take(4 * s);
+    plan.slot_t = take(4 * s);
+    plan.adap_s = take(4 * s);
+    plan.adap_b = take(4 * (n_adapters + 1));
+    plan.mask = reinterpret_cast<uint32_t*>(take(16 * s));
+    plan.max_slots = (int)s;
+    plan.may_permute = lora_may_permute(M, n_adapters);
     return plan;
 }
 
 // ---- plan ----------------------------------------------------------------------------
-// One CTA per bucket reads all ids: the tokens of smaller buckets are its offset, its
-// own are compacted in order (ballots), so the plan depends on the ids alone.  Further
-// CTAs list the different adapters of each 128-token tile.  ids stay in L2; one launch.
+// CTA 0 lists the slots, 32 tiles at a time: a warp marks its tile's adapters in a bitmap.
+// Where the plan may permute, one further CTA per bucket (an adapter, or none) reads all
+// ids: the tokens of smaller buckets are its offset, its own are compacted in order
+// (ballots), so the order depends on the ids alone.  ids stay in L2; one launch.
 constexpr int kPlanThreads = 1024;
 
-__global__ void __launch_bounds__(kPlanThreads) k_lora_plan(const int32_t* __restrict__ ids, int M, int n_adapters,
-                                                            const LoraPlan plan) {
-    __shared__ int red[32];
-    __shared__ int tile_ids[kLoraTile];
+__device__ __forceinline__ int lora_id(const int32_t* ids, int64_t m, int n_adapters) {
+    const int a = ids[m];
+    return (a < 0 || a >= n_adapters) ? n_adapters : a;
+}
+
+// inclusive sum over the block; `ws` holds 32 ints
+__device__ __forceinline__ int block_scan(int x, int* ws) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += v;
+    }
+    __syncthreads();
+    if (lane == 31) ws[warp] = x;
+    __syncthreads();
+    const int w = lane < warp ? ws[lane] : 0;
+    return x + __reduce_add_sync(kFull, w);
+}
+
+__device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, const LoraPlan& plan) {
+    __shared__ uint32_t bits[32][32];
+    __shared__ int ws[32], cnt[SHERRY_MAX_ADAPTERS], found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if ((int)blockIdx.x > n_adapters) {
-        const int t = blockIdx.x - n_adapters - 1;
-        int a = -1;
-        if (tid < kLoraTile) {
-            const int m = t * kLoraTile + tid;
-            a = m < M ? ids[m] : -1;
-            if (a < 0 || a >= n_adapters) a = -1;
-            tile_ids[tid] = a;
+    const int tiles = (int)plan.tiles;
+    cnt[tid] = 0;
+    int total = 0;
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+        const int t = t0 + warp;
+        bits[warp][lane] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kLoraTile / 32; ++j) {
+            const int64_t m = (int64_t)t * kLoraTile + 32 * j + lane;
+            const int a = t < tiles && m < M ? lora_id(ids, m, n) : n;
+            if (a < n) atomicOr(&bits[warp][a >> 5], 1u << (a & 31));
         }
         __syncthreads();
-        bool first = a >= 0;
-        if (first)
-            for (int j = 0; j < tid; ++j)
-                if (tile_ids[j] == a) {
-                    first = false;
-                    break;
-                }
-        const unsigned mask = __ballot_sync(kFull, first);
-        if (lane == 0) red[warp] = __popc(mask);
+        uint32_t word = bits[warp][lane];
+        int sum = __popc(word);
+        const int mine = sum;
+        sum = block_scan(sum, ws);
+        int at = total + sum - mine;
+        if (lane == 0 && t < tiles) plan.tile_b[t] = at;
+        while (word) {
+            const int a = 32 * lane + __ffs(word) - 1;
+            word &= word - 1;
+            if (at < plan.max_slots) {
+                plan.slot_a[at] = a;
+                plan.slot_t[at] = t;
+            }
+            ++at;
+            atomicAdd(&cnt[a], 1);
+        }
+        const int all = __reduce_add_sync(kFull, ws[lane]);
+        total += all;
+    }
+    __syncthreads();
+    if (total <= plan.max_slots) {
+        const int c = cnt[tid], end = block_scan(c, ws);
+        cnt[tid] = end - c;
+        if (tid < n) plan.adap_b[tid] = end - c;
+        if (tid == n - 1) plan.adap_b[n] = end;
         __syncthreads();
-        int at = 0;
-        for (int w = 0; w < warp; ++w) at += red[w];
-        if (first) plan.tile_a[(int64_t)t * kLoraTile + at + __popc(mask & ((1u << lane) - 1u))] = a;
-        if (tid == 0) plan.tile_n[t] = red[0] + red[1] + red[2] + red[3];
+        for (int s = tid; s < total; s += kPlanThreads) {
+            const int a = plan.slot_a[s];
+            int before = 0;
+            for (int j = 0; j < s; ++j) before += plan.slot_a[j] == a;
+            plan.adap_s[cnt[a] + before] = s;
+        }
+        if (tid == 0) {
+            plan.head[0] = 0;
+            plan.head[1] = total;
+            plan.tile_b[tiles] = total;
+        }
         return;
     }
-    const int me = blockIdx.x;
-    int below = 0;
-    for (int m = tid; m < M; m += kPlanThreads) {
-        const int a = ids[m];
-        below += ((a < 0 || a >= n_adapters) ? n_adapters : a) < me;
+    // adapter by adapter: a tile's slots are the adapters whose tokens reach into it
+    cnt[tid] = 0;
+    __syncthreads();
+    for (int m0 = 0; m0 < M; m0 += kPlanThreads) {
+        const int m = m0 + tid;
+        const int a = m < M ? lora_id(ids, m, n) : n;
+        const unsigned same = __match_any_sync(kFull, a);
+        if (a < n && lane == __ffs(same) - 1) atomicAdd(&cnt[a], __popc(same));
     }
+    __syncthreads();
+    const int c = cnt[tid], end = block_scan(c, ws), first = end - c;
+    const int tb = first / kLoraTile, slots = c > 0 ? (end - 1) / kLoraTile - tb + 1 : 0;
+    const int send = block_scan(slots, ws);
+    for (int i = 0; i < slots; ++i) {
+        plan.slot_a[send - slots + i] = tid;
+        plan.slot_t[send - slots + i] = tb + i;
+        plan.adap_s[send - slots + i] = send - slots + i;
+    }
+    if (tid < n) plan.adap_b[tid] = send - slots;
+    if (tid == n - 1) {
+        plan.adap_b[n] = send;
+        plan.head[0] = 1;
+        plan.head[1] = send;
+        found = send;
+    }
+    __syncthreads();
+    total = found;
+    for (int t = tid; t <= tiles; t += kPlanThreads) {  // slots of smaller tiles
+        int lo = 0, hi = total;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (plan.slot_t[mid] < t)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        plan.tile_b[t] = lo;
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_lora_plan(const int32_t* ids, int M, int n_adapters,
+                                                            const LoraPlan plan) {
+    pdl_trigger();
+    if (blockIdx.x == 0) {
+        plan_slots(ids, M, n_adapters, plan);
+        return;
+    }
+    __shared__ int red[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int me = blockIdx.x - 1;
+    int below = 0;
+    for (int64_t m = tid; m < M; m += kPlanThreads) below += lora_id(ids, m, n_adapters) < me;
     below = __reduce_add_sync(kFull, below);
     if (lane == 0) red[warp] = below;
     __syncthreads();
     int at = __reduce_add_sync(kFull, red[lane]);
-    if (tid == 0) plan.offs[me] = at;
-    for (int m0 = 0; m0 < M; m0 += kPlanThreads) {
-        const int m = m0 + tid;
-        bool mine = false;
-        if (m < M) {
-            const int a = ids[m];
-            mine = ((a < 0 || a >= n_adapters) ? n_adapters : a) == me;
-        }
+    for (int64_t m0 = 0; m0 < M; m0 += kPlanThreads) {
+        const int64_t m = m0 + tid;
+        const bool mine = m < M && lora_id(ids, m, n_adapters) == me;
         const unsigned mask = __ballot_sync(kFull, mine);
         __syncthreads();
         if (lane == 0) red[warp] = __popc(mask);
         __syncthreads();
         const int c = red[lane];
         const int before = __reduce_add_sync(kFull, lane < warp ? c : 0);
-        if (mine) plan.perm[at + before + __popc(mask & ((1u << lane) - 1u))] = m;
+        if (mine) plan.perm[at + before + __popc(mask & ((1u << lane) - 1u))] = (int)m;
         at += __reduce_add_sync(kFull, c);
     }
-    if (tid == 0 && me == n_adapters) plan.offs[n_adapters + 1] = at;
 }
 
 int lora_plan_launch(const int32_t* ids, int64_t M, int n_adapters, const LoraPlan& plan, cudaStream_t stream) {
-    const int64_t tiles = (M + kLoraTile - 1) / kLoraTile;
-    k_lora_plan<<<(unsigned)(n_adapters + 1 + tiles), kPlanThreads, 0, stream>>>(ids, (int)M, n_adapters, plan);
-    SHERRY_LAUNCH_CHECK();
-    return SHERRY_OK;
+    const unsigned grid = plan.may_permute ? (unsigned)n_adapters + 2u : 1u;
+    return launch_after(k_lora_plan, grid, kPlanThreads, 0, stream, 1, false, ids, (int)M, n_adapters, plan);
+}
+
+// ---- rows in the plan's order, or with an aligned length ------------------------------
+// TMA wants rows whose bytes are a multiple of 16, and tiles whose rows stand together.
+struct RowsParams {
+    LoraRows job[2];
+    int64_t M;
+    const int32_t* head;  // null: no plan
+    const int32_t* perm;
+    int count;
+};
+
+constexpr int kRowsThreads = 1024, kRowsWide = 256;  // four rows at a time
+
+__global__ void __launch_bounds__(kRowsThreads) k_lora_rows(const RowsParams P) {
+    pdl_trigger();
+    pdl_wait();
+    const bool permuted = P.head && P.head[0] != 0;
+    constexpr int kRows = kRowsThreads / kRowsWide;
+    const int lane = threadIdx.x % kRowsWide;
+    for (int j = 0; j < P.count; ++j) {
+        const LoraRows& J = P.job[j];
+        if (!permuted && !J.always) continue;
+        for (int64_t p = blockIdx.x * kRows + threadIdx.x / kRowsWide; p < P.M; p += (int64_t)gridDim.x * kRows) {
+            const uint16_t* src = J.src + (permuted ? (int64_t)P.perm[p] : p) * J.N;
+            uint16_t* dst = J.dst + p * J.ld;
+            if (J.N == J.ld) {  // (multiples of 8)
+#pragma unroll 4
+                for (int64_t i = lane; i < J.N / 8; i += kRowsWide)
+                    reinterpret_cast<uint4*>(dst)[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            } else {
+#pragma unroll 4
+                for (int64_t i = lane; i < J.ld; i += kRowsWide) dst[i] = i < J.N ? __ldg(src + i) : (uint16_t)0;
+            }
+        }
+    }
+}
+
+int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan& plan, cudaStream_t stream) {
+    RowsParams P{};
+    P.M = M;
+    P.count = count;
+    for (int j = 0; j < count; ++j) P.job[j] = jobs[j];
+    const bool planned = plan.head && plan.may_permute;
+    P.head = planned ? plan.head : nullptr;
+    P.perm = plan.perm;
+    const unsigned grid = (unsigned)std::min<int64_t>((M + 3) / 4, 148 * 2);
+    return launch_after(k_lora_rows, grid, kRowsThreads, 0, stream, 1, plan.head != nullptr, P);
 }
 
 // ---- into rank space -----------------------------------------------------------------
-__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// A cluster per slot: the tile's 128 rows of G by the adapter's W on the tensor cores,
+// D [128 tokens][rp ranks], the sum over C split over the cluster's CTAs and joined in order
+// through distributed shared memory.  Rows of other tokens are computed along (a row of D
+// depends on its own row of G alone) and dropped at the end, where the slot's mask is made.
+// W comes by rank rows (A_a: K-major operand) or by rows of C (B_a: MN-major).  The warps
+// that end a slot are idle until then: first they make V2's image and V's zeros.
+//   warps 0..3 end a slot, warp 4 TMA, warp 5 MMA issue
+constexpr int kDnThreads = 192;
+constexpr int kDnStages = 6;
+constexpr int kDnStage = 2 * 128 * 64 * 2;  // 16 KB of G, up to 16 KB of W
+constexpr int kDnSmem = kDnStages * kDnStage + 1024;
 
 struct DownParams {
+    LoraPlan plan;
+    const int32_t* ids;
+    const float* scaling;
+    const float* unit;
+    float* V;
+    uint16_t* img;
+    const float* V2;
+    uint16_t* img2;
+    int M, C, R, rp, terms, terms2, n_adapters;
+    int by_row, product;  // product: there is a W
+};
+
+// the token at position p if it is adapter a's, else -1
+__device__ __forceinline__ int slot_token(const DownParams& P, bool permuted, int64_t p, int a) {
+    if (p >= P.M) return -1;
+    const int m = permuted ? P.plan.perm[p] : (int)p;
+    return P.ids[m] == a ? m : -1;
+}
+
+__device__ __forceinline__ void put_terms(uint16_t* row, int rp, int terms, int r, float x, float y) {
+    for (int t = 0; t < terms; ++t) *reinterpret_cast<uint32_t*>(row + t * rp + r) = split_next(x, y);
+}
+
+// 32 tokens at a time, a warp each: V's zeros for tokens of no adapter, and a quarter of a slot of V2's image
+__device__ __forceinline__ void down_side(const DownParams& P, bool permuted, int slots, int w0, int ws) {
+    const int lane = threadIdx.x & 31;
+    if (P.V)
+        for (int64_t u = w0; u * 32 < P.M; u += ws) {
+            const int64_t m = u * 32 + lane;
+            const bool none = m < P.M && lora_id(P.ids, m, P.n_adapters) == P.n_adapters;
+            for (unsigned left = __ballot_sync(kFull, none); left; left &= left - 1) {
+                float* row = P.V + (u * 32 + __ffs(left) - 1) * P.R;
+                for (int r = lane; r < P.R; r += 32) row[r] = 0.0f;
+            }
+        }
+    if (P.V2)
+        for (int u = w0; u < 4 * slots; u += ws) {
+            const int s = u >> 2, q = u & 3;
+            const int m = slot_token(P, permuted, (int64_t)P.plan.slot_t[s] * kLoraTile + 32 * q + lane, P.plan.slot_a[s]);
+            const unsigned in = __ballot_sync(kFull, m >= 0);
+            if (lane == 0) P.plan.mask[u] = in;
+            const int pairs = P.rp / 2;
+            for (int i0 = 0; i0 < 32 * pairs; i0 += 32) {  // (whole warps: pairs is a multiple of 8)
+                const int i = i0 + lane, row = i / pairs, r = 2 * (i % pairs);
+                const int mr = __shfl_sync(kFull, m, row);
+                float2 v = make_float2(0.0f, 0.0f);
+                if (mr >= 0 && r < P.R) v = *reinterpret_cast<const float2*>(P.V2 + (int64_t)mr * P.R + r);
+                put_terms(P.img2 + ((int64_t)u * 32 + row) * (P.terms2 * P.rp), P.rp, P.terms2, r, v.x, v.y);
+            }
+        }
+}
+
+__global__ void __launch_bounds__(kDnThreads, 1)
+k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap gpmap,
+            const __grid_constant__ CUtensorMap wmap, const __grid_constant__ DownParams P) {
+    extern __shared__ __align__(1024) unsigned char dsm[];
+    __shared__ uint64_t bars[2 * kDnStages + 1];
+    __shared__ uint32_t tmem_base_s;
+    __shared__ volatile int abort_s;
+    __shared__ int tok[kLoraTile];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CL = (int)cluster.num_blocks(), cr = (int)cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
+    const uint32_t bar0 = smem_u32(&bars[0]);
+    auto full = [&](int i) { return bar0 + 8u * i; };
+    auto empty = [&](int i) { return bar0 + 8u * (kDnStages + i); };
+    const uint32_t done = bar0 + 8u * (2 * kDnStages);
+    uint32_t cols = 32;
+    while ((int)cols < P.rp) cols *= 2;
+    if (tid == 0) {
+        abort_s = 0;
+        for (int i = 0; i < kDnStages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_s)),
+                     "r"(cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_trigger();
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    const bool permuted = P.plan.may_permute && P.plan.head[0] != 0;
+    const int slots = P.plan.head[1];
+    const int steps = (P.C + 63) / 64;
+    const int s0 = (int)((int64_t)steps * cr / CL), s1 = (int)((int64_t)steps * (cr + 1) / CL);
+    const int wboxes = P.by_row ? (P.rp + 63) / 64 : 1;
+    const uint32_t wbytes = P.by_row ? (uint32_t)wboxes * 64 * 128 : (uint32_t)P.rp * 128;
+    const int pitch = P.rp + 4;  // floats
+    float* sum = reinterpret_cast<float*>(dsm + (base - smem_u32(dsm)));
+    if (warp < 4 && !P.product) down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
+
+    int c = 0;  // stage and its phase, of the TMA and the MMA thread
+    uint32_t ph = 0, dph = 0;
+    int used = 0;  // loads of the TMA thread
+    for (int s = P.product ? blockIdx.x / CL : slots; s < slots; s += gridDim.x / CL) {  // (whole clusters)
+        const int a = P.plan.slot_a[s];
+        const int64_t p0 = (int64_t)P.plan.slot_t[s] * kLoraTile;
+        if (warp == 4) {
+            if (lane == 0) {
+                for (int st = s0; st < s1; ++st) {
+                    if (!mbar_wait(empty(c), ph ^ 1u, &abort_s)) break;
+                    const uint32_t dst = base + (uint32_t)c * kDnStage;
+                    mbar_expect_tx(full(c), 128 * 128 + wbytes);
+                    tma_load_2d(dst, permuted ? &gpmap : &gmap, st * 64, (int)p0, full(c));
+                    if (P.by_row) {
+                        for (int j = 0; j < wboxes; ++j)
+                            tma_load_3d(dst + 128 * 128 + (uint32_t)j * 64 * 128, &wmap, 64 * j, st * 64, a, full(c));
+                    } else {
+                        tma_load_3d(dst + 128 * 128, &wmap, st * 64, 0, a, full(c));
+                    }
+                    ++used;
+                    if (++c == kDnStages) { c = 0; ph ^= 1u; }
+                }
+                for (int i = 0; i < kDnStages && i < used; ++i)  // every load lands before shared memory is reused
+                    mbar_drain(full(i), (uint32_t)(((used - 1 - i) / kDnStages) & 1));
+            }
+            __syncwarp();
+        } else if (warp == 5) {
+            if (lane == 0) {
+                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)P.by_row << 16) |
+                                       ((uint32_t)(P.rp >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+                for (int st = s0; st < s1; ++st) {
+                    if (!mbar_wait(full(c), ph, &abort_s)) break;
+                    tc_fence_after();
+                    const uint32_t at = base + (uint32_t)c * kDnStage;
+                    const uint64_t da = smem_desc(at);
+                    const uint64_t db = P.by_row ? smem_desc_mn(at + 128 * 128, 64 * 128) : smem_desc(at + 128 * 128);
+                    const uint64_t bstep = P.by_row ? 2 * (1024 >> 4) : 2;  // 16 rows of C: two atoms, or 32 bytes
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ss(tmem, da + (uint64_t)(2 * kk), db + kk * bstep, idesc, (st == s0 && kk == 0) ? 0u : 1u);
+                    mma_commit(empty(c));
+                    if (++c == kDnStages) { c = 0; ph ^= 1u; }
+                }
+                mma_commit(done);
+                mbar_drain(done, dph);
+                dph ^= 1u;
+            }
+            __syncwarp();
+        } else {
+            tok[tid] = slot_token(P, permuted, p0 + tid, a);
+            const unsigned in = __ballot_sync(kFull, tok[tid] >= 0);
+            if (cr == 0 && lane == 0) P.plan.mask[4 * s + warp] = in;
+            if (s == (int)(blockIdx.x / CL)) down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
+        }
+        tc_fence_before();
+        __syncthreads();  // all products done, no load in flight
+        tc_fence_after();
+        if (warp < 4) {
+            float* row = sum + (warp * 32 + lane) * pitch;
+            const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
+            for (int i = 0; i < P.rp; i += 16) {
+                uint32_t v[16];
+                SHERRY_TMEM_LD16(t_row + (uint32_t)i, v);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float4 f = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                           __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                    if (s0 == s1) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    *reinterpret_cast<float4*>(row + i + 4 * j) = f;
+                }
+            }
+        }
+        tc_fence_before();
+        cluster.sync();
+        tc_fence_after();
+        const float scale = P.scaling ? P.scaling[a] : 1.0f;
+        const float inv = P.unit ? 1.0f / dgrad_unit(P.unit) : 1.0f;
+        const int pairs = P.rp / 2, i1 = kLoraTile * (cr + 1) / CL * pairs;
+        for (int i = kLoraTile * cr / CL * pairs + tid; i < i1; i += kDnThreads) {
+            const int row = i / pairs, r = 2 * (i % pairs), m = tok[row];
+            float2 v = make_float2(0.0f, 0.0f);
+            if (m >= 0) {
+                for (int q = 0; q < CL; ++q) {
+                    const float2 w = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sum, q) + row * pitch + r);
+                    v.x += w.x;
+                    v.y += w.y;
+                }
+                v.x *= scale;
+                v.y *= scale;
+                if (P.V && r < P.R) *reinterpret_cast<float2*>(P.V + (int64_t)m * P.R + r) = v;
+            }
+            if (P.img)
+                put_terms(P.img + ((int64_t)s * kLoraTile + row) * (P.terms * P.rp), P.rp, P.terms, r, v.x * inv,
+                          v.y * inv);
+        }
+        fence_proxy_async();  // the sums were read and written here; the next slot's loads come through TMA
+        cluster.sync();       // the others' partial sums are read until here
+    }
+    // clusters without a slot still have a share of the side work
+    if (P.product && warp < 4 && (int)(blockIdx.x / CL) >= slots)
+        down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
+    __syncthreads();
+    if (warp == 5)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+}
+
+int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const LoraPlan& plan, int sms,
+                     cudaStream_t stream) {
+    DownParams P{};
+    P.plan = plan;
+    P.ids = d.ids;
+    P.scaling = d.scaling;
+    P.unit = d.unit;
+    P.V = d.V;
+    P.img = d.img.data;
+    P.V2 = d.V2;
+    P.img2 = d.img2.data;
+    P.M = (int)M;
+    P.C = (int)d.C;
+    P.R = R;
+    P.rp = lora_rp(R);
+    P.terms = d.img.terms;
+    P.terms2 = d.img2.terms;
+    P.n_adapters = n_adapters;
+    P.by_row = d.by_row;
+    P.product = d.W != nullptr;
+    CUtensorMap gmap{}, gpmap{}, wmap{};
+    // slots where tokens are well placed; with more of them a cluster takes several
+    const int64_t est = std::min<int64_t>(plan.max_slots, plan.tiles + n_adapters), steps = (d.C + 63) / 64;
+    int cl = 1;
+    if (d.W) {
+        int st = encode_2d(&gmap, d.G, d.ldg, M, kLoraTile);
+        if (st) return st;
+        gpmap = gmap;
+        if (d.Gp && (st = encode_2d(&gpmap, d.Gp, d.ldg, M, kLoraTile))) return st;
+        st = d.by_row ? encode_3d(&wmap, d.W, R, d.C, n_adapters, 64) : encode_3d(&wmap, d.W, d.C, R, n_adapters, P.rp);
+        if (st) return st;
+        // the sum is split until the slots fill the SMs once
+        while (cl < 8 && est * cl * 2 <= sms && steps >= 8 * cl) cl *= 2;
+    }
+    const int64_t grid = std::min<int64_t>(est * cl, (int64_t)4 * sms / cl * cl);
+    if ((int64_t)plan.max_slots * 4 > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
+    static PerDevice once;
+    int v = 0;
+    const int st = per_device(once, &v, [](int& x) {
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_lora_down, cudaFuncAttributeMaxDynamicSharedMemorySize, kDnSmem));
+        x = 1;
+        return SHERRY_OK;
+    });
+    if (st) return st;
+    return launch_after(k_lora_down, (unsigned)grid, kDnThreads, kDnSmem, stream, cl, true, gmap, gpmap, wmap, P);
+}
+
+struct FewParams {
     const uint16_t* G;
     const uint16_t* W;
     const float* scaling;
     const int32_t* ids;
     float* V;
     int64_t ldg, ldw;
-    LoraPlan plan;
     int M, C, R, n_adapters;
 };
 
-// Bucket and token range [t0, t1) (places in perm) of tile `tile` when each bucket is cut
-// into tiles of T tokens; false past the last.  Called by whole warps.
-__device__ __forceinline__ bool bucket_tile(const LoraPlan& plan, int buckets, int T, int tile, int& bucket, int& t0,
-                                            int& t1) {
-    const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int b0 = 0; b0 < buckets; b0 += 32) {
-        const int b = b0 + lane;
-        const int lo = b < buckets ? plan.offs[b] : 0, hi = b < buckets ? plan.offs[b + 1] : 0;
-        const int n = (hi - lo + T - 1) / T;
-        int sum = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kFull, sum, o);
-            if (lane >= o) sum += v;
-        }
-        const unsigned hit = __ballot_sync(kFull, before + sum > tile);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            const int j = tile - before - __shfl_sync(kFull, sum - n, src);
-            bucket = b0 + src;
-            t0 = __shfl_sync(kFull, lo, src) + j * T;
-            t1 = min(t0 + T, __shfl_sync(kFull, hi, src));
-            return true;
-        }
-        before += __shfl_sync(kFull, sum, 31);
-    }
-    return false;
-}
-
-// 64 tokens of one adapter x R ranks; the sum over C is split over the CTAs of a cluster and
-// two halves of each CTA's warps (4 groups of 16 tokens x 2), and joined in a fixed order
-// through distributed shared memory.  mma.sync fragments are loaded from global memory as
-// they are: 16 bytes per lane are four k pairs of a row, and both operands use the same
-// order of k.
-constexpr int kDownTok = 64;
-
-template <int NT>  // 8-rank tiles
-__global__ void __launch_bounds__(256) k_lora_down(const DownParams P) {
-    cg::cluster_group cluster = cg::this_cluster();
-    const int CL = (int)cluster.num_blocks(), cr = (int)cluster.block_rank();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int group = warp & 3, half = warp >> 2;
-    __shared__ float part[kDownTok][8 * NT];
-    int bucket, t0, t1;
-    if (!bucket_tile(P.plan, P.n_adapters + 1, kDownTok, blockIdx.x / CL, bucket, t0, t1)) return;
-    const int R = P.R;
-    if (bucket == P.n_adapters) {  // tokens of no adapter
-        if (cr == 0)
-            for (int i = threadIdx.x; i < (t1 - t0) * R; i += 256)
-                P.V[(int64_t)P.plan.perm[t0 + i / R] * R + i % R] = 0.0f;
-        return;
-    }
-    const int g = lane >> 2, c = lane & 3;
-    const int ta = t0 + group * 16 + g, tb = ta + 8;
-    const uint16_t* ga = P.G + (int64_t)(ta < t1 ? P.plan.perm[ta] : 0) * P.ldg + 8 * c;
-    const uint16_t* gb = P.G + (int64_t)(tb < t1 ? P.plan.perm[tb] : 0) * P.ldg + 8 * c;
-    const bool oka = ta < t1, okb = tb < t1;
-    const uint16_t* wr = P.W + ((int64_t)bucket * R + g) * P.ldw + 8 * c;
-    const int steps = (P.C + 31) / 32;
-    const int parts = 2 * CL, mine = 2 * cr + half;
-    const int s0 = (int)((int64_t)steps * mine / parts), s1 = (int)((int64_t)steps * (mine + 1) / parts);
-    float acc[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    constexpr int UB = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    if (t0 + group * 16 < t1) {
-        for (int s = s0; s < s1; s += UB) {
-            uint4 xa[UB], xb[UB], w[UB][NT];
-#pragma unroll
-            for (int u = 0; u < UB; ++u) {
-                const int k = 32 * (s + u);
-                const bool in = s + u < s1 && k + 8 * c < P.C;
-                xa[u] = in && oka ? __ldg(reinterpret_cast<const uint4*>(ga + k)) : zero;
-                xb[u] = in && okb ? __ldg(reinterpret_cast<const uint4*>(gb + k)) : zero;
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    w[u][i] = in && 8 * i + g < R ? __ldg(reinterpret_cast<const uint4*>(wr + 8 * i * P.ldw + k)) : zero;
-            }
-#pragma unroll
-            for (int u = 0; u < UB; ++u)
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    mma16816(acc[i], xa[u].x, xb[u].x, xa[u].y, xb[u].y, w[u][i].x, w[u][i].y);
-                    mma16816(acc[i], xa[u].z, xb[u].z, xa[u].w, xb[u].w, w[u][i].z, w[u][i].w);
-                }
-        }
-    }
-    // accumulator (row g or g + 8, rank 2c or 2c + 1 of each tile): the first half's, plus the second's
-    const int r0 = group * 16 + g;
-    if (half == 1) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            *reinterpret_cast<float2*>(&part[r0][8 * i + 2 * c]) = make_float2(acc[i][0], acc[i][1]);
-            *reinterpret_cast<float2*>(&part[r0 + 8][8 * i + 2 * c]) = make_float2(acc[i][2], acc[i][3]);
-        }
-    }
-    __syncthreads();
-    if (half == 0) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            part[r0][8 * i + 2 * c] += acc[i][0];
-            part[r0][8 * i + 2 * c + 1] += acc[i][1];
-            part[r0 + 8][8 * i + 2 * c] += acc[i][2];
-            part[r0 + 8][8 * i + 2 * c + 1] += acc[i][3];
-        }
-    }
-    cluster.sync();
-    const float scale = P.scaling ? P.scaling[bucket] : 1.0f;
-    for (int i = cr * 256 + threadIdx.x; i < (t1 - t0) * R; i += 256 * CL) {
-        const int row = i / R, r = i % R;
-        float sum = 0.0f;
-        for (int q = 0; q < CL; ++q) sum += cluster.map_shared_rank(&part[0][0], q)[row * (8 * NT) + r];
-        P.V[(int64_t)P.plan.perm[t0 + row] * R + r] = scale * sum;
-    }
-    cluster.sync();  // the others' partial sums are read until here
-}
-
-template <int NT>
-static int down_launch_nt(const DownParams& P, int cl, int64_t tiles, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * cl));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)cl;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_lora_down<NT>, P));
-    return SHERRY_OK;
-}
-
-int lora_down_launch(const uint16_t* G, int64_t ldg, int64_t M, int64_t C, const uint16_t* W, int64_t ldw, int R,
-                     const int32_t* ids, const float* scaling, int n_adapters, const LoraPlan& plan, float* V, int sms,
-                     cudaStream_t stream) {
-    const DownParams P{G, W, scaling, ids, V, ldg, ldw, plan, (int)M, (int)C, R, n_adapters};
-    const int64_t full = (M + kDownTok - 1) / kDownTok;
-    const int64_t tiles = full + n_adapters + 1;  // every bucket may end inside a tile
-    const int64_t steps = (C + 31) / 32;
-    int cl = 1;
-    while (cl < 8 && full * cl < 2 * (int64_t)sms && steps >= 8 * cl) cl *= 2;
-    const int nt = R / 8;
-    if (nt <= 1) return down_launch_nt<1>(P, cl, tiles, stream);
-    if (nt <= 2) return down_launch_nt<2>(P, cl, tiles, stream);
-    if (nt <= 4) return down_launch_nt<4>(P, cl, tiles, stream);
-    if (nt <= 8) return down_launch_nt<8>(P, cl, tiles, stream);
-    return down_launch_nt<16>(P, cl, tiles, stream);
-}
-
 // Few tokens: a CTA per token and four ranks, 16-byte loads, fp32 on the CUDA cores.
-__global__ void __launch_bounds__(128) k_lora_down_few(const DownParams P) {
+__global__ void __launch_bounds__(128) k_lora_down_few(const FewParams P) {
     __shared__ float red[4][4];
     const int m = blockIdx.y, r0 = 4 * blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -337,7 +601,7 @@ __global__ void __launch_bounds__(128) k_lora_down_few(const DownParams P) {
 
 int lora_down_few_launch(const uint16_t* G, int64_t ldg, int64_t M, int64_t C, const uint16_t* W, int64_t ldw, int R,
                          const int32_t* ids, const float* scaling, int n_adapters, float* V, cudaStream_t stream) {
-    const DownParams P{G, W, scaling, ids, V, ldg, ldw, LoraPlan{}, (int)M, (int)C, R, n_adapters};
+    const FewParams P{G, W, scaling, ids, V, ldg, ldw, (int)M, (int)C, R, n_adapters};
     k_lora_down_few<<<dim3((unsigned)(R / 4), (unsigned)M), 128, 0, stream>>>(P);
     SHERRY_LAUNCH_CHECK();
     return SHERRY_OK;
@@ -385,246 +649,250 @@ int lora_up_launch(const float* Yin, int64_t M, int64_t N, const float* U, const
     return SHERRY_OK;
 }
 
-// ---- layouts ---------------------------------------------------------------------------
-// B_a [N][R] -> [R][ld]: the product dY B sums over n, which the fragments want contiguous.
-__global__ void __launch_bounds__(256) k_lora_transpose(const uint16_t* __restrict__ src, int N, int R,
-                                                        uint16_t* __restrict__ dst, int64_t ld, int nblocks) {
-    __shared__ uint16_t t[64][SHERRY_MAX_RANK + 2];
-    const int a = blockIdx.x / nblocks, n0 = (blockIdx.x % nblocks) * 64;
-    for (int i = threadIdx.x; i < 64 * R; i += 256) {
-        const int n = n0 + i / R;
-        t[i / R][i % R] = n < N ? src[((int64_t)a * N + n) * R + i % R] : (uint16_t)0;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 64 * R; i += 256) {
-        const int r = i >> 6, n = i & 63;
-        if (n0 + n < ld) dst[((int64_t)a * R + r) * ld + n0 + n] = t[n][r];
-    }
-}
-
-int lora_transpose_launch(const uint16_t* src, int n_adapters, int64_t N, int R, uint16_t* dst, int64_t ld,
-                          cudaStream_t stream) {
-    const int64_t nb = (ld + 63) / 64;
-    if (nb * n_adapters > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
-    k_lora_transpose<<<(unsigned)(nb * n_adapters), 256, 0, stream>>>(src, (int)N, R, dst, ld, (int)nb);
-    SHERRY_LAUNCH_CHECK();
-    return SHERRY_OK;
-}
-
-// Rows of an odd width, copied 16-byte aligned (TMA and the vector loads need it).
-__global__ void __launch_bounds__(256) k_lora_pad(const uint16_t* __restrict__ src, int64_t M, int64_t N,
-                                                  uint16_t* __restrict__ dst, int64_t ld) {
-    const int64_t total = M * ld;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / ld, n = i % ld;
-        dst[i] = n < N ? src[m * N + n] : (uint16_t)0;
-    }
-}
-
-int lora_pad_launch(const uint16_t* src, int64_t M, int64_t N, uint16_t* dst, int64_t ld, cudaStream_t stream) {
-    const int64_t blocks = std::min<int64_t>((M * ld + 255) / 256, 148 * 16);
-    k_lora_pad<<<(unsigned)blocks, 256, 0, stream>>>(src, M, N, dst, ld);
-    SHERRY_LAUNCH_CHECK();
-    return SHERRY_OK;
-}
-
 // ---- gradients of the adapters ---------------------------------------------------------
-// out_a[r][c] = sum over adapter a's tokens of V[m][r] G[m][c]: 128 columns per CTA, tokens in
-// chunks of 32.  G's rows are gathered by cp.async into shared memory and enter mma.sync as
-// operand B through ldmatrix.trans; V's split terms are stored transposed ([r][m]) as operand
-// A.  The tokens are split over the CTAs of a cluster, whose sums are joined in order.
-constexpr int kGradCols = 128, kGradTok = 32;
-constexpr int kGradGRow = kGradCols * 2 + 16;  // bytes per token row of G, padded for ldmatrix
-constexpr int kGradVRow = kGradTok * 2 + 16;   // bytes per rank row of V^T
+// out_a[r][c] = sum over adapter a's tokens of V[m][r] G[m][c] on the tensor cores: D [128 columns
+// of G][terms x rp], the tokens of the adapter's slots summed in stages of 64.  Both operands come
+// by TMA as they are stored and are MN-major (tokens are the rows); V is the image, so other
+// tokens' rows are zero, and in tiles that the adapter shares G's rows of other tokens are
+// zeroed too, in shared memory: an infinity there would make NaN of 0 * inf.  The terms of V
+// are columns of D side by side, added at the end.  Stages are split over the CTAs of a
+// cluster, whose sums are joined in order.
+//   warps 0..3 make the rows ready and end the tile, warp 4 TMA, warp 5 MMA issue
+constexpr int kGrThreads = 192;
+constexpr int kGrCols = 128, kGrTok = 64;
+constexpr int kGrG = kGrTok * kGrCols * 2;  // two boxes of 64 columns: 16 KB
+constexpr int kGrV = kGrTok * 64 * 2;       // each 64 columns of the image: 8 KB
+constexpr int kGrMaxStages = 6;
+constexpr int kGrExtra = 2560;              // a CTA's shared memory beside its stages: alignment, statics, the system's
 
 struct GradParams {
-    LoraGradJob job[2];
-    int cblocks[2];  // column blocks of each job
     LoraPlan plan;
-    int R, n_adapters, out_bf16;
+    void* out[2];
+    const float* unit[2];
+    int64_t C[2];
+    int by_column[2], cblocks[2];
+    int R, rp, terms, n_adapters, out_bf16;
+    int vboxes, stages;
+};
+struct GradMaps {
+    CUtensorMap g[2], gp[2], v[2];
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-    const int n = in ? 16 : 0;  // 0: zero fill, nothing read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-// RT: 16-rank tiles; SPL: split terms of V
-template <int RT, int SPL>
-__global__ void __launch_bounds__(256) k_lora_grad(const GradParams P) {
-    constexpr int kV = SPL * 16 * RT * kGradVRow, kG = kGradTok * kGradGRow;
-    constexpr int kSum = 16 * RT * kGradCols * 4;
-    constexpr int kBytes = (2 * kG + kV) > kSum ? (2 * kG + kV) : kSum;
-    extern __shared__ __align__(16) unsigned char gs[];
-    static_assert(kBytes <= 100 * 1024, "shared memory");
+__global__ void __launch_bounds__(kGrThreads)
+k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradParams P) {
+    extern __shared__ __align__(1024) unsigned char gsm[];
+    __shared__ uint64_t bars[3 * kGrMaxStages + 1];
+    __shared__ uint32_t tmem_base_s;
+    __shared__ volatile int abort_s;
     cg::cluster_group cluster = cg::this_cluster();
     const int CL = (int)cluster.num_blocks(), cr = (int)cluster.block_rank();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int b = blockIdx.x / CL;
     const int j = b >= P.cblocks[0] * P.n_adapters ? 1 : 0;
     if (j) b -= P.cblocks[0] * P.n_adapters;
-    const LoraGradJob& J = P.job[j];
-    const int a = b / P.cblocks[j], c0 = (b % P.cblocks[j]) * kGradCols;
-    const int R = P.R;
-    const int lo = P.plan.offs[a], hi = P.plan.offs[a + 1];
-    const int chunks = (hi - lo + kGradTok - 1) / kGradTok;
-    const int ch0 = (int)((int64_t)chunks * cr / CL), ch1 = (int)((int64_t)chunks * (cr + 1) / CL);
-    const uint32_t sG = smem_u32(gs), sV = sG + 2 * kG;
-    float acc[RT][2][4];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][t][e] = 0.0f;
-
-    auto load_g = [&](int ch, int buf) {
-        // 32 rows x 16 pieces of 16 bytes
-#pragma unroll
-        for (int i = 0; i < kGradTok * 16 / 256; ++i) {
-            const int p = tid + 256 * i, row = p >> 4, piece = p & 15;
-            const int t = lo + ch * kGradTok + row;
-            const bool in = t < hi && c0 + 8 * piece < J.ldg;
-            const uint16_t* src = in ? J.G + (int64_t)P.plan.perm[t] * J.ldg + c0 + 8 * piece : J.G;
-            cp_async16(sG + buf * kG + row * kGradGRow + piece * 16, src, in);
+    const int a = b / P.cblocks[j], c0 = (b % P.cblocks[j]) * kGrCols;
+    const uint32_t base = (smem_u32(gsm) + 1023u) & ~1023u;
+    const uint32_t bar0 = smem_u32(&bars[0]);
+    const int ST = P.stages, ncols = P.terms * P.rp;
+    const uint32_t SB = (uint32_t)(kGrG + P.vboxes * kGrV);
+    auto full = [&](int i) { return bar0 + 8u * i; };
+    auto ready = [&](int i) { return bar0 + 8u * (kGrMaxStages + i); };
+    auto empty = [&](int i) { return bar0 + 8u * (2 * kGrMaxStages + i); };
+    const uint32_t done = bar0 + 8u * (3 * kGrMaxStages);
+    uint32_t tcols = 32;
+    while ((int)tcols < ncols) tcols *= 2;
+    if (tid == 0) {
+        abort_s = 0;
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(ready(i), 128);
+            mbar_init(empty(i), 1);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    if (ch0 < ch1) load_g(ch0, 0);
-    for (int ch = ch0; ch < ch1; ++ch) {
-        const int buf = (ch - ch0) & 1;
-        if (ch + 1 < ch1)
-            load_g(ch + 1, buf ^ 1);
-        else
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        // V^T: thread = token pair x ranks; two tokens make one 4-byte store
-        for (int i = tid; i < (kGradTok / 2) * 16 * RT; i += 256) {
-            const int r = i % (16 * RT), t = lo + ch * kGradTok + 2 * (i / (16 * RT));
-            const float v0 = (r < R && t < hi) ? J.V[(int64_t)P.plan.perm[t] * R + r] : 0.0f;
-            const float v1 = (r < R && t + 1 < hi) ? J.V[(int64_t)P.plan.perm[t + 1] * R + r] : 0.0f;
-#pragma unroll
-            for (int s = 0; s < SPL; ++s)
-                *reinterpret_cast<uint32_t*>(gs + 2 * kG + (s * 16 * RT + r) * kGradVRow + (i / (16 * RT)) * 4) =
-                    split_pair(v0, v1, s);
-        }
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < kGradTok / 16; ++kk) {
-            // operand B: tokens 16 kk .. +16 x this warp's 16 columns; matrices (k 0-7, n 0-7), (k 8-15, n 0-7), (.., n 8-15)
-            uint32_t bf[4];
-            ldsm4t(bf, sG + buf * kG + (16 * kk + (lane & 7) + ((lane >> 3) & 1) * 8) * kGradGRow +
-                           (16 * warp + (lane >> 4) * 8) * 2);
-#pragma unroll
-            for (int s = 0; s < SPL; ++s)
-#pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    uint32_t af[4];
-                    ldsm4(af, sV + (s * 16 * RT + 16 * i + (lane & 15)) * kGradVRow + (16 * kk + (lane >> 4) * 8) * 2);
-                    mma16816(acc[i][0], af[0], af[1], af[2], af[3], bf[0], bf[1]);
-                    mma16816(acc[i][1], af[0], af[1], af[2], af[3], bf[2], bf[3]);
-                }
-        }
-        __syncthreads();
+        mbar_init(done, 1);
+        fence_mbar_init();
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_s)),
+                     "r"(tcols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_trigger();
+    pdl_wait();
+    tc_fence_before();
     __syncthreads();
-    // this CTA's sums [16 RT][128] in shared memory, then the cluster's in order
-    float* sum = reinterpret_cast<float*>(gs);
-    const int g = lane >> 2, c = lane & 3;
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    const bool permuted = P.plan.may_permute && P.plan.head[0] != 0;
+    const int32_t* list = P.plan.adap_s + P.plan.adap_b[a];
+    const int stages = 2 * (P.plan.adap_b[a + 1] - P.plan.adap_b[a]);
+    const int s0 = (int)((int64_t)stages * cr / CL), s1 = (int)((int64_t)stages * (cr + 1) / CL);
+
+    if (warp < 4) {
+        int c = 0;
+        uint32_t ph = 0;
+        for (int st = s0; st < s1; ++st) {
+            const uint32_t* mk = P.plan.mask + 4 * list[st >> 1] + 2 * (st & 1);
+            const uint32_t lo = mk[0], hi = mk[1];
+            if (!mbar_wait(full(c), ph, &abort_s)) break;
+            if ((lo & hi) != 0xffffffffu) {
+                const int row = tid & 63;
+                if (!(((row & 32) ? hi : lo) >> (row & 31) & 1u)) {
+                    const uint32_t at = base + (uint32_t)c * SB + (uint32_t)((tid >> 6) * (kGrTok * 128) + row * 128);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            float* p = sum + (16 * i + g) * kGradCols + 16 * warp + 8 * t + 2 * c;
-            *reinterpret_cast<float2*>(p) = make_float2(acc[i][t][0], acc[i][t][1]);
-            *reinterpret_cast<float2*>(p + 8 * kGradCols) = make_float2(acc[i][t][2], acc[i][t][3]);
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16u * i), "r"(0) : "memory");
+                }
+                fence_proxy_async();
+            }
+            mbar_arrive(ready(c));
+            if (++c == ST) { c = 0; ph ^= 1u; }
         }
+    } else if (warp == 4) {
+        if (lane == 0) {
+            int c = 0, n = 0;
+            uint32_t ph = 0;
+            for (int st = s0; st < s1; ++st, ++n) {
+                const int s = list[st >> 1];
+                const int row = P.plan.slot_t[s] * kLoraTile + kGrTok * (st & 1);
+                if (!mbar_wait(empty(c), ph ^ 1u, &abort_s)) break;
+                const uint32_t dst = base + (uint32_t)c * SB;
+                mbar_expect_tx(full(c), SB);
+                const CUtensorMap* gm = permuted ? &maps.gp[j] : &maps.g[j];
+                for (int q = 0; q < 2; ++q) tma_load_2d(dst + q * (kGrG / 2), gm, c0 + 64 * q, row, full(c));
+                for (int q = 0; q < P.vboxes; ++q)
+                    tma_load_2d(dst + kGrG + q * kGrV, &maps.v[j], 64 * q, s * kLoraTile + kGrTok * (st & 1), full(c));
+                if (++c == ST) { c = 0; ph ^= 1u; }
+            }
+            for (int i = 0; i < ST && i < n; ++i) mbar_drain(full(i), (uint32_t)(((n - 1 - i) / ST) & 1));
+        }
+        __syncwarp();
+    } else {
+        if (lane == 0) {
+            const int n0 = min(ncols, 256), n1 = ncols - n0;
+            const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(128 >> 4) << 24);
+            int c = 0;
+            uint32_t ph = 0;
+            for (int st = s0; st < s1; ++st) {
+                if (!mbar_wait(ready(c), ph, &abort_s)) break;
+                tc_fence_after();
+                const uint32_t at = base + (uint32_t)c * SB;
+                const uint64_t da = smem_desc_mn(at, kGrG / 2), db = smem_desc_mn(at + kGrG, kGrV);
+#pragma unroll
+                for (int kk = 0; kk < kGrTok / 16; ++kk) {  // 16 tokens: two atoms of eight rows
+                    const uint64_t step = (uint64_t)(2 * kk * (1024 >> 4));
+                    const uint32_t acc = (st == s0 && kk == 0) ? 0u : 1u;
+                    mma_bf16_ss(tmem, da + step, db + step, id | ((uint32_t)(n0 >> 3) << 17), acc);
+                    if (n1 > 0)
+                        mma_bf16_ss(tmem + 256, da + step, db + step + (uint64_t)((4 * kGrV) >> 4),
+                                    id | ((uint32_t)(n1 >> 3) << 17), acc);
+                }
+                mma_commit(empty(c));
+                if (++c == ST) { c = 0; ph ^= 1u; }
+            }
+            mma_commit(done);
+            mbar_drain(done, 0u);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();  // all products done, no load in flight
+    tc_fence_after();
+    // this CTA's sums [128 columns][rp] in shared memory, then the cluster's in order
+    const int pitch = P.rp + 1;
+    float* sum = reinterpret_cast<float*>(gsm + (base - smem_u32(gsm)));
+    if (warp < 4) {
+        float* row = sum + (warp * 32 + lane) * pitch;
+        const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
+        for (int r = 0; r < P.rp; r += 16) {
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+            if (s0 < s1) {
+                for (int t = P.terms - 1; t >= 0; --t) {  // the small terms first
+                    uint32_t v[16];
+                    SHERRY_TMEM_LD16(t_row + (uint32_t)(t * P.rp + r), v);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[i] += __uint_as_float(v[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) row[r + i] = f[i];
+        }
+    }
+    tc_fence_before();
     cluster.sync();
-    for (int i = cr * 256 + tid; i < R * kGradCols; i += 256 * CL) {
-        const int r = J.by_column ? i % R : i / kGradCols, cc = J.by_column ? i / R : i % kGradCols;
-        if (c0 + cc >= J.C) continue;
+    if (warp == 5) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tcols));
+    }
+    const int R = P.R;
+    const int64_t C = P.C[j];
+    const float unit = P.unit[j] ? dgrad_unit(P.unit[j]) : 1.0f;
+    for (int i = cr * kGrThreads + tid; i < R * kGrCols; i += kGrThreads * CL) {
+        const int r = P.by_column[j] ? i % R : i / kGrCols, cc = P.by_column[j] ? i / R : i % kGrCols;
+        if (c0 + cc >= C) continue;
         float v = 0.0f;
-        for (int q = 0; q < CL; ++q) v += cluster.map_shared_rank(sum, q)[r * kGradCols + cc];
-        const int64_t at = J.by_column ? ((int64_t)a * J.C + c0 + cc) * R + r : ((int64_t)a * R + r) * J.C + c0 + cc;
+        for (int q = 0; q < CL; ++q) v += cluster.map_shared_rank(sum, q)[cc * pitch + r];
+        v *= unit;
+        const int64_t at = P.by_column[j] ? ((int64_t)a * C + c0 + cc) * R + r : ((int64_t)a * R + r) * C + c0 + cc;
         if (P.out_bf16)
-            reinterpret_cast<__nv_bfloat16*>(J.out)[at] = __float2bfloat16_rn(v);
+            reinterpret_cast<__nv_bfloat16*>(P.out[j])[at] = __float2bfloat16_rn(v);
         else
-            reinterpret_cast<float*>(J.out)[at] = v;
+            reinterpret_cast<float*>(P.out[j])[at] = v;
     }
     cluster.sync();
-}
-
-template <int RT, int SPL>
-static int grad_launch(const GradParams& P, int64_t blocks, int cl, cudaStream_t stream) {
-    constexpr int kV = SPL * 16 * RT * kGradVRow, kG = kGradTok * kGradGRow;
-    constexpr int kSum = 16 * RT * kGradCols * 4;
-    constexpr int kBytes = (2 * kG + kV) > kSum ? (2 * kG + kV) : kSum;
-    static PerDevice once;
-    int v = 0;
-    int st = per_device(once, &v, [](int& x) {
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_lora_grad<RT, SPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
-        x = 1;
-        return SHERRY_OK;
-    });
-    if (st) return st;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(blocks * cl));
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = kBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)cl;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_lora_grad<RT, SPL>, P));
-    return SHERRY_OK;
 }
 
 int lora_grad_launch(const LoraGradJob* jobs, int count, int R, int n_adapters, int64_t M, const LoraPlan& plan,
                      int out_bf16, int sms, cudaStream_t stream) {
     GradParams P{};
+    GradMaps maps{};
     int64_t blocks = 0;
+    P.terms = jobs[0].V.terms;
+    P.rp = jobs[0].V.rp;
     for (int j = 0; j < 2; ++j) {
-        P.job[j] = jobs[j < count ? j : 0];
-        P.cblocks[j] = (int)((P.job[j].C + kGradCols - 1) / kGradCols);
+        const LoraGradJob& J = jobs[j < count ? j : 0];
+        P.out[j] = J.out;
+        P.unit[j] = J.unit;
+        P.C[j] = J.C;
+        P.by_column[j] = J.by_column;
+        P.cblocks[j] = (int)((J.C + kGrCols - 1) / kGrCols);
         if (j < count) blocks += (int64_t)P.cblocks[j] * n_adapters;
+        int st = encode_2d(&maps.g[j], J.G, J.ldg, M, kGrTok);
+        if (!st) st = encode_2d(&maps.gp[j], J.Gp ? J.Gp : J.G, J.ldg, M, kGrTok);
+        if (!st) st = encode_2d(&maps.v[j], J.V.data, P.terms * P.rp, (int64_t)plan.max_slots * kLoraTile, kGrTok);
+        if (st) return st;
     }
     P.plan = plan;
     P.R = R;
     P.n_adapters = n_adapters;
     P.out_bf16 = out_bf16;
-    // tokens split until there are CTAs enough, each with a few chunks on average
-    const int64_t chunks = M / kGradTok / n_adapters;
+    P.vboxes = (P.terms * P.rp + 63) / 64;
+    // tokens split until there are CTAs enough, each with a few stages on average
+    const int64_t avg = 2 * ((plan.tiles + n_adapters - 1) / n_adapters);
     int cl = 1;
-    while (cl < 8 && blocks * cl < 2 * (int64_t)sms && chunks >= 4 * cl) cl *= 2;
+    while (cl < 8 && blocks * cl < 2 * (int64_t)sms && avg >= 4 * cl) cl *= 2;
     if (blocks * cl > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
-    const int rt = (R + 15) / 16;
-    // bf16 gradients: two terms of V (16 bits) are 2^-8 of their rounding; fp32: all 24 bits
-    if (out_bf16) {
-        if (rt <= 1) return grad_launch<1, 2>(P, blocks, cl, stream);
-        if (rt <= 2) return grad_launch<2, 2>(P, blocks, cl, stream);
-        if (rt <= 4) return grad_launch<4, 2>(P, blocks, cl, stream);
-        return grad_launch<8, 2>(P, blocks, cl, stream);
-    }
-    if (rt <= 1) return grad_launch<1, 3>(P, blocks, cl, stream);
-    if (rt <= 2) return grad_launch<2, 3>(P, blocks, cl, stream);
-    if (rt <= 4) return grad_launch<4, 3>(P, blocks, cl, stream);
-    return grad_launch<8, 3>(P, blocks, cl, stream);
+    // as many CTAs per SM as make one wave, or as have two stages each and TMEM; the stages that fit then
+    const int SB = kGrG + P.vboxes * kGrV, smem_sm = 228 * 1024, sum = kGrCols * (P.rp + 1) * 4;
+    int tcols = 32;
+    while (tcols < P.terms * P.rp) tcols *= 2;
+    int64_t per = std::min<int64_t>((blocks * cl + sms - 1) / sms, std::min(512 / tcols, smem_sm / (2 * SB + kGrExtra)));
+    if (per < 1) per = 1;
+    P.stages = (int)std::min<int64_t>(kGrMaxStages, (smem_sm / per - kGrExtra) / SB);
+    const int smem = std::max(P.stages * SB, sum) + 1024;
+    static PerDevice once;
+    int v = 0;
+    const int st = per_device(once, &v, [](int& x) {
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_lora_grad, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024));
+        x = 1;
+        return SHERRY_OK;
+    });
+    if (st) return st;
+    return launch_after(k_lora_grad, (unsigned)(blocks * cl), kGrThreads, (size_t)smem, stream, cl, true, maps, P);
 }
+
+int lora_status_take() { return tc_status_take(); }
 
 }  // namespace sherry

@@ -83,12 +83,8 @@ struct PParams {
     int group_steps;  // K-steps per scale group (per-row: all of K)
     float lambda;     // Arenas: weight of the dense product
     // adapters (PMode::kLora)
-    const uint16_t* B;      // bf16 [n_adapters][N][R]
-    const float* U;         // fp32 [M][R]
-    const int32_t* ids;
-    const int32_t* tile_n;  // adapters present in each 128-token tile
-    const int32_t* tile_a;  // [tiles][kLoraTile]
-    int R, terms;           // rank; bf16 terms that U is split into
+    LoraPlan plan;
+    int R, rp, terms;  // rank, rounded up to 16; bf16 terms that U is split into
 };
 
 // Arenas (ARN): the same kernel also accumulates X W^T for a dense bf16 latent
@@ -98,18 +94,18 @@ struct PParams {
 // ternary A stages shrink to 2 x 2 steps so that the dense accumulator fits in
 // TMEM (columns 384..511).
 //
-// Adapters (kLora): after a tile's last K-chunk come chunks whose operand A is B_a
-// (the rank columns of the tile's weight rows, straight from its rows into TMEM) and
-// whose X slot holds U of the tile's tokens, zero for tokens of other adapters.  The
-// decode warps write both; each different adapter of the tile and each 16 ranks is
-// one K = 16 entry per bf16 term of U, four entries a step.  They form one more
-// group, with scale 1.  A tile of one adapter of rank 16 adds 3 K = 16 products to
-// K / 16, and a tile whose tokens all differ stays right, at 128 entries a term.
+// Adapters (kLora): after a tile's last K-chunk come chunks for its slots (the adapters that
+// its tokens have) and each 64 ranks: operand A is B_a's rows, operand B the terms of U, zero
+// for tokens of other adapters, all by TMA into one X slot (the terms first, then B_a).  A
+// slot is one more accumulator group with scale 1, added for its own tokens alone, so
+// that an adapter whose weights are not finite spoils no other request's tokens.
+constexpr int kPLoraB = 3 * kPStepB;  // where B_a's tile lies in the slot: after at most three terms' tiles
 enum class PMode { kPlain, kArenas, kLora };
 
 template <int EPI, PMode MODE>
 __global__ void __launch_bounds__(PRoles<EPI>::kThreads, 1)
 k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+          const __grid_constant__ CUtensorMap bmap, const __grid_constant__ CUtensorMap umap,
           const __grid_constant__ PParams P) {
     constexpr bool ARN = MODE == PMode::kArenas, LORA = MODE == PMode::kLora;
     constexpr int kPTmaWarp = PRoles<EPI>::kTmaWarp, kPMmaWarp = PRoles<EPI>::kMmaWarp;
@@ -149,11 +145,9 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     const int nchunks = (nk + CS - 1) / CS;  // the last one may hold fewer steps
     const int gs = P.group_steps;
     const int ngroups = nk / gs;
-    // LORA: K = 16 entries of tile t's adapters, and their steps of four
-    const int rb = LORA ? (P.R + 15) / 16 : 1;
-    auto lora_entries = [&](int t) -> int { return LORA ? __ldg(P.tile_n + t / ntn) * rb * P.terms : 0; };
-    auto lora_steps = [&](int t) -> int { return LORA ? (lora_entries(t) + 3) / 4 : 0; };
-
+    // LORA: chunks of 64 ranks per slot, and whether the terms of U lie in one tile's 64 columns
+    const int lblocks = LORA ? (P.rp + 63) / 64 : 0;
+    const bool one_box = LORA && P.terms * P.rp <= 64;
     if (threadIdx.x == 0) {
         abort_s = 0;
         for (int c = 0; c < XS; ++c) {
@@ -187,6 +181,12 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
+    if constexpr (LORA) pdl_wait();
+    const bool permuted = LORA && P.plan.may_permute && P.plan.head[0] != 0;
+    // the slots of tile t; every role loads them at the tile's start and uses them at its end
+    auto slots_of = [&](int t) {
+        return LORA ? make_int2(P.plan.tile_b[t / ntn], P.plan.tile_b[t / ntn + 1]) : make_int2(0, 0);
+    };
 
     if (warp < EPI) {
         // ---------------- epilogue: row n = tile row 32*(warp%4) + lane, tokens
@@ -200,6 +200,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
         for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
             const int n = (t % ntn) * kPBM + q * 32 + lane;
             const int m0 = (t / ntn) * kPBN + half * kCols;
+            const int2 sl = slots_of(t);
             const bool row_ok = n < P.N;
             const bool gsc = !P.row_scale && row_ok;
             const float* srow = P.scales + (int64_t)(row_ok ? n : 0) * P.spr;
@@ -239,7 +240,10 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] *= a;
             if constexpr (LORA) {
-                if (lora_steps(t) > 0) {
+                for (int i = sl.x; i < sl.y; ++i) {
+                    uint32_t own[kCols / 32];  // the slot's tokens among this thread's
+#pragma unroll
+                    for (int c = 0; c < kCols / 32; ++c) own[c] = P.plan.mask[4 * i + half * (kCols / 32) + c];
                     ok = mbar_wait(acc_full(b), bph, &abort_s);
                     if (!ok) break;
                     tc_fence_after();
@@ -250,12 +254,14 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                         SHERRY_TMEM_LD16(t_row + 16 * c, v);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[16 * c + j] += __uint_as_float(v[j]);
+                        for (int j = 0; j < 16; ++j)
+                            if (own[c / 2] >> (16 * (c & 1) + j) & 1u) acc[16 * c + j] += __uint_as_float(v[j]);
                     }
                     tc_fence_before();
                     mbar_arrive(acc_empty(b));
                     if (++b == kPAcc) { b = 0; bph ^= 1u; }
                 }
+                if (!ok) break;
             }
             if constexpr (ARN) {
                 // Y = the ternary sum + lambda * the dense product
@@ -278,8 +284,9 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             if (row_ok) {
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) {
-                    const int m = m0 + j;
+                    int m = m0 + j;
                     if (m < P.M) {
+                        if (LORA && permuted) m = P.plan.perm[m];
                         const float y = acc[j];
                         if (P.y_bf16)
                             reinterpret_cast<__nv_bfloat16*>(P.Y)[(int64_t)m * P.N + n] = __float2bfloat16_rn(y);
@@ -300,6 +307,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
         for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
             const int n = (t % ntn) * kPBM + i;
             const bool row_ok = n < P.N;
+            const int2 sl = slots_of(t);
             const uint32_t* idxr = P.idx + (int64_t)(row_ok ? n : 0) * P.words;
             const uint8_t* sgnr = P.sgn + (int64_t)(row_ok ? n : 0) * P.words;
             // ring of the next kPRing chunks' packed words: per step 2 idx words + 2 sign bytes
@@ -374,68 +382,11 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 }
             }
             if constexpr (LORA) {
-                // the adapters' chunks: thread i writes row i of both operands
-                const int entries = lora_entries(t), lsteps = lora_steps(t);
-                const int64_t m = (int64_t)(t / ntn) * kPBN + i;
-                const int my = m < P.M ? __ldg(P.ids + m) : -1;
-                for (int st0 = 0; st0 < lsteps && ok; st0 += CS, ++cc) {
-                    const int hbuf = cc % AB;
-                    // chunk cc - AB done: A buffer hbuf is free, and so is X slot cc % XS (XS > AB)
-                    if (cc >= AB &&
-                        !mbar_wait(chunk_empty((cc - AB) % XS), (uint32_t)(((cc - AB) / XS) & 1), &abort_s)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int e = 0; e < SPG; ++e) {
-                        const int st = SPG * g + e;
-                        if (st0 + st >= lsteps) break;
-                        uint32_t v[32];
-                        const uint32_t xrow = stX + (uint32_t)((cc % XS) * SLOTB + st * kPStepB + (i >> 3) * 1024 +
-                                                               (i & 7) * 128);
-#pragma unroll
-                        for (int el = 0; el < 4; ++el) {
-                            const int en = (st0 + st) * 4 + el, qq = en / P.terms, term = en - qq * P.terms;
-                            const int r0 = (qq % rb) * 16;
-                            const bool in = en < entries;
-                            const int a = in ? __ldg(P.tile_a + (int64_t)(t / ntn) * kLoraTile + qq / rb) : -1;
-                            uint4 b0 = make_uint4(0u, 0u, 0u, 0u), b1 = b0;
-                            if (in && row_ok) {
-                                const uint4* src =
-                                    reinterpret_cast<const uint4*>(P.B + ((int64_t)a * P.N + n) * P.R + r0);
-                                b0 = __ldg(src);
-                                if (r0 + 8 < P.R) b1 = __ldg(src + 1);
-                            }
-                            v[8 * el] = b0.x, v[8 * el + 1] = b0.y, v[8 * el + 2] = b0.z, v[8 * el + 3] = b0.w;
-                            v[8 * el + 4] = b1.x, v[8 * el + 5] = b1.y, v[8 * el + 6] = b1.z, v[8 * el + 7] = b1.w;
-                            uint32_t h[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) h[j] = 0u;
-                            if (in && a == my) {
-                                const float4* src = reinterpret_cast<const float4*>(P.U + m * P.R + r0);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    if (r0 + 4 * j < P.R) {
-                                        const float4 f = __ldg(src + j);
-                                        h[2 * j] = split_pair(f.x, f.y, term);
-                                        h[2 * j + 1] = split_pair(f.z, f.w, term);
-                                    }
-                            }
-#pragma unroll
-                            for (int hh = 0; hh < 2; ++hh)
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                 xrow + (uint32_t)(((2 * el + hh) ^ (i & 7)) * 16)),
-                                             "r"(h[4 * hh]), "r"(h[4 * hh + 1]), "r"(h[4 * hh + 2]), "r"(h[4 * hh + 3])
-                                             : "memory");
-                        }
-                        SHERRY_TMEM_ST32(t_lane + (uint32_t)((hbuf * CS + st) * kPAcols), v);
-                    }
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc_fence_before();
-                    fence_proxy_async();
-                    mbar_arrive(full_a(hbuf));
-                }
+                // the adapters' chunks use no A buffer; their turns are waited for all the same, so
+                // that no slot barrier gets two phases ahead of this thread
+                for (int left = lblocks * (sl.y - sl.x); left > 0 && ok; --left, ++cc)
+                    if (cc >= AB)
+                        ok = mbar_wait(chunk_empty((cc - AB) % XS), (uint32_t)(((cc - AB) / XS) & 1), &abort_s);
             }
         }
     } else if (warp == kPTmaWarp) {
@@ -448,6 +399,12 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
                 const int m0 = (t / ntn) * kPBN;
                 const int n0 = (t % ntn) * kPBM;
+                const int2 sl = slots_of(t);
+                int a0 = 0, a1 = 0;  // the first slots' adapters, loaded beside the K-chunks
+                if (LORA && sl.x < sl.y) {
+                    a0 = P.plan.slot_a[sl.x];
+                    a1 = P.plan.slot_a[min(sl.x + 1, sl.y - 1)];
+                }
                 for (int ch = 0; ch < nchunks; ++ch) {
                     if (!mbar_wait(chunk_empty(c), cph ^ 1u, &abort_s)) {
                         ok = false;
@@ -456,7 +413,8 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     const int steps = min(CS, nk - ch * CS);
                     mbar_expect_tx(full_x(c), (uint32_t)(steps * kPStepB * (ARN ? 2 : 1)));
                     for (int st = 0; st < steps; ++st) {
-                        tma_load_2d(stX + c * SLOTB + st * kPStepB, &xmap, (ch * CS + st) * kPBK, m0, full_x(c));
+                        tma_load_2d(stX + c * SLOTB + st * kPStepB, LORA && permuted ? &wmap : &xmap,
+                                    (ch * CS + st) * kPBK, m0, full_x(c));
                         if constexpr (ARN)
                             tma_load_2d(stX + c * SLOTB + kWOff + st * kPStepB, &wmap, (ch * CS + st) * kPBK, n0,
                                         full_x(c));
@@ -465,15 +423,22 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     if (++c == XS) { c = 0; cph ^= 1u; }
                 }
                 if constexpr (LORA) {
-                    // the decode warps fill these slots themselves
-                    for (int st0 = 0; st0 < lora_steps(t) && ok; st0 += CS) {
-                        if (!mbar_wait(chunk_empty(c), cph ^ 1u, &abort_s)) {
-                            ok = false;
-                            break;
+                    for (int i = sl.x; i < sl.y && ok; ++i) {
+                        const int a = i == sl.x ? a0 : i == sl.x + 1 ? a1 : P.plan.slot_a[i];
+                        for (int r0 = 0; r0 < P.rp; r0 += 64) {
+                            if (!mbar_wait(chunk_empty(c), cph ^ 1u, &abort_s)) {
+                                ok = false;
+                                break;
+                            }
+                            const int boxes = one_box ? 1 : P.terms;
+                            const uint32_t slot = stX + c * SLOTB;
+                            mbar_expect_tx(full_x(c), (uint32_t)((boxes + 1) * kPStepB));
+                            for (int j = 0; j < boxes; ++j)
+                                tma_load_2d(slot + j * kPStepB, &umap, j * P.rp + r0, i * kLoraTile, full_x(c));
+                            tma_load_3d(slot + kPLoraB, &bmap, r0, n0, a, full_x(c));
+                            ++issued[c];
+                            if (++c == XS) { c = 0; cph ^= 1u; }
                         }
-                        mbar_arrive(full_x(c));
-                        ++issued[c];
-                        if (++c == XS) { c = 0; cph ^= 1u; }
                     }
                 }
             }
@@ -491,6 +456,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             int cc = 0, c = 0, b = 0;
             uint32_t cph = 0, bph = 0;
             uint32_t dph = 0;  // ARN: phase parity of the dense accumulator's use
+            uint32_t aph = 0;  // phase parities of the A buffers' uses
             bool ok = true;
             // one MMA step (K = 64: four K = 16 MMAs) into accumulator b, and (ARN) the
             // dense step into the dense accumulator; returns false on a timed-out wait
@@ -529,9 +495,11 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             };
             for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
                 int gleft = gs;  // steps left in the current group
+                const int2 sl = slots_of(t);
                 for (int ch = 0; ch < nchunks; ++ch, ++cc) {
                     const int hbuf = cc % AB;
-                    if (!mbar_wait(full_a(hbuf), (uint32_t)((cc / AB) & 1), &abort_s)) { ok = false; break; }
+                    if (!mbar_wait(full_a(hbuf), (aph >> hbuf) & 1u, &abort_s)) { ok = false; break; }
+                    aph ^= 1u << hbuf;
                     if (!mbar_wait(full_x(c), cph, &abort_s)) { ok = false; break; }
                     tc_fence_after();
                     const uint64_t db0 = smem_desc(stX + c * SLOTB);
@@ -559,27 +527,20 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     if (++c == XS) { c = 0; cph ^= 1u; }
                 }
                 if constexpr (LORA) {
-                    const int lsteps = lora_steps(t);
-                    if (ok && lsteps > 0) {
-                        if (!mbar_wait(acc_empty(b), bph ^ 1u, &abort_s)) break;
+                    for (int left = sl.y - sl.x; left > 0 && ok; --left) {
+                        if (!mbar_wait(acc_empty(b), bph ^ 1u, &abort_s)) { ok = false; break; }
                         const uint32_t td = tmem + (uint32_t)(b * kPBN);
-                        for (int st0 = 0; st0 < lsteps; st0 += CS, ++cc) {
-                            const int hbuf = cc % AB;
-                            if (!mbar_wait(full_a(hbuf), (uint32_t)((cc / AB) & 1), &abort_s) ||
-                                !mbar_wait(full_x(c), cph, &abort_s)) {
-                                ok = false;
-                                break;
-                            }
+                        for (int r0 = 0; r0 < P.rp; r0 += 64, ++cc) {
+                            if (!mbar_wait(full_x(c), cph, &abort_s)) { ok = false; break; }
                             tc_fence_after();
-                            const uint64_t db0 = smem_desc(stX + c * SLOTB);
-                            const uint32_t ta0 = tmem + (uint32_t)(kPAcol + hbuf * CS * kPAcols);
-                            const int steps = min(CS, lsteps - st0);
-                            for (int st = 0; st < steps; ++st)
-#pragma unroll
-                                for (int kk = 0; kk < kPBK / 16; ++kk)
-                                    mma_bf16_ts(td, ta0 + (uint32_t)(st * kPAcols + 8 * kk),
-                                                db0 + (uint64_t)((st * kPStepB) >> 4) + (uint64_t)(2 * kk), kIdesc,
-                                                (st0 + st + kk) == 0 ? 0u : 1u);
+                            const uint64_t du = smem_desc(stX + c * SLOTB), db = smem_desc(stX + c * SLOTB + kPLoraB);
+                            const int nk16 = min(4, (P.rp - r0) / 16);
+                            for (int i = P.terms - 1; i >= 0; --i)  // the small terms first
+                                for (int kk = 0; kk < nk16; ++kk)   // 16 ranks: 32 bytes of a row
+                                    mma_bf16_ss(td, db + (uint64_t)(2 * kk),
+                                                du + (uint64_t)(one_box ? (i * P.rp) / 8 + 2 * kk
+                                                                        : ((i * kPStepB) >> 4) + 2 * kk),
+                                                kIdesc, (r0 == 0 && i == P.terms - 1 && kk == 0) ? 0u : 1u);
                             mma_commit(chunk_empty(c));
                             if (++c == XS) { c = 0; cph ^= 1u; }
                         }
@@ -622,7 +583,8 @@ static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, i
     int st = encode_2d(&map, d.X, s.K, M, kPBN);
     if (st) return st;
     if (Wd && (st = encode_2d(&wmap, Wd, s.K, s.N, kPBM))) return st;
-    if (!Wd) wmap = map;  // unused
+    if (!Wd) wmap = map;  // unused, or X in the plan's order
+    CUtensorMap bmap = map, umap = map;
     PParams P{};
     P.idx = d.idx;
     P.sgn = d.sgn;
@@ -639,13 +601,14 @@ static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, i
     P.group_steps = s.granularity == SHERRY_PER_GROUP ? s.group / kPBK : (int)(s.K / kPBK);
     P.lambda = lambda;
     if (lora) {
-        P.B = lora->B;
-        P.U = lora->U;
-        P.ids = lora->ids;
-        P.tile_n = lora->plan.tile_n;
-        P.tile_a = lora->plan.tile_a;
+        P.plan = lora->plan;
         P.R = lora->R;
-        P.terms = y_bf16 ? 2 : 3;  // 16 bits of U under a bf16 result, all 24 under an fp32 one
+        P.rp = lora->U.rp;
+        P.terms = lora->U.terms;
+        if (lora->Xp && (st = encode_2d(&wmap, lora->Xp, s.K, M, kPBN))) return st;
+        if ((st = encode_3d(&bmap, lora->B, lora->R, s.N, lora->n_adapters, kPBM))) return st;
+        if ((st = encode_2d(&umap, lora->U.data, P.rp * P.terms, (int64_t)lora->plan.max_slots * kLoraTile, kPBN)))
+            return st;
     }
     // per device: the shared-memory opt-in of every instantiation, and the SM count
     static PerDevice dev_sms;
@@ -672,19 +635,20 @@ static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, i
     const bool epi16 = s.granularity == SHERRY_PER_GROUP && s.K <= 4096;
     if (lora) {
         if (epi16)
-            k_prefill<16, PMode::kLora><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, P);
-        else
-            k_prefill<8, PMode::kLora><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            return launch_after(k_prefill<16, PMode::kLora>, grid, PRoles<16>::kThreads, kPSmem, stream, 1, true, map,
+                                wmap, bmap, umap, P);
+        return launch_after(k_prefill<8, PMode::kLora>, grid, PRoles<8>::kThreads, kPSmem, stream, 1, true, map, wmap,
+                            bmap, umap, P);
     } else if (Wd) {
         if (epi16)
-            k_prefill<16, PMode::kArenas><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            k_prefill<16, PMode::kArenas><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, bmap, umap, P);
         else
-            k_prefill<8, PMode::kArenas><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            k_prefill<8, PMode::kArenas><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, bmap, umap, P);
     } else {
         if (epi16)
-            k_prefill<16, PMode::kPlain><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            k_prefill<16, PMode::kPlain><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, bmap, umap, P);
         else
-            k_prefill<8, PMode::kPlain><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, P);
+            k_prefill<8, PMode::kPlain><<<grid, PRoles<8>::kThreads, kPSmem, stream>>>(map, wmap, bmap, umap, P);
     }
     SHERRY_LAUNCH_CHECK();
     return SHERRY_OK;
@@ -716,7 +680,8 @@ int device_status_take(cudaStream_t stream) {
     const int w = skinny_status_take();
     const int x = stream_status_take();
     const int y = dgrad_status_take();
-    return v ? v : w ? w : x ? x : y;
+    const int z = lora_status_take();
+    return v ? v : w ? w : x ? x : y ? y : z;
 }
 
 }  // namespace sherry

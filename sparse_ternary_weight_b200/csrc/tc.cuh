@@ -77,6 +77,19 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Launches that overlap their predecessor's end (launch_after): everything before pdl_wait touches
+// nothing that a kernel before it writes; after it, all of the stream's earlier work is complete.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // K-major, 128-byte swizzled operand: 8-row atoms of 1024 bytes
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
     uint64_t d = 0;
@@ -85,6 +98,18 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
     d |= (uint64_t)(1024 >> 4) << 32;             // stride byte offset: 8 rows x 128 B
     d |= (uint64_t)1 << 46;                       // descriptor version (sm_100)
     d |= (uint64_t)2 << 61;                       // SWIZZLE_128B
+    return d;
+}
+
+// MN-major, 128-byte swizzled operand (the contiguous axis is the one that is not summed over): atoms
+// of 64 elements x 8 rows (1024 B); the next 64 elements are `leading` bytes on, the next 8 rows 1024
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t leading) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3fff);
+    d |= (uint64_t)(leading >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
     return d;
 }
 
@@ -188,6 +213,50 @@ static int encode_2d(CUtensorMap* map, const void* base, int64_t inner, int64_t 
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SHERRY_OK : SHERRY_ERR_UNSUPPORTED;
+}
+
+// bf16 [slabs][rows][inner], boxes of 64 elements x box_rows rows of one slab; what lies past a slab's
+// edges reads as zero
+static int encode_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t slabs, int box_rows) {
+    EncodeTiled enc = encode_fn();
+    if (!enc) return SHERRY_ERR_UNSUPPORTED;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)slabs};
+    const cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)(inner * rows) * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SHERRY_OK : SHERRY_ERR_UNSUPPORTED;
+}
+
+// Launch `kernel` in clusters of `cluster`; with `after` it may begin while the kernel before it in the
+// stream ends (it calls pdl_wait before it touches that kernel's results).
+template <typename... Params, typename... Args>
+static int launch_after(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                        int cluster, bool after, Args&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2]{};
+    int n = 0;
+    if (cluster > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = (unsigned)cluster;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (after) {
+        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = at;
+    cfg.numAttrs = n;
+    SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...));
+    return SHERRY_OK;
 }
 
 }  // namespace sherry

@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_lora_plan(const int32_t* ids, 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int me = blockIdx.x - 1;
     int below = 0;
+#pragma unroll 8
     for (int64_t m = tid; m < M; m += kPlanThreads) below += lora_id(ids, m, n_adapters) < me;
     below = __reduce_add_sync(kFull, below);
     if (lane == 0) red[warp] = below;
@@ -288,9 +289,9 @@ int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan&
 // that end a slot are idle until then: first they make V2's image and V's zeros.
 //   warps 0..3 end a slot, warp 4 TMA, warp 5 MMA issue
 constexpr int kDnThreads = 192;
-constexpr int kDnStages = 6;
-constexpr int kDnStage = 2 * 128 * 64 * 2;  // 16 KB of G, up to 16 KB of W
-constexpr int kDnSmem = kDnStages * kDnStage + 1024;
+constexpr int kDnMaxStages = 6;
+constexpr int kDnG = 128 * 64 * 2;   // 16 KB of G a stage, then up to 16 KB of W
+constexpr int kDnHalf = 110 * 1024;  // two CTAs per SM: more clusters run at once than with one
 
 struct DownParams {
     LoraPlan plan;
@@ -303,6 +304,7 @@ struct DownParams {
     uint16_t* img2;
     int M, C, R, rp, terms, terms2, n_adapters;
     int by_row, product;  // product: there is a W
+    int stages, stage_bytes;
 };
 
 // the token at position p if it is adapter a's, else -1
@@ -312,8 +314,31 @@ __device__ __forceinline__ int slot_token(const DownParams& P, bool permuted, in
     return P.ids[m] == a ? m : -1;
 }
 
-__device__ __forceinline__ void put_terms(uint16_t* row, int rp, int terms, int r, float x, float y) {
-    for (int t = 0; t < terms; ++t) *reinterpret_cast<uint32_t*>(row + t * rp + r) = split_next(x, y);
+// eight ranks of an image row in every term
+__device__ __forceinline__ void put_terms(uint16_t* at, int rp, int terms, const float* f) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = f[i];
+    for (int t = 0; t < terms; ++t) {
+        uint4 v;
+        v.x = split_next(x[0], x[1]);
+        v.y = split_next(x[2], x[3]);
+        v.z = split_next(x[4], x[5]);
+        v.w = split_next(x[6], x[7]);
+        *reinterpret_cast<uint4*>(at + t * rp) = v;
+    }
+}
+
+// f[i] = the cluster's sums of column i of eight, in order; the columns are `stride` floats apart
+__device__ __forceinline__ void cluster_sum8(cg::cluster_group& cluster, int CL, float* at, int stride, float* f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+#pragma unroll 4
+    for (int q = 0; q < CL; ++q) {
+        const float* p = cluster.map_shared_rank(at, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] += p[i * stride];
+    }
 }
 
 // 32 tokens at a time, a warp each: V's zeros for tokens of no adapter, and a quarter of a slot of V2's image
@@ -334,38 +359,39 @@ __device__ __forceinline__ void down_side(const DownParams& P, bool permuted, in
             const int m = slot_token(P, permuted, (int64_t)P.plan.slot_t[s] * kLoraTile + 32 * q + lane, P.plan.slot_a[s]);
             const unsigned in = __ballot_sync(kFull, m >= 0);
             if (lane == 0) P.plan.mask[u] = in;
-            const int pairs = P.rp / 2;
-            for (int i0 = 0; i0 < 32 * pairs; i0 += 32) {  // (whole warps: pairs is a multiple of 8)
-                const int i = i0 + lane, row = i / pairs, r = 2 * (i % pairs);
-                const int mr = __shfl_sync(kFull, m, row);
-                float2 v = make_float2(0.0f, 0.0f);
-                if (mr >= 0 && r < P.R) v = *reinterpret_cast<const float2*>(P.V2 + (int64_t)mr * P.R + r);
-                put_terms(P.img2 + ((int64_t)u * 32 + row) * (P.terms2 * P.rp), P.rp, P.terms2, r, v.x, v.y);
+            for (int r = 0; r < P.rp; r += 8) {
+                float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                if (m >= 0 && r < P.R) {
+                    const float4* src = reinterpret_cast<const float4*>(P.V2 + (int64_t)m * P.R + r);
+                    const float4 x = src[0], y = src[1];
+                    f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+                }
+                put_terms(P.img2 + ((int64_t)u * 32 + lane) * (P.terms2 * P.rp) + r, P.rp, P.terms2, f);
             }
         }
 }
 
-__global__ void __launch_bounds__(kDnThreads, 1)
+__global__ void __launch_bounds__(kDnThreads, 2)
 k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap gpmap,
             const __grid_constant__ CUtensorMap wmap, const __grid_constant__ DownParams P) {
     extern __shared__ __align__(1024) unsigned char dsm[];
-    __shared__ uint64_t bars[2 * kDnStages + 1];
+    __shared__ uint64_t bars[2 * kDnMaxStages + 1];
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
-    __shared__ int tok[kLoraTile];
     cg::cluster_group cluster = cg::this_cluster();
     const int CL = (int)cluster.num_blocks(), cr = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_u32(&bars[0]);
     auto full = [&](int i) { return bar0 + 8u * i; };
-    auto empty = [&](int i) { return bar0 + 8u * (kDnStages + i); };
-    const uint32_t done = bar0 + 8u * (2 * kDnStages);
+    auto empty = [&](int i) { return bar0 + 8u * (kDnMaxStages + i); };
+    const uint32_t done = bar0 + 8u * (2 * kDnMaxStages);
+    const int ST = P.stages;
     uint32_t cols = 32;
     while ((int)cols < P.rp) cols *= 2;
     if (tid == 0) {
         abort_s = 0;
-        for (int i = 0; i < kDnStages; ++i) {
+        for (int i = 0; i < ST; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
         }
@@ -389,7 +415,6 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
     const int s0 = (int)((int64_t)steps * cr / CL), s1 = (int)((int64_t)steps * (cr + 1) / CL);
     const int wboxes = P.by_row ? (P.rp + 63) / 64 : 1;
     const uint32_t wbytes = P.by_row ? (uint32_t)wboxes * 64 * 128 : (uint32_t)P.rp * 128;
-    const int pitch = P.rp + 4;  // floats
     float* sum = reinterpret_cast<float*>(dsm + (base - smem_u32(dsm)));
     if (warp < 4 && !P.product) down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
 
@@ -399,24 +424,25 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
     for (int s = P.product ? blockIdx.x / CL : slots; s < slots; s += gridDim.x / CL) {  // (whole clusters)
         const int a = P.plan.slot_a[s];
         const int64_t p0 = (int64_t)P.plan.slot_t[s] * kLoraTile;
+        int m = -1;  // warps 0..3: the thread's token
         if (warp == 4) {
             if (lane == 0) {
                 for (int st = s0; st < s1; ++st) {
                     if (!mbar_wait(empty(c), ph ^ 1u, &abort_s)) break;
-                    const uint32_t dst = base + (uint32_t)c * kDnStage;
-                    mbar_expect_tx(full(c), 128 * 128 + wbytes);
+                    const uint32_t dst = base + (uint32_t)(c * P.stage_bytes);
+                    mbar_expect_tx(full(c), kDnG + wbytes);
                     tma_load_2d(dst, permuted ? &gpmap : &gmap, st * 64, (int)p0, full(c));
                     if (P.by_row) {
                         for (int j = 0; j < wboxes; ++j)
-                            tma_load_3d(dst + 128 * 128 + (uint32_t)j * 64 * 128, &wmap, 64 * j, st * 64, a, full(c));
+                            tma_load_3d(dst + kDnG + (uint32_t)j * 64 * 128, &wmap, 64 * j, st * 64, a, full(c));
                     } else {
-                        tma_load_3d(dst + 128 * 128, &wmap, st * 64, 0, a, full(c));
+                        tma_load_3d(dst + kDnG, &wmap, st * 64, 0, a, full(c));
                     }
                     ++used;
-                    if (++c == kDnStages) { c = 0; ph ^= 1u; }
+                    if (++c == ST) { c = 0; ph ^= 1u; }
                 }
-                for (int i = 0; i < kDnStages && i < used; ++i)  // every load lands before shared memory is reused
-                    mbar_drain(full(i), (uint32_t)(((used - 1 - i) / kDnStages) & 1));
+                for (int i = 0; i < ST && i < used; ++i)  // every load lands before shared memory is reused
+                    mbar_drain(full(i), (uint32_t)(((used - 1 - i) / ST) & 1));
             }
             __syncwarp();
         } else if (warp == 5) {
@@ -426,15 +452,15 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
                 for (int st = s0; st < s1; ++st) {
                     if (!mbar_wait(full(c), ph, &abort_s)) break;
                     tc_fence_after();
-                    const uint32_t at = base + (uint32_t)c * kDnStage;
+                    const uint32_t at = base + (uint32_t)(c * P.stage_bytes);
                     const uint64_t da = smem_desc(at);
-                    const uint64_t db = P.by_row ? smem_desc_mn(at + 128 * 128, 64 * 128) : smem_desc(at + 128 * 128);
+                    const uint64_t db = P.by_row ? smem_desc_mn(at + kDnG, 64 * 128) : smem_desc(at + kDnG);
                     const uint64_t bstep = P.by_row ? 2 * (1024 >> 4) : 2;  // 16 rows of C: two atoms, or 32 bytes
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_bf16_ss(tmem, da + (uint64_t)(2 * kk), db + kk * bstep, idesc, (st == s0 && kk == 0) ? 0u : 1u);
                     mma_commit(empty(c));
-                    if (++c == kDnStages) { c = 0; ph ^= 1u; }
+                    if (++c == ST) { c = 0; ph ^= 1u; }
                 }
                 mma_commit(done);
                 mbar_drain(done, dph);
@@ -442,55 +468,62 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
             }
             __syncwarp();
         } else {
-            tok[tid] = slot_token(P, permuted, p0 + tid, a);
-            const unsigned in = __ballot_sync(kFull, tok[tid] >= 0);
+            m = slot_token(P, permuted, p0 + tid, a);
+            const unsigned in = __ballot_sync(kFull, m >= 0);
             if (cr == 0 && lane == 0) P.plan.mask[4 * s + warp] = in;
             if (s == (int)(blockIdx.x / CL)) down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
         }
         tc_fence_before();
         __syncthreads();  // all products done, no load in flight
         tc_fence_after();
-        if (warp < 4) {
-            float* row = sum + (warp * 32 + lane) * pitch;
-            const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
-            for (int i = 0; i < P.rp; i += 16) {
-                uint32_t v[16];
-                SHERRY_TMEM_LD16(t_row + (uint32_t)i, v);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        // lane = token: eight ranks at a time, straight from TMEM or as [rank][token] for the cluster
+        const float scale = P.scaling ? P.scaling[a] : 1.0f;
+        const float inv = P.unit ? 1.0f / dgrad_unit(P.unit) : 1.0f;
+        auto put = [&](int r, float* f) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float4 f = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                           __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-                    if (s0 == s1) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    *reinterpret_cast<float4*>(row + i + 4 * j) = f;
+            for (int i = 0; i < 8; ++i) f[i] = m >= 0 ? f[i] * scale : 0.0f;
+            if (P.V && m >= 0 && r < P.R) {
+                float4* dst = reinterpret_cast<float4*>(P.V + (int64_t)m * P.R + r);
+                dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+            if (P.img) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] *= inv;
+                put_terms(P.img + ((int64_t)s * kLoraTile + tid) * (P.terms * P.rp) + r, P.rp, P.terms, f);
+            }
+        };
+        if (warp < 4) {
+            const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
+            for (int r = 0; r < P.rp; r += 16) {
+                uint32_t v[16];
+                SHERRY_TMEM_LD16(t_row + (uint32_t)r, v);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                float f[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = s0 < s1 ? __uint_as_float(v[i]) : 0.0f;
+                if (CL == 1) {
+                    put(r, f);
+                    put(r + 8, f + 8);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[(r + i) * kLoraTile + tid] = f[i];
                 }
             }
         }
         tc_fence_before();
         cluster.sync();
         tc_fence_after();
-        const float scale = P.scaling ? P.scaling[a] : 1.0f;
-        const float inv = P.unit ? 1.0f / dgrad_unit(P.unit) : 1.0f;
-        const int pairs = P.rp / 2, i1 = kLoraTile * (cr + 1) / CL * pairs;
-        for (int i = kLoraTile * cr / CL * pairs + tid; i < i1; i += kDnThreads) {
-            const int row = i / pairs, r = 2 * (i % pairs), m = tok[row];
-            float2 v = make_float2(0.0f, 0.0f);
-            if (m >= 0) {
-                for (int q = 0; q < CL; ++q) {
-                    const float2 w = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sum, q) + row * pitch + r);
-                    v.x += w.x;
-                    v.y += w.y;
+        if (CL > 1) {
+            if (warp < 4)
+                for (int r = 8 * cr; r < P.rp; r += 8 * CL) {
+                    float f[8];
+                    cluster_sum8(cluster, CL, sum + r * kLoraTile + tid, kLoraTile, f);
+                    put(r, f);
                 }
-                v.x *= scale;
-                v.y *= scale;
-                if (P.V && r < P.R) *reinterpret_cast<float2*>(P.V + (int64_t)m * P.R + r) = v;
-            }
-            if (P.img)
-                put_terms(P.img + ((int64_t)s * kLoraTile + row) * (P.terms * P.rp), P.rp, P.terms, r, v.x * inv,
-                          v.y * inv);
+            fence_proxy_async();  // the sums were read and written here; the next slot's loads come through TMA
+            cluster.sync();       // the others' partial sums are read until here
         }
-        fence_proxy_async();  // the sums were read and written here; the next slot's loads come through TMA
-        cluster.sync();       // the others' partial sums are read until here
     }
     // clusters without a slot still have a share of the side work
     if (P.product && warp < 4 && (int)(blockIdx.x / CL) >= slots)
@@ -534,17 +567,20 @@ int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const 
         // the sum is split until the slots fill the SMs once
         while (cl < 8 && est * cl * 2 <= sms && steps >= 8 * cl) cl *= 2;
     }
+    P.stage_bytes = kDnG + (d.by_row ? (P.rp + 63) / 64 * 64 * 128 : (P.rp * 128 + 1023) / 1024 * 1024);
+    P.stages = std::min(kDnMaxStages, (kDnHalf - 2048) / P.stage_bytes);
+    const int smem = std::max(P.stages * P.stage_bytes, P.rp * kLoraTile * 4) + 1024;
     const int64_t grid = std::min<int64_t>(est * cl, (int64_t)4 * sms / cl * cl);
     if ((int64_t)plan.max_slots * 4 > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     static PerDevice once;
     int v = 0;
     const int st = per_device(once, &v, [](int& x) {
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_lora_down, cudaFuncAttributeMaxDynamicSharedMemorySize, kDnSmem));
+        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_lora_down, cudaFuncAttributeMaxDynamicSharedMemorySize, kDnHalf));
         x = 1;
         return SHERRY_OK;
     });
     if (st) return st;
-    return launch_after(k_lora_down, (unsigned)grid, kDnThreads, kDnSmem, stream, cl, true, gmap, gpmap, wmap, P);
+    return launch_after(k_lora_down, (unsigned)grid, kDnThreads, (size_t)smem, stream, cl, true, gmap, gpmap, wmap, P);
 }
 
 struct FewParams {
@@ -663,7 +699,8 @@ constexpr int kGrCols = 128, kGrTok = 64;
 constexpr int kGrG = kGrTok * kGrCols * 2;  // two boxes of 64 columns: 16 KB
 constexpr int kGrV = kGrTok * 64 * 2;       // each 64 columns of the image: 8 KB
 constexpr int kGrMaxStages = 6;
-constexpr int kGrExtra = 2560;              // a CTA's shared memory beside its stages: alignment, statics, the system's
+constexpr int kGrHeld = 32;                 // slots whose table a CTA holds in shared memory
+constexpr int kGrExtra = 3328;              // a CTA's shared memory beside its stages: alignment, statics, the system's
 
 struct GradParams {
     LoraPlan plan;
@@ -682,6 +719,8 @@ __global__ void __launch_bounds__(kGrThreads)
 k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradParams P) {
     extern __shared__ __align__(1024) unsigned char gsm[];
     __shared__ uint64_t bars[3 * kGrMaxStages + 1];
+    __shared__ int2 held[kGrHeld];
+    __shared__ uint4 held_mask[kGrHeld];
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
     cg::cluster_group cluster = cg::this_cluster();
@@ -723,16 +762,31 @@ k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradP
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
     const bool permuted = P.plan.may_permute && P.plan.head[0] != 0;
-    const int32_t* list = P.plan.adap_s + P.plan.adap_b[a];
-    const int stages = 2 * (P.plan.adap_b[a + 1] - P.plan.adap_b[a]);
+    const int first = P.plan.adap_b[a], stages = 2 * (P.plan.adap_b[a + 1] - first);
+    const int32_t* list = P.plan.adap_s + first;
     const int s0 = (int)((int64_t)stages * cr / CL), s1 = (int)((int64_t)stages * (cr + 1) / CL);
+    // the first slots of this CTA's stages, their tiles and masks: loaded at once, not stage by stage
+    const int held0 = s0 >> 1, held1 = min(held0 + kGrHeld, (s1 + 1) >> 1);
+    if (tid < held1 - held0) {
+        const int s = list[held0 + tid];
+        held[tid] = make_int2(s, P.plan.slot_t[s]);
+        held_mask[tid] = *reinterpret_cast<const uint4*>(P.plan.mask + 4 * s);
+    }
+    __syncthreads();
+    auto slot_of = [&](int i) {
+        if (i < held1) return held[i - held0];
+        const int s = list[i];
+        return make_int2(s, P.plan.slot_t[s]);
+    };
 
     if (warp < 4) {
         int c = 0;
         uint32_t ph = 0;
         for (int st = s0; st < s1; ++st) {
-            const uint32_t* mk = P.plan.mask + 4 * list[st >> 1] + 2 * (st & 1);
-            const uint32_t lo = mk[0], hi = mk[1];
+            const int i = st >> 1;
+            const uint4 mk = i < held1 ? held_mask[i - held0]
+                                       : *reinterpret_cast<const uint4*>(P.plan.mask + 4 * list[i]);
+            const uint32_t lo = (st & 1) ? mk.z : mk.x, hi = (st & 1) ? mk.w : mk.y;
             if (!mbar_wait(full(c), ph, &abort_s)) break;
             if ((lo & hi) != 0xffffffffu) {
                 const int row = tid & 63;
@@ -752,8 +806,8 @@ k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradP
             int c = 0, n = 0;
             uint32_t ph = 0;
             for (int st = s0; st < s1; ++st, ++n) {
-                const int s = list[st >> 1];
-                const int row = P.plan.slot_t[s] * kLoraTile + kGrTok * (st & 1);
+                const int2 sl = slot_of(st >> 1);
+                const int s = sl.x, row = sl.y * kLoraTile + kGrTok * (st & 1);
                 if (!mbar_wait(empty(c), ph ^ 1u, &abort_s)) break;
                 const uint32_t dst = base + (uint32_t)c * SB;
                 mbar_expect_tx(full(c), SB);
@@ -797,11 +851,42 @@ k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradP
     tc_fence_before();
     __syncthreads();  // all products done, no load in flight
     tc_fence_after();
-    // this CTA's sums [128 columns][rp] in shared memory, then the cluster's in order
-    const int pitch = P.rp + 1;
+    // lane = column: eight ranks at a time, straight from TMEM or as [rank][column] for the cluster
+    const int R = P.R;
+    const int64_t C = P.C[j], cc = c0 + tid;
+    const float unit = P.unit[j] ? dgrad_unit(P.unit[j]) : 1.0f;
     float* sum = reinterpret_cast<float*>(gsm + (base - smem_u32(gsm)));
+    auto put = [&](int r, float* f) {
+        if (cc >= C || r >= R) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= unit;
+        if (P.by_column[j]) {
+            const int64_t at = ((int64_t)a * C + cc) * R + r;
+            if (P.out_bf16) {
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                    h[i] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(P.out[j]) + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+                float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(P.out[j]) + at);
+                dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+        } else {
+            const int64_t at = ((int64_t)a * R + r) * C + cc;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (P.out_bf16)
+                    reinterpret_cast<__nv_bfloat16*>(P.out[j])[at + i * C] = __float2bfloat16_rn(f[i]);
+                else
+                    reinterpret_cast<float*>(P.out[j])[at + i * C] = f[i];
+            }
+        }
+    };
     if (warp < 4) {
-        float* row = sum + (warp * 32 + lane) * pitch;
         const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
         for (int r = 0; r < P.rp; r += 16) {
             float f[16];
@@ -816,8 +901,13 @@ k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradP
                     for (int i = 0; i < 16; ++i) f[i] += __uint_as_float(v[i]);
                 }
             }
+            if (CL == 1) {
+                put(r, f);
+                put(r + 8, f + 8);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) row[r + i] = f[i];
+                for (int i = 0; i < 16; ++i) sum[(r + i) * kGrCols + tid] = f[i];
+            }
         }
     }
     tc_fence_before();
@@ -826,22 +916,15 @@ k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradP
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tcols));
     }
-    const int R = P.R;
-    const int64_t C = P.C[j];
-    const float unit = P.unit[j] ? dgrad_unit(P.unit[j]) : 1.0f;
-    for (int i = cr * kGrThreads + tid; i < R * kGrCols; i += kGrThreads * CL) {
-        const int r = P.by_column[j] ? i % R : i / kGrCols, cc = P.by_column[j] ? i / R : i % kGrCols;
-        if (c0 + cc >= C) continue;
-        float v = 0.0f;
-        for (int q = 0; q < CL; ++q) v += cluster.map_shared_rank(sum, q)[cc * pitch + r];
-        v *= unit;
-        const int64_t at = P.by_column[j] ? ((int64_t)a * C + c0 + cc) * R + r : ((int64_t)a * R + r) * C + c0 + cc;
-        if (P.out_bf16)
-            reinterpret_cast<__nv_bfloat16*>(P.out[j])[at] = __float2bfloat16_rn(v);
-        else
-            reinterpret_cast<float*>(P.out[j])[at] = v;
+    if (CL > 1) {
+        if (warp < 4)
+            for (int r = 8 * cr; r < R; r += 8 * CL) {
+                float f[8];
+                cluster_sum8(cluster, CL, sum + r * kGrCols + tid, kGrCols, f);
+                put(r, f);
+            }
+        cluster.sync();  // the others' partial sums are read until here
     }
-    cluster.sync();
 }
 
 int lora_grad_launch(const LoraGradJob* jobs, int count, int R, int n_adapters, int64_t M, const LoraPlan& plan,
@@ -875,7 +958,7 @@ int lora_grad_launch(const LoraGradJob* jobs, int count, int R, int n_adapters, 
     while (cl < 8 && blocks * cl < 2 * (int64_t)sms && avg >= 4 * cl) cl *= 2;
     if (blocks * cl > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     // as many CTAs per SM as make one wave, or as have two stages each and TMEM; the stages that fit then
-    const int SB = kGrG + P.vboxes * kGrV, smem_sm = 228 * 1024, sum = kGrCols * (P.rp + 1) * 4;
+    const int SB = kGrG + P.vboxes * kGrV, smem_sm = 228 * 1024, sum = kGrCols * P.rp * 4;
     int tcols = 32;
     while (tcols < P.terms * P.rp) tcols *= 2;
     int64_t per = std::min<int64_t>((blocks * cl + sms - 1) / sms, std::min(512 / tcols, smem_sm / (2 * SB + kGrExtra)));

@@ -201,6 +201,10 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             const int n = (t % ntn) * kPBM + q * 32 + lane;
             const int m0 = (t / ntn) * kPBN + half * kCols;
             const int2 sl = slots_of(t);
+            uint32_t own0[kCols / 32];  // the first slot's tokens among this thread's
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c)
+                own0[c] = LORA && sl.x < sl.y ? P.plan.mask[4 * sl.x + half * (kCols / 32) + c] : 0u;
             const bool row_ok = n < P.N;
             const bool gsc = !P.row_scale && row_ok;
             const float* srow = P.scales + (int64_t)(row_ok ? n : 0) * P.spr;
@@ -241,9 +245,10 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             for (int j = 0; j < kCols; ++j) acc[j] *= a;
             if constexpr (LORA) {
                 for (int i = sl.x; i < sl.y; ++i) {
-                    uint32_t own[kCols / 32];  // the slot's tokens among this thread's
+                    uint32_t own[kCols / 32];
 #pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c) own[c] = P.plan.mask[4 * i + half * (kCols / 32) + c];
+                    for (int c = 0; c < kCols / 32; ++c)
+                        own[c] = i == sl.x ? own0[c] : P.plan.mask[4 * i + half * (kCols / 32) + c];
                     ok = mbar_wait(acc_full(b), bph, &abort_s);
                     if (!ok) break;
                     tc_fence_after();
@@ -281,12 +286,22 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 mbar_arrive(dense_empty);
                 dph ^= 1u;
             }
-            if (row_ok) {
+            if (row_ok && LORA && permuted) {
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) {
-                    int m = m0 + j;
+                    if (m0 + j < P.M) {
+                        const int64_t at = (int64_t)P.plan.perm[m0 + j] * P.N + n;
+                        if (P.y_bf16)
+                            reinterpret_cast<__nv_bfloat16*>(P.Y)[at] = __float2bfloat16_rn(acc[j]);
+                        else
+                            reinterpret_cast<float*>(P.Y)[at] = acc[j];
+                    }
+                }
+            } else if (row_ok) {
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    const int m = m0 + j;
                     if (m < P.M) {
-                        if (LORA && permuted) m = P.plan.perm[m];
                         const float y = acc[j];
                         if (P.y_bf16)
                             reinterpret_cast<__nv_bfloat16*>(P.Y)[(int64_t)m * P.N + n] = __float2bfloat16_rn(y);

@@ -9,6 +9,7 @@ missing or the tensors are not on a CUDA device, the calls raise.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 from . import _abi
@@ -31,8 +32,20 @@ def _ptr(t) -> int | None:
 
 
 def _stream(device=None) -> int:
+    """Handle of the current stream of ``device`` (as torch.cuda.current_stream, without
+    the object around it, which costs more than a launch's arguments)."""
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    index = None if device is None else device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+
+
+_NO_GUARD = nullcontext()
+
+
+def _on(device):
+    """A guard that makes ``device`` current; nothing where it is."""
+    import torch
+    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _require_cuda(*ts):
@@ -453,7 +466,7 @@ def _stream_workspace(nbytes: int, device) -> "object":
     import torch
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    key = (str(device), "linear", _stream(device))
+    key = (device, "linear", _stream(device))
     seen = lib().sherry_timeout_count()
     if seen != _ws_timeouts[0]:
         _ws_cache.clear()
@@ -534,7 +547,7 @@ def linear_lora(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None, out
     U = torch.empty((M, R), dtype=torch.float32, device=X.device) if return_u else None
     if return_u and P.N == 0:
         U.zero_()
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         L = lib()
         wsb = L.sherry_linear_lora_workspace_bytes(M, P.N, P.K, P.granularity, P.group, n, R, yd)
         ws = _stream_workspace(wsb, X.device) if wsb else None
@@ -551,7 +564,7 @@ def linear_backward(dY, P: PackedWeight, out=None):
     _same_device(dY.device, P.idx)
     M = dY.shape[0]
     out = _result(out, (M, P.K), torch.bfloat16, dY.device)
-    with torch.cuda.device(dY.device):
+    with _on(dY.device):
         L = lib()
         wsb = L.sherry_linear_backward_workspace_bytes(M, P.N, P.K)
         ws = _scratch(wsb, dY.device)
@@ -582,9 +595,9 @@ def linear_lora_backward(dY, X, P: PackedWeight, A, B, ids, U, scaling=None, gra
     grad_dtype = grad_dtype or torch.bfloat16
     gd = {torch.float32: F32, torch.bfloat16: BF16}[grad_dtype]
     dX = torch.empty_like(X) if need[0] else None
-    dA = torch.empty(A.shape, dtype=grad_dtype, device=X.device) if need[1] else None
-    dB = torch.empty(B.shape, dtype=grad_dtype, device=X.device) if need[2] else None
-    with torch.cuda.device(X.device):
+    dA = torch.empty_like(A, dtype=grad_dtype) if need[1] else None
+    dB = torch.empty_like(B, dtype=grad_dtype) if need[2] else None
+    with _on(X.device):
         L = lib()
         wsb = L.sherry_linear_lora_backward_workspace_bytes(M, P.N, P.K, n, R)
         ws = _scratch(wsb, X.device)
@@ -692,9 +705,10 @@ def _scores(M, V, targets, top, device):
     import torch
     if not 0 <= top <= min(V, _abi.MAX_TOP):
         raise ValueError(f"top must be 0 to min(V, {_abi.MAX_TOP})")
-    f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)  # noqa: E731
-    return TokenLogprobs(f32(M) if targets is not None else None, f32(M), f32(M, 2), f32(M, top) if top else None,
-                         torch.empty((M, top), dtype=torch.int32, device=device) if top else None)
+    entropy = torch.empty(M, dtype=torch.float32, device=device)  # the others from it: cheaper than anew
+    top_logp = entropy.new_empty((M, top)) if top else None
+    return TokenLogprobs(torch.empty_like(entropy) if targets is not None else None, entropy, entropy.new_empty((M, 2)),
+                         top_logp, torch.empty_like(top_logp, dtype=torch.int32) if top else None)
 
 
 def token_logprobs(logits, targets=None, top: int = 0) -> TokenLogprobs:
@@ -708,7 +722,7 @@ def token_logprobs(logits, targets=None, top: int = 0) -> TokenLogprobs:
     M, V = z.shape
     targets = _targets(targets, M, V, z.device)
     r = _scores(M, V, targets, top, z.device)
-    with torch.cuda.device(z.device):
+    with _on(z.device):
         check(lib().sherry_token_logprobs(_ptr(z), dt, M, V, ld, _ptr(targets), top, _ptr(r.logp), _ptr(r.entropy),
                                           _ptr(r.stats), _ptr(r.top_logp), _ptr(r.top_ids), _stream(z.device)),
               "token_logprobs")
@@ -735,14 +749,14 @@ def token_logprobs_backward(logits, targets, stats, entropy, dlogp=None, dentrop
     if stats is None or (dentropy is not None and entropy is None) or (dlogp is not None and targets is None):
         raise ValueError("needs stats, targets with dlogp, and entropy with dentropy")
     if out is None:
-        out = torch.empty((M, V), dtype=z.dtype, device=z.device)
+        out = z.new_empty((M, V))
     elif (out.dtype != z.dtype or tuple(out.shape) != (M, V) or (V > 1 and out.stride(1) != 1)
           or (M > 1 and out.stride(0) < V)):
         raise ValueError("out must be [M, V] of the logits' type with rows of unit stride")
     elif M > 0 and _spans_overlap(z, out) and not (out.data_ptr() == z.data_ptr() and (M == 1 or out.stride(0) == ld)):
         raise ValueError("out must be the logits themselves or not overlap them")
     ldd = out.stride(0) if M > 1 else V
-    with torch.cuda.device(z.device):
+    with _on(z.device):
         check(lib().sherry_token_logprobs_backward(_ptr(z), dt, M, V, ld, _ptr(targets), _ptr(stats), _ptr(entropy),
                                                    _ptr(dlogp), _ptr(dentropy), _ptr(out), ldd, _stream(z.device)),
               "token_logprobs_backward")
@@ -805,7 +819,7 @@ def linear_logprobs(X, P: PackedWeight, targets=None, top: int = 0) -> TokenLogp
         raise ValueError(f"a head has 1 to {_abi.MAX_VOCAB} rows")
     targets = _targets(targets, M, P.N, X.device)
     r = _scores(M, P.N, targets, top, X.device)
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         L = lib()
         wsb = L.sherry_linear_logprobs_workspace_bytes(M, P.N, P.K, P.granularity, P.group)
         ws = _stream_workspace(wsb, X.device) if wsb else None

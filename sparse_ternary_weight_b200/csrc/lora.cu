@@ -78,6 +78,7 @@ LoraPlan lora_plan_in(void* mem, int64_t M, int n_adapters) {
 // ids: the tokens of smaller buckets are its offset, its own are compacted in order
 // (ballots), so the order depends on the ids alone.  ids stay in L2; one launch.
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanHeld = 2048;
 
 __device__ __forceinline__ int lora_id(const int32_t* ids, int64_t m, int n_adapters) {
     const int a = ids[m];
@@ -102,6 +103,7 @@ __device__ __forceinline__ int block_scan(int x, int* ws) {
 __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, const LoraPlan& plan) {
     __shared__ uint32_t bits[32][32];
     __shared__ int ws[32], cnt[SHERRY_MAX_ADAPTERS], found;
+    __shared__ uint16_t held[kPlanHeld];  // the first slots' adapters
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tiles = (int)plan.tiles;
     cnt[tid] = 0;
@@ -117,21 +119,21 @@ __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, con
             if (a < n) atomicOr(&bits[warp][a >> 5], 1u << (a & 31));
         }
         __syncthreads();
-        uint32_t word = bits[warp][lane];
-        int sum = __popc(word);
-        const int mine = sum;
-        sum = block_scan(sum, ws);
-        int at = total + sum - mine;
+        const uint32_t word = bits[warp][lane];
+        const int mine = __popc(word), at = total + block_scan(mine, ws) - mine;
         if (lane == 0 && t < tiles) plan.tile_b[t] = at;
-        while (word) {
-            const int a = 32 * lane + __ffs(word) - 1;
-            word &= word - 1;
-            if (at < plan.max_slots) {
-                plan.slot_a[at] = a;
-                plan.slot_t[at] = t;
+        for (unsigned some = __ballot_sync(kFull, word != 0u); some; some &= some - 1) {
+            const int w = __ffs(some) - 1;  // a lane per adapter of each 32
+            const uint32_t ws32 = __shfl_sync(kFull, word, w);
+            const int s = __shfl_sync(kFull, at, w) + __popc(ws32 & ((1u << lane) - 1u)), a = 32 * w + lane;
+            if (ws32 >> lane & 1u) {
+                if (s < plan.max_slots) {
+                    plan.slot_a[s] = a;
+                    plan.slot_t[s] = t;
+                }
+                if (s < kPlanHeld) held[s] = (uint16_t)a;
+                atomicAdd(&cnt[a], 1);
             }
-            ++at;
-            atomicAdd(&cnt[a], 1);
         }
         const int all = __reduce_add_sync(kFull, ws[lane]);
         total += all;
@@ -144,9 +146,11 @@ __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, con
         if (tid == n - 1) plan.adap_b[n] = end;
         __syncthreads();
         for (int s = tid; s < total; s += kPlanThreads) {
-            const int a = plan.slot_a[s];
+            const int a = s < kPlanHeld ? held[s] : plan.slot_a[s];
             int before = 0;
-            for (int j = 0; j < s; ++j) before += plan.slot_a[j] == a;
+#pragma unroll 8
+            for (int j = 0; j < min(s, kPlanHeld); ++j) before += held[j] == a;
+            for (int j = kPlanHeld; j < s; ++j) before += plan.slot_a[j] == a;
             plan.adap_s[cnt[a] + before] = s;
         }
         if (tid == 0) {
@@ -934,16 +938,17 @@ int lora_grad_launch(const LoraGradJob* jobs, int count, int R, int n_adapters, 
     int64_t blocks = 0;
     P.terms = jobs[0].V.terms;
     P.rp = jobs[0].V.rp;
-    for (int j = 0; j < 2; ++j) {
-        const LoraGradJob& J = jobs[j < count ? j : 0];
+    for (int j = 0; j < count; ++j) {
+        const LoraGradJob& J = jobs[j];
         P.out[j] = J.out;
         P.unit[j] = J.unit;
         P.C[j] = J.C;
         P.by_column[j] = J.by_column;
         P.cblocks[j] = (int)((J.C + kGrCols - 1) / kGrCols);
-        if (j < count) blocks += (int64_t)P.cblocks[j] * n_adapters;
+        blocks += (int64_t)P.cblocks[j] * n_adapters;
         int st = encode_2d(&maps.g[j], J.G, J.ldg, M, kGrTok);
-        if (!st) st = encode_2d(&maps.gp[j], J.Gp ? J.Gp : J.G, J.ldg, M, kGrTok);
+        maps.gp[j] = maps.g[j];
+        if (!st && J.Gp) st = encode_2d(&maps.gp[j], J.Gp, J.ldg, M, kGrTok);
         if (!st) st = encode_2d(&maps.v[j], J.V.data, P.terms * P.rp, (int64_t)plan.max_slots * kLoraTile, kGrTok);
         if (st) return st;
     }

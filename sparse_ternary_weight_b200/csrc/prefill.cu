@@ -32,7 +32,10 @@
 #include "lut.cuh"
 #include "tc.cuh"
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
+
+namespace cg = cooperative_groups;
 
 namespace sherry {
 
@@ -99,6 +102,9 @@ struct PParams {
 // for tokens of other adapters, all by TMA into one X slot (the terms first, then B_a).  A
 // slot is one more accumulator group with scale 1, added for its own tokens alone, so
 // that an adapter whose weights are not finite spoils no other request's tokens.
+// Where there are fewer tiles than SMs a cluster of CL CTAs shares a tile: each sums its part
+// of K (whole groups), the last one adds the slots, and the partial tiles are joined
+// in order through distributed shared memory (331 x 2050 x 8192, rank 8: SPLITFIG).
 constexpr int kPLoraB = 3 * kPStepB;  // where B_a's tile lies in the slot: after at most three terms' tiles
 enum class PMode { kPlain, kArenas, kLora };
 
@@ -141,9 +147,17 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     // chunk and accumulator phases run on across tiles
     const int ntn = (P.N + kPBM - 1) / kPBM;
     const int ntiles = ntn * ((P.M + kPBN - 1) / kPBN);
-    const int nk = P.K / kPBK;
+    // LORA: CTAs that share a tile (then one tile each), and this one's place
+    const int CL = LORA ? (int)cg::this_cluster().num_blocks() : 1;
+    const int cr = LORA ? (int)cg::this_cluster().block_rank() : 0;
+    const unsigned tile0 = blockIdx.x / CL, tstride = gridDim.x / CL;  // LORA
+    // this CTA's steps kb .. kb + nk of K, in groups of gs
+    const int ksteps = P.K / kPBK;
+    const int unit = LORA && P.row_scale ? 1 : P.group_steps;
+    const int kb = LORA ? (int)((int64_t)(ksteps / unit) * cr / CL) * unit : 0;
+    const int nk = LORA ? (int)((int64_t)(ksteps / unit) * (cr + 1) / CL) * unit - kb : ksteps;
+    const int gs = LORA && P.row_scale ? nk : P.group_steps;
     const int nchunks = (nk + CS - 1) / CS;  // the last one may hold fewer steps
-    const int gs = P.group_steps;
     const int ngroups = nk / gs;
     // LORA: chunks of 64 ranks per slot, and whether the terms of U lie in one tile's 64 columns
     const int lblocks = LORA ? (P.rp + 63) / 64 : 0;
@@ -185,7 +199,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     const bool permuted = LORA && P.plan.may_permute && P.plan.head[0] != 0;
     // the slots of tile t; every role loads them at the tile's start and uses them at its end
     auto slots_of = [&](int t) {
-        return LORA ? make_int2(P.plan.tile_b[t / ntn], P.plan.tile_b[t / ntn + 1]) : make_int2(0, 0);
+        return LORA && cr == CL - 1 ? make_int2(P.plan.tile_b[t / ntn], P.plan.tile_b[t / ntn + 1]) : make_int2(0, 0);
     };
 
     if (warp < EPI) {
@@ -197,7 +211,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
         int b = 0;
         uint32_t bph = 0;  // phase parity of accumulator b's use
         uint32_t dph = 0;  // ARN: phase parity of the dense accumulator's use
-        for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+        for (int t = LORA ? tile0 : blockIdx.x; t < ntiles && ok; t += LORA ? tstride : gridDim.x) {
             const int n = (t % ntn) * kPBM + q * 32 + lane;
             const int m0 = (t / ntn) * kPBN + half * kCols;
             const int2 sl = slots_of(t);
@@ -207,7 +221,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 own0[c] = LORA && sl.x < sl.y ? P.plan.mask[4 * sl.x + half * (kCols / 32) + c] : 0u;
             const bool row_ok = n < P.N;
             const bool gsc = !P.row_scale && row_ok;
-            const float* srow = P.scales + (int64_t)(row_ok ? n : 0) * P.spr;
+            const float* srow = P.scales + (int64_t)(row_ok ? n : 0) * P.spr + (LORA && !P.row_scale ? kb / gs : 0);
             // group scales are loaded two groups ahead of their use
             float a_next = gsc ? __ldg(srow) : 1.0f;
             float a_next2 = (gsc && ngroups > 1) ? __ldg(srow + 1) : 1.0f;
@@ -286,7 +300,12 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 mbar_arrive(dense_empty);
                 dph ^= 1u;
             }
-            if (row_ok && LORA && permuted) {
+            if (LORA && CL > 1) {
+                // the tile as [token][row] in the X slots: every product and load of this CTA is done
+                float* part = reinterpret_cast<float*>(psmem + (base - smem_u32(psmem)));
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) part[(half * kCols + j) * kPBM + q * 32 + lane] = acc[j];
+            } else if (row_ok && LORA && permuted) {
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) {
                     if (m0 + j < P.M) {
@@ -319,12 +338,12 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
         const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)kPAcol;
         int cc = 0;  // chunks done so far (all tiles)
         bool ok = true;
-        for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+        for (int t = LORA ? tile0 : blockIdx.x; t < ntiles && ok; t += LORA ? tstride : gridDim.x) {
             const int n = (t % ntn) * kPBM + i;
             const bool row_ok = n < P.N;
             const int2 sl = slots_of(t);
-            const uint32_t* idxr = P.idx + (int64_t)(row_ok ? n : 0) * P.words;
-            const uint8_t* sgnr = P.sgn + (int64_t)(row_ok ? n : 0) * P.words;
+            const uint32_t* idxr = P.idx + (int64_t)(row_ok ? n : 0) * P.words + (LORA ? 2 * kb : 0);
+            const uint8_t* sgnr = P.sgn + (int64_t)(row_ok ? n : 0) * P.words + (LORA ? 2 * kb : 0);
             // ring of the next kPRing chunks' packed words: per step 2 idx words + 2 sign bytes
             uint2 rw[kPRing][2];
             uint32_t rs[kPRing][2];
@@ -411,7 +430,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             uint32_t cph = 0;  // phase parity of slot c's use
             int issued[XS] = {};  // chunks loaded into each slot (phases of full_x)
             bool ok = true;
-            for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+            for (int t = LORA ? tile0 : blockIdx.x; t < ntiles && ok; t += LORA ? tstride : gridDim.x) {
                 const int m0 = (t / ntn) * kPBN;
                 const int n0 = (t % ntn) * kPBM;
                 const int2 sl = slots_of(t);
@@ -429,7 +448,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     mbar_expect_tx(full_x(c), (uint32_t)(steps * kPStepB * (ARN ? 2 : 1)));
                     for (int st = 0; st < steps; ++st) {
                         tma_load_2d(stX + c * SLOTB + st * kPStepB, LORA && permuted ? &wmap : &xmap,
-                                    (ch * CS + st) * kPBK, m0, full_x(c));
+                                    ((LORA ? kb : 0) + ch * CS + st) * kPBK, m0, full_x(c));
                         if constexpr (ARN)
                             tma_load_2d(stX + c * SLOTB + kWOff + st * kPStepB, &wmap, (ch * CS + st) * kPBK, n0,
                                         full_x(c));
@@ -508,13 +527,14 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 }
                 return true;
             };
-            for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+            for (int t = LORA ? tile0 : blockIdx.x; t < ntiles && ok; t += LORA ? tstride : gridDim.x) {
                 int gleft = gs;  // steps left in the current group
                 const int2 sl = slots_of(t);
                 for (int ch = 0; ch < nchunks; ++ch, ++cc) {
                     const int hbuf = cc % AB;
-                    if (!mbar_wait(full_a(hbuf), (aph >> hbuf) & 1u, &abort_s)) { ok = false; break; }
-                    aph ^= 1u << hbuf;
+                    const uint32_t ah = LORA ? (aph >> hbuf) & 1u : (uint32_t)((cc / AB) & 1);
+                    if (!mbar_wait(full_a(hbuf), ah, &abort_s)) { ok = false; break; }
+                    if constexpr (LORA) aph ^= 1u << hbuf;
                     if (!mbar_wait(full_x(c), cph, &abort_s)) { ok = false; break; }
                     tc_fence_after();
                     const uint64_t db0 = smem_desc(stX + c * SLOTB);
@@ -573,6 +593,31 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
         __syncwarp();
     }
 
+    if constexpr (LORA) {
+        if (CL > 1) {
+            cg::cluster_group cluster = cg::this_cluster();
+            __syncwarp();
+            cluster.sync();
+            if (warp < EPI) {  // this CTA's share of the tokens
+                float* part = reinterpret_cast<float*>(psmem + (base - smem_u32(psmem)));
+                const int row = threadIdx.x % kPBM, n = (tile0 % ntn) * kPBM + row, share = kPBN / CL;
+#pragma unroll 4
+                for (int i = threadIdx.x / kPBM; i < share; i += EPI / 4) {
+                    const int j = share * cr + i;
+                    int m = (tile0 / ntn) * kPBN + j;
+                    if (m >= P.M || n >= P.N) continue;
+                    if (permuted) m = P.plan.perm[m];
+                    float y = 0.0f;
+                    for (int r = 0; r < CL; ++r) y += cluster.map_shared_rank(part, r)[j * kPBM + row];
+                    if (P.y_bf16)
+                        reinterpret_cast<__nv_bfloat16*>(P.Y)[(int64_t)m * P.N + n] = __float2bfloat16_rn(y);
+                    else
+                        reinterpret_cast<float*>(P.Y)[(int64_t)m * P.N + n] = y;
+                }
+            }
+            cluster.sync();  // the others' tiles are read until here
+        }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == kPMmaWarp) {
@@ -590,6 +635,9 @@ bool prefill_eligible(const ProbShape& s, int64_t M) {
     if (M > (int64_t)0x7fffffff / 2) return false;
     return true;
 }
+
+// SMs that clusters of one CTA per SM can fill, in percent: what is left over in a GPC stays empty
+constexpr int kPRoom = 88;
 
 // Wd: the latent bf16 weight for Arenas; lora: the adapters' part of P (null: the plain linear)
 static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16,
@@ -649,11 +697,15 @@ static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, i
     // for per-row scales (one drain per tile; -1.5% at 2048 and 4096 tokens)
     const bool epi16 = s.granularity == SHERRY_PER_GROUP && s.K <= 4096;
     if (lora) {
+        // K is split while that still gives every CTA an SM, and each of them two chunks or more in whole groups
+        const int64_t steps = s.K / kPBK, units = P.row_scale ? steps : steps / P.group_steps;
+        int cl = 1;
+        while (cl < 8 && tiles * cl * 2 <= sms * kPRoom / 100 && units >= 2 * cl && steps >= 16 * cl) cl *= 2;
         if (epi16)
-            return launch_after(k_prefill<16, PMode::kLora>, grid, PRoles<16>::kThreads, kPSmem, stream, 1, true, map,
-                                wmap, bmap, umap, P);
-        return launch_after(k_prefill<8, PMode::kLora>, grid, PRoles<8>::kThreads, kPSmem, stream, 1, true, map, wmap,
-                            bmap, umap, P);
+            return launch_after(k_prefill<16, PMode::kLora>, grid * cl, PRoles<16>::kThreads, kPSmem, stream, cl, true,
+                                map, wmap, bmap, umap, P);
+        return launch_after(k_prefill<8, PMode::kLora>, grid * cl, PRoles<8>::kThreads, kPSmem, stream, cl, true, map,
+                            wmap, bmap, umap, P);
     } else if (Wd) {
         if (epi16)
             k_prefill<16, PMode::kArenas><<<grid, PRoles<16>::kThreads, kPSmem, stream>>>(map, wmap, bmap, umap, P);

@@ -758,8 +758,9 @@ int sherry_linear_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, 
         if ((st = lora_rows_launch(&rows, 1, M, LoraPlan{}, cs))) return st;
         G = rows.dst;
     }
-    return dgrad_launch(ProbShape{N, K, granularity, group}, idx, sgn, scales, G, ld, M, dX, nullptr, ws + w.part,
-                        device_sms(), cs);
+    const ProbShape s{N, K, granularity, group};
+    if ((st = dgrad_launch(s, idx, sgn, scales, G, ld, M, dX, nullptr, ws + w.part, device_sms(), cs))) return st;
+    return dgrad_join_launch(s, scales, M, dX, ws + w.part, device_sms(), cs);
 }
 
 size_t sherry_linear_lora_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int n_adapters, int rank) {
@@ -828,15 +829,16 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     }
     if ((st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs))) return st;
     const LoraGradArgs args{A, imgp, Gp, rank, n_adapters, plan};
-    if (dX && (st = dgrad_launch(ProbShape{N, K, granularity, group}, idx, sgn, scales, G, ld, M, dX, &args, ws + w.part,
-                                 sms, cs)))
-        return st;
+    const ProbShape s{N, K, granularity, group};
+    if (dX && (st = dgrad_launch(s, idx, sgn, scales, G, ld, M, dX, &args, ws + w.part, sms, cs))) return st;
     LoraGradJob jobs[2];
     int count = 0;
     if (dB) jobs[count++] = LoraGradJob{imgu, G, Gp, ld, N, dB, nullptr, 1};
     if (dA) jobs[count++] = LoraGradJob{imgp, X, plan.may_permute ? xp : nullptr, K, K, dA, scales, 0};
-    if (count == 0) return SHERRY_OK;
-    return lora_grad_launch(jobs, count, rank, n_adapters, M, plan, grad_dtype == SHERRY_BF16, sms, cs);
+    if (count &&
+        (st = lora_grad_launch(jobs, count, rank, n_adapters, M, plan, grad_dtype == SHERRY_BF16, dX != nullptr, sms, cs)))
+        return st;
+    return dX ? dgrad_join_launch(s, scales, M, dX, ws + w.part, sms, cs) : SHERRY_OK;
 }
 
 static int check_logits(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld) {

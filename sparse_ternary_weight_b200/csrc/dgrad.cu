@@ -161,8 +161,8 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
     if constexpr (LORA) {
-        pdl_trigger();
         pdl_wait();
+        pdl_trigger();  // only now: the next kernel reads what this one has waited for
     }
     const bool permuted = LORA && P.plan.may_permute && P.plan.head[0] != 0;
 
@@ -506,14 +506,16 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
     if (items > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)std::min<int64_t>(items, sms);
     auto kernel = g.tm == 2 ? (lora ? k_dgrad<2, true> : k_dgrad<2, false>) : (lora ? k_dgrad<1, true> : k_dgrad<1, false>);
-    st = launch_after(kernel, grid, kGThreads, kGSmem, stream, 1, lora != nullptr, map, ypmap, pmap, amap, P);
-    if (st) return st;
-    if (g.splits > 1) {
-        const int64_t total = M * s.K;
-        return launch_after(k_dgrad_join, (unsigned)((total / 4 + 255) / 256), 256, 0, stream, 1, true,
-                            static_cast<const float*>(workspace), g.splits, total, scales, dX);
-    }
-    return SHERRY_OK;
+    return launch_after(kernel, grid, kGThreads, kGSmem, stream, 1, lora != nullptr, map, ypmap, pmap, amap, P);
+}
+
+int dgrad_join_launch(const ProbShape& s, const float* scales, int64_t M, uint16_t* dX, const void* workspace, int sms,
+                      cudaStream_t stream) {
+    const GPlan g = dgrad_plan(M, s.N, s.K, sms);
+    if (g.splits == 1) return SHERRY_OK;
+    const int64_t total = M * s.K;
+    return launch_after(k_dgrad_join, (unsigned)((total / 4 + 255) / 256), 256, 0, stream, 1, true,
+                        static_cast<const float*>(workspace), g.splits, total, scales, dX);
 }
 
 int dgrad_status_take() { return tc_status_take(); }

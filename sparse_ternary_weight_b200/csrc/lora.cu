@@ -79,6 +79,7 @@ LoraPlan lora_plan_in(void* mem, int64_t M, int n_adapters) {
 // (ballots), so the order depends on the ids alone.  ids stay in L2; one launch.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanHeld = 2048;
+constexpr int kPlanAhead = 8;  // ids a thread holds while it places them
 
 __device__ __forceinline__ int lora_id(const int32_t* ids, int64_t m, int n_adapters) {
     const int a = ids[m];
@@ -116,7 +117,8 @@ __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, con
         for (int j = 0; j < kLoraTile / 32; ++j) {
             const int64_t m = (int64_t)t * kLoraTile + 32 * j + lane;
             const int a = t < tiles && m < M ? lora_id(ids, m, n) : n;
-            if (a < n) atomicOr(&bits[warp][a >> 5], 1u << (a & 31));
+            const unsigned same = __match_any_sync(kFull, a);  // (neighbours are mostly of one adapter)
+            if (a < n && lane == __ffs(same) - 1) atomicOr(&bits[warp][a >> 5], 1u << (a & 31));
         }
         __syncthreads();
         const uint32_t word = bits[warp][lane];
@@ -217,17 +219,26 @@ __global__ void __launch_bounds__(kPlanThreads) k_lora_plan(const int32_t* ids, 
     if (lane == 0) red[warp] = below;
     __syncthreads();
     int at = __reduce_add_sync(kFull, red[lane]);
-    for (int64_t m0 = 0; m0 < M; m0 += kPlanThreads) {
-        const int64_t m = m0 + tid;
-        const bool mine = m < M && lora_id(ids, m, n_adapters) == me;
-        const unsigned mask = __ballot_sync(kFull, mine);
-        __syncthreads();
-        if (lane == 0) red[warp] = __popc(mask);
-        __syncthreads();
-        const int c = red[lane];
-        const int before = __reduce_add_sync(kFull, lane < warp ? c : 0);
-        if (mine) plan.perm[at + before + __popc(mask & ((1u << lane) - 1u))] = (int)m;
-        at += __reduce_add_sync(kFull, c);
+    for (int64_t m0 = 0; m0 < M; m0 += kPlanAhead * kPlanThreads) {
+        bool mine[kPlanAhead];
+#pragma unroll
+        for (int u = 0; u < kPlanAhead; ++u) {
+            const int64_t m = m0 + u * kPlanThreads + tid;
+            mine[u] = m < M && lora_id(ids, m, n_adapters) == me;
+        }
+#pragma unroll
+        for (int u = 0; u < kPlanAhead; ++u) {
+            if (m0 + u * kPlanThreads >= M) break;
+            const unsigned mask = __ballot_sync(kFull, mine[u]);
+            __syncthreads();
+            if (lane == 0) red[warp] = __popc(mask);
+            __syncthreads();
+            const int c = red[lane];
+            const int before = __reduce_add_sync(kFull, lane < warp ? c : 0);
+            if (mine[u])
+                plan.perm[at + before + __popc(mask & ((1u << lane) - 1u))] = (int)(m0 + u * kPlanThreads + tid);
+            at += __reduce_add_sync(kFull, c);
+        }
     }
 }
 
@@ -413,6 +424,8 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
+    const int slot0 = blockIdx.x / CL;  // (below max_slots: the grid has no more clusters)
+    int a = P.plan.slot_a[slot0], tile = P.plan.slot_t[slot0];  // loaded beside the head, in vain past the last slot
     const bool permuted = P.plan.may_permute && P.plan.head[0] != 0;
     const int slots = P.plan.head[1];
     const int steps = (P.C + 63) / 64;
@@ -425,9 +438,12 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
     int c = 0;  // stage and its phase, of the TMA and the MMA thread
     uint32_t ph = 0, dph = 0;
     int used = 0;  // loads of the TMA thread
-    for (int s = P.product ? blockIdx.x / CL : slots; s < slots; s += gridDim.x / CL) {  // (whole clusters)
-        const int a = P.plan.slot_a[s];
-        const int64_t p0 = (int64_t)P.plan.slot_t[s] * kLoraTile;
+    for (int s = P.product ? slot0 : slots; s < slots; s += gridDim.x / CL) {  // (whole clusters)
+        if (s != slot0) {
+            a = P.plan.slot_a[s];
+            tile = P.plan.slot_t[s];
+        }
+        const int64_t p0 = (int64_t)tile * kLoraTile;
         int m = -1;  // warps 0..3: the thread's token
         if (warp == 4) {
             if (lane == 0) {
@@ -475,7 +491,7 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
             m = slot_token(P, permuted, p0 + tid, a);
             const unsigned in = __ballot_sync(kFull, m >= 0);
             if (cr == 0 && lane == 0) P.plan.mask[4 * s + warp] = in;
-            if (s == (int)(blockIdx.x / CL)) down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
+            if (s == slot0) down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
         }
         tc_fence_before();
         __syncthreads();  // all products done, no load in flight
@@ -530,7 +546,7 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
         }
     }
     // clusters without a slot still have a share of the side work
-    if (P.product && warp < 4 && (int)(blockIdx.x / CL) >= slots)
+    if (P.product && warp < 4 && slot0 >= slots)
         down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
     __syncthreads();
     if (warp == 5)
@@ -574,7 +590,7 @@ int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const 
     P.stage_bytes = kDnG + (d.by_row ? (P.rp + 63) / 64 * 64 * 128 : (P.rp * 128 + 1023) / 1024 * 1024);
     P.stages = std::min(kDnMaxStages, (kDnHalf - 2048) / P.stage_bytes);
     const int smem = std::max(P.stages * P.stage_bytes, P.rp * kLoraTile * 4) + 1024;
-    const int64_t grid = std::min<int64_t>(est * cl, (int64_t)4 * sms / cl * cl);
+    const int64_t grid = std::min<int64_t>(est, 4 * sms / cl) * cl;
     if ((int64_t)plan.max_slots * 4 > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     static PerDevice once;
     int v = 0;
@@ -714,6 +730,7 @@ struct GradParams {
     int by_column[2], cblocks[2];
     int R, rp, terms, n_adapters, out_bf16;
     int vboxes, stages;
+    int beside;  // runs beside the kernel before it
 };
 struct GradMaps {
     CUtensorMap g[2], gp[2], v[2];
@@ -759,8 +776,13 @@ k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradP
                      "r"(tcols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    pdl_trigger();
-    pdl_wait();
+    // After the input gradient, which itself waited for what this kernel reads before it let this one
+    // start, there is nothing to wait for; only the first cluster sees to it, at its end, that this
+    // kernel does not end before that one.
+    if (!P.beside) {
+        pdl_trigger();
+        pdl_wait();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -929,11 +951,13 @@ k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradP
             }
         cluster.sync();  // the others' partial sums are read until here
     }
+    if (P.beside && blockIdx.x == 0) pdl_wait();
 }
 
 int lora_grad_launch(const LoraGradJob* jobs, int count, int R, int n_adapters, int64_t M, const LoraPlan& plan,
-                     int out_bf16, int sms, cudaStream_t stream) {
+                     int out_bf16, bool beside, int sms, cudaStream_t stream) {
     GradParams P{};
+    P.beside = beside;
     GradMaps maps{};
     int64_t blocks = 0;
     P.terms = jobs[0].V.terms;

@@ -80,6 +80,9 @@ size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int sms);
 int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, const float* scales, const uint16_t* dY,
                  int64_t ldy, int64_t M, uint16_t* dX, const LoraGradArgs* lora, void* workspace, int sms,
                  cudaStream_t stream);
+// where the rows were split over CTAs: dX from their partial sums; otherwise nothing
+int dgrad_join_launch(const ProbShape& s, const float* scales, int64_t M, uint16_t* dX, const void* workspace, int sms,
+                      cudaStream_t stream);
 
 // bytes of a plan, and the plan laid out in `mem` (256-byte aligned); false where it is too large
 size_t lora_plan_bytes(int64_t M, int n_adapters);
@@ -135,8 +138,9 @@ struct LoraGradJob {
     const float* unit;
     int by_column;
 };
+// `beside`: right after dgrad_launch's kernel, whose idle SMs it takes
 int lora_grad_launch(const LoraGradJob* jobs, int count, int R, int n_adapters, int64_t M, const LoraPlan& plan,
-                     int out_bf16, int sms, cudaStream_t stream);
+                     int out_bf16, bool beside, int sms, cudaStream_t stream);
 int lora_status_take();  // as stream_status_take
 
 }  // namespace sherry

@@ -584,14 +584,9 @@ static int check_lora(int64_t M, int n_adapters, int rank) {
     return SHERRY_OK;
 }
 
-// Up to this many tokens the product into rank space runs without a plan of tokens by adapter.
-constexpr int64_t kLoraFew = 32;
-
-// The adapters' product is part of the prefill kernel where that is the kernel of the linear
-// and tokens are not so few that a streaming or few-token kernel takes them.
-static bool lora_in_prefill(const ProbShape& s, int64_t M) {
-    return prefill_eligible(s, M) && (M > kLoraFew || !skinny_eligible(s, M));
-}
+// The adapters' product is part of the prefill kernel where that takes the shape; at most kLoraFew
+// tokens have kernels of their own.
+static bool lora_in_prefill(const ProbShape& s, int64_t M) { return M > kLoraFew && prefill_eligible(s, M); }
 
 struct LoraWs {
     size_t u, plan, img, xp, y32, total;  // offsets (0: none) and size
@@ -604,8 +599,9 @@ static int lora_terms(int dtype) { return dtype == SHERRY_BF16 ? 2 : 3; }
 static LoraWs lora_ws(const ProbShape& s, int64_t M, int n_adapters, int rank, int y_dtype) {
     LoraWs w{};
     const bool pre = lora_in_prefill(s, M);
-    size_t at = std::max(up256(pre ? 0 : linear_ws_bytes(&s, 1, M, device_sms())), kTicketBytes);
-    if (pre || M > kLoraFew) {
+    const bool few = M <= kLoraFew;
+    size_t at = std::max(up256(pre || few ? 0 : linear_ws_bytes(&s, 1, M, device_sms())), kTicketBytes);
+    if (!few) {
         w.plan = at;
         at += lora_plan_bytes(M, n_adapters);
         if (lora_may_permute(M, n_adapters)) {
@@ -619,7 +615,7 @@ static LoraWs lora_ws(const ProbShape& s, int64_t M, int n_adapters, int rank, i
     } else {
         w.u = at;
         at += up256((size_t)M * rank * sizeof(float));
-        if (y_dtype == SHERRY_BF16) {
+        if (y_dtype == SHERRY_BF16 && !few) {
             w.y32 = at;
             at += (size_t)(M * s.N) * sizeof(float);
         }
@@ -657,28 +653,23 @@ int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const
     const bool bf16 = y_dtype == SHERRY_BF16;
     const bool pre = lora_in_prefill(s, M);
     float* u = U || pre ? U : reinterpret_cast<float*>(ws + w.u);
-    LoraPlan plan{};
+    if (M <= kLoraFew) return lora_few_launch(s, d, M, bf16, A, B, rank, ids, scaling, n_adapters, u, cs);
     LoraDown down{};
-    if (w.plan) {
-        plan = lora_plan_in(ws + w.plan, M, n_adapters);
-        if ((st = lora_plan_launch(ids, M, n_adapters, plan, cs))) return st;
-        down.G = X;
-        if (w.xp) {
-            const LoraRows rows{X, reinterpret_cast<uint16_t*>(ws + w.xp), K, K, 0};
-            if ((st = lora_rows_launch(&rows, 1, M, plan, cs))) return st;
-            down.Gp = rows.dst;
-        }
-        down.ldg = down.C = K;
-        down.W = A;
-        down.ids = ids;
-        down.scaling = scaling;
-        down.V = u;
-        if (pre) down.img = LoraImage{reinterpret_cast<uint16_t*>(ws + w.img), lora_rp(rank), lora_terms(y_dtype)};
-        st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs);
-    } else {
-        st = lora_down_few_launch(X, K, M, K, A, K, rank, ids, scaling, n_adapters, u, cs);
+    const LoraPlan plan = lora_plan_in(ws + w.plan, M, n_adapters);
+    if ((st = lora_plan_launch(ids, M, n_adapters, plan, cs))) return st;
+    down.G = X;
+    if (w.xp) {
+        const LoraRows rows{X, reinterpret_cast<uint16_t*>(ws + w.xp), K, K, 0};
+        if ((st = lora_rows_launch(&rows, 1, M, plan, cs))) return st;
+        down.Gp = rows.dst;
     }
-    if (st) return st;
+    down.ldg = down.C = K;
+    down.W = A;
+    down.ids = ids;
+    down.scaling = scaling;
+    down.V = u;
+    if (pre) down.img = LoraImage{reinterpret_cast<uint16_t*>(ws + w.img), lora_rp(rank), lora_terms(y_dtype)};
+    if ((st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs))) return st;
     if (pre)
         return prefill_lora_launch(s, d, M, bf16, LoraArgs{B, down.img, down.Gp, rank, n_adapters, plan}, cs);
     float* y32 = bf16 ? reinterpret_cast<float*>(ws + w.y32) : static_cast<float*>(Y);

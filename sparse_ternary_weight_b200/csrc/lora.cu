@@ -603,67 +603,7 @@ int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const 
     return launch_after(k_lora_down, (unsigned)grid, kDnThreads, (size_t)smem, stream, cl, true, gmap, gpmap, wmap, P);
 }
 
-struct FewParams {
-    const uint16_t* G;
-    const uint16_t* W;
-    const float* scaling;
-    const int32_t* ids;
-    float* V;
-    int64_t ldg, ldw;
-    int M, C, R, n_adapters;
-};
-
-// Few tokens: a CTA per token and four ranks, 16-byte loads, fp32 on the CUDA cores.
-__global__ void __launch_bounds__(128) k_lora_down_few(const FewParams P) {
-    __shared__ float red[4][4];
-    const int m = blockIdx.y, r0 = 4 * blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int a = P.ids[m];
-    float* out = P.V + (int64_t)m * P.R + r0;
-    if (a < 0 || a >= P.n_adapters) {
-        if (threadIdx.x < 4) out[threadIdx.x] = 0.0f;
-        return;
-    }
-    const uint16_t* g = P.G + (int64_t)m * P.ldg;
-    const uint16_t* w = P.W + ((int64_t)a * P.R + r0) * P.ldw;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-    for (int k = 8 * threadIdx.x; k < P.C; k += 8 * 128) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(g + k));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(w + r * P.ldw + k));
-            const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[r] = fmaf(bf16lo(xs[j]), bf16lo(vs[j]), acc[r]);
-                acc[r] = fmaf(bf16hi(xs[j]), bf16hi(vs[j]), acc[r]);
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) acc[r] += __shfl_xor_sync(kFull, acc[r], o);
-        if (lane == 0) red[warp][r] = acc[r];
-    }
-    __syncthreads();
-    if (threadIdx.x < 4) {
-        const float s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
-        out[threadIdx.x] = (P.scaling ? P.scaling[a] : 1.0f) * s;
-    }
-}
-
-int lora_down_few_launch(const uint16_t* G, int64_t ldg, int64_t M, int64_t C, const uint16_t* W, int64_t ldw, int R,
-                         const int32_t* ids, const float* scaling, int n_adapters, float* V, cudaStream_t stream) {
-    const FewParams P{G, W, scaling, ids, V, ldg, ldw, (int)M, (int)C, R, n_adapters};
-    k_lora_down_few<<<dim3((unsigned)(R / 4), (unsigned)M), 128, 0, stream>>>(P);
-    SHERRY_LAUNCH_CHECK();
-    return SHERRY_OK;
-}
-
-// ---- out of rank space, few tokens ---------------------------------------------------
+// ---- out of rank space, where the linear is not the prefill kernel's --------------------
 __global__ void __launch_bounds__(128) k_lora_up(const float* Yin, int N, int nblocks, const float* __restrict__ U,
                                                  const uint16_t* __restrict__ B, int R, const int32_t* __restrict__ ids,
                                                  int n_adapters, void* Y, int y_bf16) {

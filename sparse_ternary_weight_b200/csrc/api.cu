@@ -584,9 +584,22 @@ static int check_lora(int64_t M, int n_adapters, int rank) {
     return SHERRY_OK;
 }
 
-// The adapters' product is part of the prefill kernel where that takes the shape; at most kLoraFew
-// tokens have kernels of their own.
-static bool lora_in_prefill(const ProbShape& s, int64_t M) { return M > kLoraFew && prefill_eligible(s, M); }
+// Which kernels run sherry_linear_lora:
+//  kFew      the few tokens' kernel (lora_few.cu), whose 16-row tiles cost the same whatever the tokens
+//            are: 32 tokens or fewer, and more of them while M / 32 x N x K is at most 2^25.  Rank 16, 2
+//            or 16 adapters, few / prefill in us: 64 x 512 x 2048 10 / 23 to 35, 64 x 8192 x 2048 29 / 30
+//            to 42, 192 x 2048 x 2048 24 / 24 to 37, but 96 x 8192 x 2048 40 / 30 to 42
+//  kPrefill  the prefill kernel with the adapters' product in it
+//  kPlain    the linear, then the adapters' product added to it: shapes that prefill does not take, and
+//            one or two tokens of a large weight, where the linear's lookup kernel is faster than the few
+//            tokens' (1 x 8192 x 8192: 14 / 24; 1 x 8192 x 2048: 12 / 10)
+enum class LoraRoute { kFew, kPrefill, kPlain };
+static LoraRoute lora_route(const ProbShape& s, int64_t M) {
+    const int64_t large = (int64_t)1 << 25;
+    if (M <= 2 && s.N * s.K > large) return LoraRoute::kPlain;
+    if (M <= kLoraFew || (M <= 8 * kLoraFew && (M + kLoraFew - 1) / kLoraFew * s.N * s.K <= large)) return LoraRoute::kFew;
+    return prefill_eligible(s, M) ? LoraRoute::kPrefill : LoraRoute::kPlain;
+}
 
 struct LoraWs {
     size_t u, plan, img, xp, y32, total;  // offsets (0: none) and size
@@ -598,10 +611,10 @@ static int lora_terms(int dtype) { return dtype == SHERRY_BF16 ? 2 : 3; }
 // The linear's own workspace comes first and always keeps the ticket region to itself.
 static LoraWs lora_ws(const ProbShape& s, int64_t M, int n_adapters, int rank, int y_dtype) {
     LoraWs w{};
-    const bool pre = lora_in_prefill(s, M);
-    const bool few = M <= kLoraFew;
-    size_t at = std::max(up256(pre || few ? 0 : linear_ws_bytes(&s, 1, M, device_sms())), kTicketBytes);
-    if (!few) {
+    const LoraRoute r = lora_route(s, M);
+    const bool pre = r == LoraRoute::kPrefill, few = r == LoraRoute::kFew;
+    size_t at = std::max(up256(r == LoraRoute::kPlain ? linear_ws_bytes(&s, 1, M, device_sms()) : 0), kTicketBytes);
+    if (!few && M > 2) {
         w.plan = at;
         at += lora_plan_bytes(M, n_adapters);
         if (lora_may_permute(M, n_adapters)) {
@@ -651,27 +664,32 @@ int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int sms = device_sms();
     const bool bf16 = y_dtype == SHERRY_BF16;
-    const bool pre = lora_in_prefill(s, M);
+    const LoraRoute route = lora_route(s, M);
+    const bool pre = route == LoraRoute::kPrefill;
     float* u = U || pre ? U : reinterpret_cast<float*>(ws + w.u);
-    if (M <= kLoraFew) return lora_few_launch(s, d, M, bf16, A, B, rank, ids, scaling, n_adapters, u, cs);
-    LoraDown down{};
-    const LoraPlan plan = lora_plan_in(ws + w.plan, M, n_adapters);
-    if ((st = lora_plan_launch(ids, M, n_adapters, plan, cs))) return st;
-    down.G = X;
-    if (w.xp) {
-        const LoraRows rows{X, reinterpret_cast<uint16_t*>(ws + w.xp), K, K, 0};
-        if ((st = lora_rows_launch(&rows, 1, M, plan, cs))) return st;
-        down.Gp = rows.dst;
+    if (route == LoraRoute::kFew) return lora_few_launch(s, d, M, bf16, A, B, rank, ids, scaling, n_adapters, u, cs);
+    if (w.plan) {
+        LoraDown down{};
+        const LoraPlan plan = lora_plan_in(ws + w.plan, M, n_adapters);
+        if ((st = lora_plan_launch(ids, M, n_adapters, plan, cs))) return st;
+        down.G = X;
+        if (w.xp) {
+            const LoraRows rows{X, reinterpret_cast<uint16_t*>(ws + w.xp), K, K, 0};
+            if ((st = lora_rows_launch(&rows, 1, M, plan, cs))) return st;
+            down.Gp = rows.dst;
+        }
+        down.ldg = down.C = K;
+        down.W = A;
+        down.ids = ids;
+        down.scaling = scaling;
+        down.V = u;
+        if (pre) down.img = LoraImage{reinterpret_cast<uint16_t*>(ws + w.img), lora_rp(rank), lora_terms(y_dtype)};
+        if ((st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs))) return st;
+        if (pre)
+            return prefill_lora_launch(s, d, M, bf16, LoraArgs{B, down.img, down.Gp, rank, n_adapters, plan}, cs);
+    } else if ((st = lora_down_few_launch(s, d, M, A, rank, ids, scaling, n_adapters, u, cs))) {
+        return st;
     }
-    down.ldg = down.C = K;
-    down.W = A;
-    down.ids = ids;
-    down.scaling = scaling;
-    down.V = u;
-    if (pre) down.img = LoraImage{reinterpret_cast<uint16_t*>(ws + w.img), lora_rp(rank), lora_terms(y_dtype)};
-    if ((st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs))) return st;
-    if (pre)
-        return prefill_lora_launch(s, d, M, bf16, LoraArgs{B, down.img, down.Gp, rank, n_adapters, plan}, cs);
     float* y32 = bf16 ? reinterpret_cast<float*>(ws + w.y32) : static_cast<float*>(Y);
     d.Y = y32;
     if ((st = linear_launch(&s, &d, 1, M, 0, workspace, sms, cs))) return st;

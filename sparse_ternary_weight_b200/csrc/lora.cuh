@@ -120,11 +120,14 @@ struct LoraDown {
 };
 int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const LoraPlan& plan, int sms,
                      cudaStream_t stream);
-// The whole operator for at most kLoraFew tokens, without a plan (lora_few.cu); U fp32 [M][R] is written
-constexpr int64_t kLoraFew = 32;
+// The whole operator for few tokens, without a plan (lora_few.cu); U fp32 [M][R] is written
+constexpr int64_t kLoraFew = 32;  // tokens of one CTA
 int lora_few_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16, const uint16_t* A,
                     const uint16_t* B, int R, const int32_t* ids, const float* scaling, int n_adapters, float* U,
                     cudaStream_t stream);
+// U alone, likewise
+int lora_down_few_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, const uint16_t* A, int R,
+                         const int32_t* ids, const float* scaling, int n_adapters, float* U, cudaStream_t stream);
 // Y[m][n] = Yin[m][n] + sum_r U[m][r] B[a][n][r]
 int lora_up_launch(const float* Yin, int64_t M, int64_t N, const float* U, const uint16_t* B, int R,
                    const int32_t* ids, int n_adapters, void* Y, int y_bf16, cudaStream_t stream);

@@ -87,7 +87,7 @@ struct FewUpParams {
     const int32_t* ids;
     void* Y;
     int M, N, K, words;
-    int group_words, spr;  // words per scale group and scales per row (SCALE 1, 2)
+    int group_words, spr;  // words per scale group, and scales per row (0: one for all)
     int per_tensor;
     int R, n_adapters, y_bf16;
 };
@@ -100,16 +100,17 @@ __device__ __forceinline__ void few_mma(float* d, uint32_t a0, uint32_t a1, uint
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: tiles of 8 tokens.  SCALE: 0 per row or tensor (applied at the end), 1 groups of whole chunks of
-// 128 weights, 2 any groups (promoted word by word)
+// NT: tiles of 8 tokens.  SCALE: 0 per row or tensor (applied at the end) and 1 groups of whole chunks
+// of 128 weights, both for K % 128 == 0; 2 all other shapes (loaded and promoted word by word)
 template <int NT, int SCALE>
-__global__ void __launch_bounds__(32 * kFewWarps) k_lora_few(const __grid_constant__ FewUpParams P) {
+__global__ void __launch_bounds__(32 * kFewWarps, NT == 1 ? 3 : 2) k_lora_few(const __grid_constant__ FewUpParams P) {
+    constexpr bool XAHEAD = NT <= 2;  // X is loaded with the words; for four tiles when it is used (registers)
     pdl_trigger();
     __shared__ __align__(256) uint32_t table[64];  // the 32 patterns' low halves, then high halves
     __shared__ float part[kFewWarps][8 * NT * kFewPitch];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int n0 = blockIdx.x * kFewRows;
+    const int n0 = blockIdx.x * kFewRows, m0 = blockIdx.y * (8 * NT);  // rows and tokens of this CTA
     if (tid < 32) {
         const uint2 e = decode_block_bf16((uint32_t)tid & 15u, (uint32_t)tid >> 4);
         table[tid] = e.x;
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_lora_few(const __grid_consta
     }
     // B's rows are fetched beside the linear
     for (int o = tid; o < kFewRows * 8 * NT; o += 32 * kFewWarps) {
-        const int n = n0 + o % kFewRows, m = o / kFewRows;
+        const int n = n0 + o % kFewRows, m = m0 + o / kFewRows;
         if (m < P.M && n < P.N) {
             const int a = P.ids[m];
             if (a >= 0 && a < P.n_adapters) {
@@ -136,15 +137,33 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_lora_few(const __grid_consta
     const uint8_t* sb = P.sgn + rb * P.words;
     const float* al = P.scales + ra * P.spr;
     const float* bl = P.scales + rb * P.spr;
-    const bool vec = P.words % 4 == 0;
+    constexpr bool vec = SCALE != 2;
     const int chunks = (P.words + 3) / 4;
     const int ch0 = chunks * warp / kFewWarps, ch1 = chunks * (warp + 1) / kFewWarps;
-    struct Words {
+    struct Chunk {  // 128 weights of both rows and the tokens' X
         uint32_t a[4], b[4];
         uint32_t sa, sb;
         float al, bl;
+        uint4 x[XAHEAD ? 4 : 1][NT];
     };
-    auto fetch = [&](int ch, Words& w) {
+    const uint16_t* xr[NT];  // the lane's token of each tile (past the last: the last again), at its place in a word
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xr[t] = P.X + (int64_t)min(m0 + 8 * t + g, P.M - 1) * P.K + 8 * c;
+    auto fetch_x = [&](int ch, uint4 (*x)[NT]) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint4* p = reinterpret_cast<const uint4*>(xr[t] + 128 * ch);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // past the row: zero
+                x[j][t] = vec || 4 * ch + j < P.words ? __ldg(p + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    int group = 0, left = P.group_words / 4;  // SCALE 1: the fetched chunk's group, and its chunks from there on
+    if (SCALE == 1) {
+        group = ch0 / left;
+        left -= ch0 % left;
+    }
+    auto fetch = [&](int ch, Chunk& w) {
         if (ch >= ch1) return;
         const int w0 = 4 * ch;
         if (vec) {
@@ -157,7 +176,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_lora_few(const __grid_consta
             w.sa = w.sb = 0u;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool in = w0 + j < P.words;  // past the row X reads as zero
+                const bool in = w0 + j < P.words;
                 w.a[j] = in ? __ldg(ia + w0 + j) : 0u;
                 w.b[j] = in ? __ldg(ib + w0 + j) : 0u;
                 if (in) {
@@ -167,45 +186,49 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_lora_few(const __grid_consta
             }
         }
         if (SCALE == 1) {
-            w.al = __ldg(al + w0 / P.group_words);
-            w.bl = __ldg(bl + w0 / P.group_words);
+            w.al = __ldg(al + group);
+            w.bl = __ldg(bl + group);
+            if (--left == 0) {
+                ++group;
+                left = P.group_words / 4;
+            }
         }
+        if (XAHEAD) fetch_x(ch, w.x);
     };
     float sum[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[t][j] = 0.0f;
-    Words w, next;
-    fetch(ch0, w);
-    for (int ch = ch0; ch < ch1; ++ch) {
-        fetch(ch + 1, next);
-        uint4 x[4][NT];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int m = 8 * t + g;
-                x[j][t] = make_uint4(0u, 0u, 0u, 0u);
-                if (m < P.M && 4 * ch + j < P.words)
-                    x[j][t] = __ldg(reinterpret_cast<const uint4*>(P.X + (int64_t)m * P.K + 32 * (4 * ch + j) + 8 * c));
-            }
+    auto multiply = [&](int ch, Chunk& w) {
+        if (ch >= ch1) return;
+        uint4 xl[XAHEAD ? 1 : 4][NT];
+        if (!XAHEAD) fetch_x(ch, xl);
+        uint4(*x)[NT] = XAHEAD ? w.x : xl;
         float acc[NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[t][j] = SCALE == 0 ? sum[t][j] : 0.0f;
+        // byte j of even[q] (odd[q]): 4 * code of block 2c (2c + 1) of row q's word j, code = nibble + 16 * sign
+        uint32_t even[2], odd[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t* v = q ? w.b : w.a;
+            const uint32_t sg = q ? w.sb : w.sa;
+            const uint32_t sel = (uint32_t)c | (uint32_t)(c + 4) << 4;
+            const uint32_t bytes = __byte_perm(__byte_perm(v[0], v[1], sel), __byte_perm(v[2], v[3], sel), 0x5410u);
+            even[q] = ((bytes << 2) & 0x3c3c3c3cu) | ((sg << (6 - 2 * c)) & 0x40404040u);
+            odd[q] = ((bytes >> 2) & 0x3c3c3c3cu) | (__funnelshift_l(sg, sg, (5 - 2 * c) & 31) & 0x40404040u);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t ev[2], od[2];
-            spread_word(w.a[j], w.sa >> (8 * j), ev[0], od[0]);
-            spread_word(w.b[j], w.sb >> (8 * j), ev[1], od[1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // blocks 2c and 2c + 1
                 uint32_t lo[2], hi[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const uint32_t at = __byte_perm(h ? od[q] : ev[q], tab, (uint32_t)c | 0x7650u);
+                    const uint32_t at = __byte_perm(h ? odd[q] : even[q], tab, (uint32_t)j | 0x7650u);
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo[q]) : "r"(at));
                     asm volatile("ld.shared.u32 %0, [%1+128];" : "=r"(hi[q]) : "r"(at));
                 }
@@ -233,7 +256,17 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_lora_few(const __grid_consta
                 for (int j = 0; j < 4; ++j)
                     sum[t][j] = SCALE == 0 ? acc[t][j] : fmaf(j < 2 ? w.al : w.bl, acc[t][j], sum[t][j]);
         }
-        w = next;
+    };
+    // two chunks in turn, each loaded again as soon as it is used
+    Chunk w0, w1;
+    fetch(ch0, w0);
+    fetch(ch0 + 1, w1);
+#pragma unroll 1
+    for (int ch = ch0; ch < ch1; ch += 2) {
+        multiply(ch, w0);
+        fetch(ch + 2, w0);
+        multiply(ch + 1, w1);
+        fetch(ch + 3, w1);
     }
     // rows g and g + 8, tokens 2c and 2c + 1 of each tile
 #pragma unroll
@@ -243,11 +276,11 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_lora_few(const __grid_consta
     __syncthreads();
     pdl_wait();
     for (int o = tid; o < kFewRows * 8 * NT; o += 32 * kFewWarps) {
-        const int n = n0 + o % kFewRows, m = o / kFewRows;
+        const int n = n0 + o % kFewRows, m = m0 + o / kFewRows;
         if (m >= P.M || n >= P.N) continue;
         float y = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kFewWarps; ++q) y += part[q][m * kFewPitch + o % kFewRows];
+        for (int q = 0; q < kFewWarps; ++q) y += part[q][(m - m0) * kFewPitch + o % kFewRows];
         if (SCALE == 0) y *= __ldg(P.scales + (P.per_tensor ? 0 : n));
         const int a = P.ids[m];
         if (a >= 0 && a < P.n_adapters) {
@@ -277,17 +310,25 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_lora_few(const __grid_consta
 }
 
 template <int NT>
-static int few_launch(const FewUpParams& P, int scale, unsigned grid, cudaStream_t stream) {
+static int few_launch(const FewUpParams& P, int scale, dim3 grid, cudaStream_t stream) {
     auto kernel = scale == 0 ? k_lora_few<NT, 0> : scale == 1 ? k_lora_few<NT, 1> : k_lora_few<NT, 2>;
+    grid.y = (unsigned)((P.M + 8 * NT - 1) / (8 * NT));
     return launch_after(kernel, grid, 32 * kFewWarps, 0, stream, 1, true, P);
+}
+
+int lora_down_few_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, const uint16_t* A, int R,
+                         const int32_t* ids, const float* scaling, int n_adapters, float* U, cudaStream_t stream) {
+    const FewParams D{d.X, A, scaling, ids, U, (int)M, (int)s.K, R, n_adapters};
+    k_lora_down_few<<<dim3((unsigned)(R / 4), (unsigned)M), 128, 0, stream>>>(D);
+    SHERRY_LAUNCH_CHECK();
+    return SHERRY_OK;
 }
 
 int lora_few_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16, const uint16_t* A,
                     const uint16_t* B, int R, const int32_t* ids, const float* scaling, int n_adapters, float* U,
                     cudaStream_t stream) {
-    const FewParams D{d.X, A, scaling, ids, U, (int)M, (int)s.K, R, n_adapters};
-    k_lora_down_few<<<dim3((unsigned)(R / 4), (unsigned)M), 128, 0, stream>>>(D);
-    SHERRY_LAUNCH_CHECK();
+    const int st = lora_down_few_launch(s, d, M, A, R, ids, scaling, n_adapters, U, stream);
+    if (st) return st;
     FewUpParams P{};
     P.X = d.X;
     P.idx = d.idx;
@@ -303,17 +344,17 @@ int lora_few_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, 
     P.words = (int)(s.K / 32);
     const bool grouped = s.granularity == SHERRY_PER_GROUP;
     P.group_words = grouped ? s.group / 32 : P.words;
-    P.spr = grouped ? (int)(s.K / s.group) : 0;
+    P.spr = grouped ? (int)(s.K / s.group) : s.granularity == SHERRY_PER_CHANNEL;
     P.per_tensor = s.granularity == SHERRY_PER_TENSOR;
     P.R = R;
     P.n_adapters = n_adapters;
     P.y_bf16 = y_bf16;
     const int64_t grid = (s.N + kFewRows - 1) / kFewRows;
     if (grid > 0x7fffffff || s.N > 0x7fffffff - kFewRows) return SHERRY_ERR_UNSUPPORTED;
-    const int scale = !grouped ? 0 : s.group % 128 == 0 ? 1 : 2;
-    if (M <= 8) return few_launch<1>(P, scale, (unsigned)grid, stream);
-    if (M <= 16) return few_launch<2>(P, scale, (unsigned)grid, stream);
-    return few_launch<4>(P, scale, (unsigned)grid, stream);
+    const int scale = s.K % 128 != 0 ? 2 : !grouped ? 0 : s.group % 128 == 0 ? 1 : 2;
+    if (M <= 8) return few_launch<1>(P, scale, dim3((unsigned)grid), stream);
+    if (M <= 16) return few_launch<2>(P, scale, dim3((unsigned)grid), stream);
+    return few_launch<4>(P, scale, dim3((unsigned)grid), stream);
 }
 
 }  // namespace sherry

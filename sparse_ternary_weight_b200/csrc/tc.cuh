@@ -233,10 +233,10 @@ static int encode_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t 
 // Launch `kernel` in clusters of `cluster`; with `after` it may begin while the kernel before it in the
 // stream ends (it calls pdl_wait before it touches that kernel's results).
 template <typename... Params, typename... Args>
-static int launch_after(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+static int launch_after(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                         int cluster, bool after, Args&&... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

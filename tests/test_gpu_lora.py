@@ -197,6 +197,70 @@ def test_linear_lora_backward(sw, orc, case, gdt):
     assert all(torch.equal(p, q) for p, q in zip((dX, dA, dB), again))
 
 
+# what the cases above leave out: prefill tiles with ranks of one and two blocks in two and three terms,
+# K split over a cluster, tokens taken adapter by adapter (odd N besides), more slots than clusters,
+# one adapter with many tiles beside many without, one and two tokens of a large weight
+MORE = [
+    (257, 130, 512, "group", 128, 128, 2, "sorted"),
+    (300, 257, 1024, "channel", 0, 128, 3, "mixed"),
+    (520, 129, 8192, "group", 128, 16, 4, "sorted"),
+    (390, 70, 4096, "tensor", 0, 24, 2, "wild"),
+    (1000, 201, 640, "group", 64, 40, 30, "mixed"),
+    (256, 130, 256, "group", 128, 16, 4, "mixed"),
+    (9000, 64, 256, "group", 128, 8, 64, "last"),
+    (1, 1056, 32768, "group", 128, 16, 2, "last"),
+    (2, 1057, 32768, "channel", 0, 8, 3, "sorted"),
+]
+MORE_IDS = [f"M{c[0]}-{c[1]}x{c[2]}-{c[3]}{c[4]}-r{c[5]}x{c[6]}-{c[7]}" for c in MORE]
+
+
+@pytest.mark.parametrize("case", MORE, ids=MORE_IDS)
+def test_linear_lora_more(sw, orc, case):
+    test_linear_lora(sw, orc, case)
+
+
+@pytest.mark.parametrize("gdt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", MORE[:7], ids=MORE_IDS[:7])
+def test_linear_lora_backward_more(sw, orc, case, gdt):
+    test_linear_lora_backward(sw, orc, case, gdt)
+
+
+@pytest.mark.parametrize("M,n", [(20, 3), (300, 3), (1000, 20)])
+def test_tokens_of_none_may_hold_anything(sw, orc, M, n):
+    """Rows of padding (id -1) full of NaN and infinities reach no other token and no gradient."""
+    import torch
+    pr = Problem(sw, orc, M, 130, 512, "group", 128, 16, n, "mixed")
+    none = torch.from_numpy(pr.idsh < 0).cuda()
+    assert bool(none.any()) and not bool(none.all())
+    y, U = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+    want = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, U, pr.scaling, torch.float32)
+    X, G = pr.X.clone(), pr.G.clone()
+    for t in (X, G):
+        rows = torch.full_like(t, float("nan"))
+        rows[:, ::2] = float("inf")
+        t.copy_(torch.where(none[:, None], rows, t))
+    y2, U2 = sw.linear_lora(X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+    assert torch.equal(y2[~none], y[~none]) and torch.equal(U2, U)
+    dX, dA, dB = sw.linear_lora_backward(G, X, pr.P, pr.A, pr.B, pr.ids, U2, pr.scaling, torch.float32)
+    assert torch.equal(dX[~none], want[0][~none])
+    assert torch.equal(dA, want[1]) and torch.equal(dB, want[2])
+
+
+@pytest.mark.parametrize("M,ids", [(20, "mixed"), (300, "sorted"), (300, "mixed"), (1000, "mixed")])
+def test_an_adapter_that_is_not_finite_stays_alone(sw, orc, M, ids):
+    """NaN and infinities in one adapter's weights reach its own tokens only."""
+    import torch
+    pr = Problem(sw, orc, M, 130, 512, "group", 128, 16, 4, ids)
+    y = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling)
+    A, B = pr.A.clone(), pr.B.clone()
+    A[1] = float("nan")
+    B[1, ::2] = float("inf")
+    y2 = sw.linear_lora(pr.X, pr.P, A, B, pr.ids, pr.scaling)
+    own = pr.ids == 1
+    assert torch.equal(y2[~own], y[~own])
+    assert not bool(torch.isfinite(y2[own]).any())
+
+
 def test_large_backward_tiles(sw, orc):
     """Enough tiles for the 256-token form of the input gradient, ragged in every direction."""
     import torch
@@ -294,6 +358,25 @@ def test_autograd(sw, orc):
     ones = torch.ones_like(pr.G)
     want = sw.linear_lora_backward(ones, pr.X, pr.P, pr.A, pr.B, pr.ids, U, pr.scaling, need=(False, False, True))[2]
     assert torch.equal(B2.grad, want)
+
+
+def test_capture_of_a_permuted_call(sw, orc):
+    """A replay whose ids make other slots, another order of tokens or none takes them as they then are."""
+    import torch
+    pr = Problem(sw, orc, 700, 130, 512, "group", 128, 16, 12, "mixed")
+    g = torch.cuda.CUDAGraph()
+    sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling)
+    with torch.cuda.graph(g):
+        y, u = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+        grads = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, u, pr.scaling)
+    for ids in (pr.ids.clone(), pr.ids.sort().values, torch.full_like(pr.ids, -1), torch.flip(pr.ids, [0])):
+        pr.ids.copy_(ids)
+        g.replay()
+        torch.cuda.synchronize()
+        want, U = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+        assert torch.equal(y, want) and torch.equal(u, U)
+        again = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, U, pr.scaling)
+        assert all(torch.equal(p, q) for p, q in zip(grads, again))
 
 
 @pytest.mark.parametrize("M", [4, 40])

@@ -291,8 +291,9 @@ size_t sherry_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   U        fp32 [M][rank] (16-byte aligned), optional (NULL): written, zero for
  *            tokens of no adapter; the backward pass wants it
  *   Y        as sherry_linear
- *   workspace  sherry_linear_lora_workspace_bytes(...) bytes, a linear workspace:
- *            its first 256 KiB zero before first use, left zero by every call
+ *   workspace  sherry_linear_lora_workspace_bytes(...) bytes, 256-byte aligned; where
+ *            sherry_linear_lora_needs_tickets says so a linear workspace (its first 256
+ *            KiB zero before first use, left zero by every call), otherwise any scratch
  * fp32 accumulation; U enters tensor-core products as bf16 terms that keep 16 (bf16
  * Y) or 24 (fp32 Y) significant bits. */
 int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K,
@@ -302,6 +303,7 @@ int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K,
                        void* workspace, size_t workspace_bytes, void* stream);
 size_t sherry_linear_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int granularity, int group,
                                           int n_adapters, int rank, int y_dtype);
+int sherry_linear_lora_needs_tickets(int64_t M, int64_t N, int64_t K, int granularity, int group);
 
 /* Gradients of sherry_linear_lora, with P[m] = scaling[a] dY[m] B_a and sums over the
  * tokens of adapter a (scaling is a constant; T alpha is frozen):

@@ -478,6 +478,27 @@ def _stream_workspace(nbytes: int, device) -> "object":
     return buf
 
 
+_native = [None]
+
+
+def _calls():
+    """The compiled form of the ordinary calls (csrc/binding.cpp): contiguous tensors of the
+    right types on the current device.  Its functions return None for any other call,
+    which the wrappers then convert or refuse themselves, and an int for a status."""
+    if _native[0] is None:
+        lib()  # a missing library is reported in its own words
+        from . import _binding as module
+        _native[0] = module
+    return _native[0]
+
+
+def _done(r, what):
+    """What the binding returned, unless that is the status of a refused call."""
+    if type(r) is int:
+        check(r, what)
+    return r
+
+
 def _scratch(nbytes: int, device) -> "object":
     """Uninitialised scratch of one call, from torch's stream-ordered allocator."""
     import torch
@@ -538,11 +559,16 @@ def linear_lora(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None, out
     scaling fp32 [n_adapters] or None for 1.  With ``return_u`` returns (Y, U), U fp32
     [M, rank], which :func:`linear_lora_backward` takes."""
     import torch
+    out_dtype = out_dtype or torch.float32
+    yd = {torch.float32: F32, torch.bfloat16: BF16}[out_dtype]
+    if out is None:
+        r = _done(_calls().linear_lora(X, P.idx, P.sgn, P.scales, P.N, P.K, P.granularity, P.group, A, B, ids, scaling,
+                                         yd, return_u), "linear_lora")
+        if r is not None:
+            return r if return_u else r[0]
     X = _activations(X, P.K)
     A, B, ids, scaling, n, R = _adapters(X, P, A, B, ids, scaling)
     M = X.shape[0]
-    out_dtype = out_dtype or torch.float32
-    yd = {torch.float32: F32, torch.bfloat16: BF16}[out_dtype]
     out = _result(out, (M, P.N), out_dtype, X.device)
     U = torch.empty((M, R), dtype=torch.float32, device=X.device) if return_u else None
     if return_u and P.N == 0:
@@ -550,7 +576,8 @@ def linear_lora(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None, out
     with _on(X.device):
         L = lib()
         wsb = L.sherry_linear_lora_workspace_bytes(M, P.N, P.K, P.granularity, P.group, n, R, yd)
-        ws = _stream_workspace(wsb, X.device) if wsb else None
+        tickets = wsb and L.sherry_linear_lora_needs_tickets(M, P.N, P.K, P.granularity, P.group)
+        ws = _stream_workspace(wsb, X.device) if tickets else _scratch(wsb, X.device)
         check(L.sherry_linear_lora(_ptr(X), M, P.N, P.K, _ptr(P.idx), _ptr(P.sgn), _ptr(P.scales), P.granularity,
                                    P.group, _ptr(A), _ptr(B), _ptr(ids), _ptr(scaling), n, R, _ptr(U), _ptr(out), yd,
                                    _ptr(ws), wsb, _stream(X.device)), "linear_lora")
@@ -580,6 +607,13 @@ def linear_lora_backward(dY, X, P: PackedWeight, A, B, ids, U, scaling=None, gra
     tokens in ``grad_dtype`` (bf16, the default, or fp32).  ``need`` leaves out the
     gradients that are not wanted (None in their place)."""
     import torch
+    grad_dtype = grad_dtype or torch.bfloat16
+    gd = {torch.float32: F32, torch.bfloat16: BF16}[grad_dtype]
+    r = _done(_calls().linear_lora_backward(dY, X, P.idx, P.sgn, P.scales, P.N, P.K, P.granularity, P.group, A, B, ids,
+                                              scaling, U, gd, bool(need[0]) + 2 * bool(need[1]) + 4 * bool(need[2])),
+              "linear_lora_backward")
+    if r is not None:
+        return r
     dY = _activations(dY, P.N, "dY")
     X = _activations(X, P.K)
     M = X.shape[0]
@@ -592,8 +626,6 @@ def linear_lora_backward(dY, X, P: PackedWeight, A, B, ids, U, scaling=None, gra
     if need[2] and U is None:
         raise ValueError("dB needs U of the forward pass")
     U = None if U is None else U.contiguous()
-    grad_dtype = grad_dtype or torch.bfloat16
-    gd = {torch.float32: F32, torch.bfloat16: BF16}[grad_dtype]
     dX = torch.empty_like(X) if need[0] else None
     dA = torch.empty_like(A, dtype=grad_dtype) if need[1] else None
     dB = torch.empty_like(B, dtype=grad_dtype) if need[2] else None
@@ -717,7 +749,9 @@ def token_logprobs(logits, targets=None, top: int = 0) -> TokenLogprobs:
     a padded buffer), in one pass.  targets is int32 or int64 [M]; a value outside
     [0, V) is left out (log p 0, no gradient).  -inf logits have p = 0; a row of -inf
     only gives -inf and entropy 0, one with NaN or +inf gives NaN and ids -1."""
-    import torch
+    r = _done(_calls().token_logprobs(logits, targets, top), "token_logprobs")
+    if r is not None:
+        return TokenLogprobs(*r)
     z, dt, ld = _logits(logits)
     M, V = z.shape
     targets = _targets(targets, M, V, z.device)
@@ -734,6 +768,11 @@ def token_logprobs_backward(logits, targets, stats, entropy, dlogp=None, dentrop
     dlogp (onehot(target) - p) - dentropy p (log p + entropy).  ``out`` may be the logits
     themselves (rows in place) or a tensor that does not overlap them."""
     import torch
+    if out is None:
+        r = _done(_calls().token_logprobs_backward(logits, targets, stats, entropy, dlogp, dentropy),
+                  "token_logprobs_backward")
+        if r is not None:
+            return r
     z, dt, ld = _logits(logits)
     M, V = z.shape
     targets = _targets(targets, M, V, z.device)

@@ -71,6 +71,7 @@ SIGNATURES = {
     "sherry_linear_lora": (i32, [vp, i64, i64, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp, i32, vp, sz,
                                  vp]),
     "sherry_linear_lora_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, i32, i32]),
+    "sherry_linear_lora_needs_tickets": (i32, [i64, i64, i64, i32, i32]),
     "sherry_linear_lora_backward": (i32, [vp, vp, i64, i64, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp,
                                           vp, vp, i32, vp, sz, vp]),
     "sherry_linear_lora_backward_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),

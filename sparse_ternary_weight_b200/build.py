@@ -16,6 +16,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libsherry.so")
 OBJ = os.path.join(ROOT, "_build")
+BINDING = os.path.join(HERE, "_binding.so")
 
 SOURCES = ["api.cu", "quantize.cu", "unpack.cu", "gemv.cu", "gemv_stream.cu", "gemv_mma.cu", "gemv_tc.cu", "prefill.cu", "noalloc.cu", "tequila.cu", "lora.cu",
            "lora_few.cu", "dgrad.cu", "logprobs.cu"]
@@ -56,7 +57,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc(), *ARCH, "-shared", "-o", OUT + ".tmp", *objs, "-lcudart"]
         subprocess.run(cmd, check=True)
         os.replace(OUT + ".tmp", OUT)
+    _build_binding(force)
     return OUT
+
+
+def _build_binding(force: bool) -> None:
+    """The host-side module of ordinary calls on torch tensors (csrc/binding.cpp), for the
+    installed torch; linked against libsherry.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    src = os.path.join(CSRC, "binding.cpp")
+    if not (force or _stale(BINDING, [src, os.path.join(ROOT, "include", "sherry.h"), torch.version.__file__, __file__])):
+        return
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    dirs = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), *include_paths()]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(a for d in dirs for a in ("-isystem", d)), src, OUT, "-o", BINDING + ".tmp", "-Wl,-rpath,$ORIGIN",
+           f"-Wl,-rpath,{libs}", "-L", libs, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    subprocess.run(cmd, check=True)
+    os.replace(BINDING + ".tmp", BINDING)
 
 
 if __name__ == "__main__":

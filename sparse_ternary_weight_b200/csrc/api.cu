@@ -608,7 +608,7 @@ struct LoraWs {
 // bf16 terms of U or P: 16 bits under a bf16 result, all 24 under an fp32 one
 static int lora_terms(int dtype) { return dtype == SHERRY_BF16 ? 2 : 3; }
 
-// The linear's own workspace comes first and always keeps the ticket region to itself.
+// The linear's own workspace, tickets first, comes before the rest.
 static LoraWs lora_ws(const ProbShape& s, int64_t M, int n_adapters, int rank, int y_dtype) {
     LoraWs w{};
     const LoraRoute r = lora_route(s, M);
@@ -642,6 +642,11 @@ size_t sherry_linear_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int g
     if (check_shape(N, K) || check_gran(K, granularity, group) || check_lora(M, n_adapters, rank) || M == 0 || N == 0)
         return 0;
     return lora_ws(ProbShape{N, K, granularity, group}, M, n_adapters, rank, y_dtype).total;
+}
+
+int sherry_linear_lora_needs_tickets(int64_t M, int64_t N, int64_t K, int granularity, int group) {
+    if (check_shape(N, K) || check_gran(K, granularity, group) || M <= 0 || N == 0) return 0;
+    return lora_route(ProbShape{N, K, granularity, group}, M) == LoraRoute::kPlain;
 }
 
 int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const uint32_t* idx, const uint8_t* sgn,

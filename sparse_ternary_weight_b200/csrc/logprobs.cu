@@ -19,13 +19,14 @@
 // does not matter.  Rows of many equal values overflow the list and are gone through
 // once more with a rising threshold.
 //
-// Rows whose maximum is beyond +-1e38 (masks of the type's lowest value
-// everywhere) would overflow m L and take a second pass with z - m first.  All
-// -inf: log p = -inf, H = 0.  NaN or +inf in a row: NaN, and no tokens (-1).
+// m L is rounded by up to 2^-24 of itself, so rows whose maximum is beyond +-1e8 (masks of
+// a huge value everywhere) would leave fp32's range by 2^(m L - r) and take a
+// second pass with z - m first.  All -inf: log p = -inf, H = 0.  NaN or +inf in a row: NaN, and no tokens (-1).
 //
 // Backward (k_logprobs_bwd): elementwise, one read and one write; the rows of
 // the output may be aligned differently from those of the input, in which case a
-// thread joins two aligned vectors of the input into one of the output.
+// thread joins two aligned vectors of the input into one of the output.  Both go past
+// the caches as streams (2048 x 128256 bf16: 186 -> 172 us, floor 163).
 // Both are bound by HBM.
 #include "common.cuh"
 #include "lut.cuh"
@@ -46,7 +47,8 @@ constexpr int kLpRefine = 96;    // keys beyond the wanted ones that make a cut 
 constexpr int kLpMaxTop = SHERRY_MAX_TOP;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kEdge = 1e38f;   // row maxima beyond this overflow m * log2(e) or come near it
+constexpr float kEdge = 1e8f;    // row maxima beyond this: 2^(m L - r), up to 2^9 here, would leave fp32's range
+static_assert(8 * kLpMaxTop <= kLpCap, "the cluster's best fit the list");
 static_assert(kLpMaxTop <= 32, "the first threshold is a bound of the 32nd largest");
 
 struct LpParams {
@@ -70,11 +72,52 @@ __device__ __forceinline__ float ex2(float x) {
 // r = rn(m L): the product must be rounded by itself everywhere, never inside a fused multiply-add
 __device__ __forceinline__ float ref_of(float m) { return __fmul_rn(fmaxf(m, -kEdge), kLog2e); }
 
+// two floats side by side: one instruction for both
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    return ((uint64_t)__float_as_uint(y) << 32) | __float_as_uint(x);
+}
+__device__ __forceinline__ float lo_of(uint64_t p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float hi_of(uint64_t p) { return __uint_as_float((uint32_t)(p >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Elements below kFloor count as kFloor: 0 * -inf would be NaN in the weighted sum, while 2^(kFloor L - r)
+// is 0 for every r of a row that is not at the edge (its maximum is above -kEdge), and kFloor L - r finite.
+constexpr float kFloor = -2e8f;
+
 template <typename T>
 struct LpVec;
 template <>
 struct LpVec<__nv_bfloat16> {
     static constexpr int N = 8;
+    // the largest element (NaN only where all are)
+    static __device__ __forceinline__ float max(uint4 v) {
+        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+        return fmaxf(bf16lo(m), bf16hi(m));
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    // the elements as pairs, raised to kFloor (NaN stays)
+    static __device__ __forceinline__ void pairs(uint4 v, uint64_t* p) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t c;
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(w[i]), "r"(0xcd3fcd3fu));  // bf16(kFloor)
+            p[i] = pair(bf16lo(c), bf16hi(c));
+        }
+    }
     static __device__ __forceinline__ void unpack(uint4 v, float* f) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -99,6 +142,17 @@ struct LpVec<__nv_bfloat16> {
 template <>
 struct LpVec<float> {
     static constexpr int N = 4;
+    static __device__ __forceinline__ float max(uint4 v) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    static __device__ __forceinline__ void pairs(uint4 v, uint64_t* p) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %1, %2;" : "=f"(c[i]) : "f"(__uint_as_float(w[i])), "f"(kFloor));
+        p[0] = pair(c[0], c[1]);
+        p[1] = pair(c[2], c[3]);
+    }
     static __device__ __forceinline__ void unpack(uint4 v, float* f) {
         f[0] = __uint_as_float(v.x);
         f[1] = __uint_as_float(v.y);
@@ -135,31 +189,23 @@ __device__ __forceinline__ uint4 lp_load(const T* row, int e0, int V) {
     return LpVec<T>::pack(f);
 }
 
-// the largest element of a vector
-template <typename T>
-__device__ __forceinline__ float lp_max(uint4 v) {
-    float f[LpVec<T>::N];
-    LpVec<T>::unpack(v, f);
-    float m = f[0];
-#pragma unroll
-    for (int j = 1; j < LpVec<T>::N; ++j) m = fmaxf(m, f[j]);
-    return m;
-}
-
+template <int TH>
 struct LpTop {  // shared state of the likeliest tokens
-    float tmax[kLpThreads];    // the threads' maxima
-    uint64_t buf[kLpCap];
+    float tmax[TH];    // the threads' maxima
+    static constexpr int kCap = kLpCap / kLpThreads * TH;  // candidate keys held
+    uint64_t buf[kCap];
     uint64_t best[kLpMaxTop];
     uint64_t thr;
-    uint8_t list[kLpThreads];  // threads that hold candidates
+    uint8_t list[TH];  // threads that hold candidates
     int cnt, listed;
 };
 
 // The `k` largest of buf[0..n), in order, into best (0 where there are fewer).
-__device__ __forceinline__ void lp_rank(LpTop& s, int n, int k) {
+template <int TH>
+__device__ __forceinline__ void lp_rank(LpTop<TH>& s, int n, int k) {
     if ((int)threadIdx.x < k) s.best[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kLpThreads) {
+    for (int i = threadIdx.x; i < n; i += TH) {
         const uint64_t me = s.buf[i];
         int r = 0;
         for (int j = 0; j < n; ++j) r += s.buf[j] > me;
@@ -169,8 +215,8 @@ __device__ __forceinline__ void lp_rank(LpTop& s, int n, int k) {
 }
 
 // Append a vector's keys at or above the threshold; elements [0, hi) of the row count.
-template <typename T>
-__device__ __forceinline__ void lp_push(LpTop& s, uint4 x, int e0, int hi, uint64_t thr, float tv) {
+template <typename T, int TH>
+__device__ __forceinline__ void lp_push(LpTop<TH>& s, uint4 x, int e0, int hi, uint64_t thr, float tv) {
     float f[LpVec<T>::N];
     LpVec<T>::unpack(x, f);
 #pragma unroll
@@ -180,7 +226,7 @@ __device__ __forceinline__ void lp_push(LpTop& s, uint4 x, int e0, int hi, uint6
             const uint64_t key = lp_key(f[j], e);
             if (key >= thr) {
                 const int at = atomicAdd(&s.cnt, 1);
-                if (at < kLpCap) s.buf[at] = key;
+                if (at < LpTop<TH>::kCap) s.buf[at] = key;
             }
         }
     }
@@ -189,8 +235,8 @@ __device__ __forceinline__ void lp_push(LpTop& s, uint4 x, int e0, int hi, uint6
 // Append one iteration's keys, after which the list is whole: where more keys pass than it holds,
 // the threshold rises to the k-th best of those held (each is in the row, so that is a bound) and
 // the iteration's are appended again.  A long list is cut back to its best.  Called by all threads.
-template <typename T>
-__device__ __noinline__ void lp_collect(LpTop& s, const uint4 (&xs)[kLpVecs], int v, int v1, int off, int V, int k) {
+template <typename T, int TH>
+__device__ __noinline__ void lp_collect(LpTop<TH>& s, const uint4 (&xs)[kLpVecs], int v, int v1, int off, int V, int k) {
     constexpr int N = LpVec<T>::N;
     const int held = s.cnt;
     __syncthreads();
@@ -198,13 +244,13 @@ __device__ __noinline__ void lp_collect(LpTop& s, const uint4 (&xs)[kLpVecs], in
         const uint64_t thr = s.thr;
         const float tv = lp_unorder((uint32_t)(thr >> 32));
         for (int u = 0; u < kLpVecs; ++u)
-            if (v + u * kLpThreads < v1 && lp_max<T>(xs[u]) >= tv)
-                lp_push<T>(s, xs[u], off + N * (v + u * kLpThreads), V, thr, tv);
+            if (v + u * TH < v1 && LpVec<T>::max(xs[u]) >= tv)
+                lp_push<T, TH>(s, xs[u], off + N * (v + u * TH), V, thr, tv);
         __syncthreads();
         const int n = s.cnt;
-        const bool over = n > kLpCap;
+        const bool over = n > LpTop<TH>::kCap;
         if (over || n > k + kLpRefine) {
-            lp_rank(s, min(n, kLpCap), k);
+            lp_rank(s, min(n, LpTop<TH>::kCap), k);
             if (threadIdx.x == 0) {
                 s.thr = max(s.thr, s.best[k - 1]);
                 s.cnt = over ? held : k;
@@ -216,8 +262,9 @@ __device__ __noinline__ void lp_collect(LpTop& s, const uint4 (&xs)[kLpVecs], in
     }
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
+// TH threads per CTA
+template <typename T, bool TOP, int TH>
+__global__ void __launch_bounds__(TH, 1024 / TH) k_logprobs(const LpParams P) {
     constexpr int N = LpVec<T>::N;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -226,8 +273,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
     const int V = P.V, top = TOP ? P.top : 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    __shared__ typename std::conditional<TOP, LpTop, int>::type top_s;
-    __shared__ float4 red[kLpThreads / 32];  // the warps' maxima, S, weighted sums
+    __shared__ typename std::conditional<TOP, LpTop<TH>, int>::type top_s;
+    __shared__ float4 red[TH / 32];  // the warps' maxima, S, weighted sums
     __shared__ float4 part;                  // this CTA's
 
     // the row's 16-byte vectors: vector v holds elements off + N v ..; this CTA's share is [v0, v1)
@@ -235,12 +282,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
     const int nv = (V - off + N - 1) / N;
     const int share = (nv + C - 1) / C;
     const int v0 = min(rank * share, nv), v1 = min(v0 + share, nv);
-    const int iters = (v1 - v0 + kLpThreads * kLpVecs - 1) / (kLpThreads * kLpVecs);
+    const int iters = (v1 - v0 + TH * kLpVecs - 1) / (TH * kLpVecs);
 
     auto fetch = [&](int it, uint4* x) {
 #pragma unroll
         for (int u = 0; u < kLpVecs; ++u) {
-            const int v = v0 + (it * kLpVecs + u) * kLpThreads + tid;
+            const int v = v0 + (it * kLpVecs + u) * TH + tid;
             x[u] = v < v1 ? lp_load(row, off + N * v, V)
                           : make_uint4(LpVec<T>::pad(), LpVec<T>::pad(), LpVec<T>::pad(), LpVec<T>::pad());
         }
@@ -253,34 +300,39 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
         target = P.targets[rowi];
         if (target >= 0 && target < V) zt = LpVec<T>::one(row + target);
     }
-    float m = -INFINITY, r = ref_of(-INFINITY), s1 = 0.0f, s2 = 0.0f;
+    float m = -INFINITY, r = ref_of(-INFINITY);
+    uint64_t a1 = 0, a2 = 0;  // S and the weighted sum, of even and odd elements
+    const uint64_t L2 = pair(kLog2e, kLog2e);
     uint4 x[kLpVecs];
     for (int it = 0; it < iters; ++it) {
         fetch(it, x);
         float bm = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kLpVecs; ++u) bm = fmaxf(bm, lp_max<T>(x[u]));
+        for (int u = 0; u < kLpVecs; ++u) bm = fmaxf(bm, LpVec<T>::max(x[u]));
         if (bm > m) {
             const float nr = ref_of(bm);
             const float d = fmaxf(r - nr, -1e4f), f = ex2(d);
-            s2 = f * fmaf(d, s1, s2);
-            s1 *= f;
+            const uint64_t f2 = pair(f, f);
+            a2 = fma2(f2, fma2(pair(d, d), a1, a2), 0);
+            a1 = fma2(f2, a1, 0);
             m = bm;
             r = nr;
         }
+        const uint64_t mr = pair(-r, -r);
 #pragma unroll
         for (int u = 0; u < kLpVecs; ++u) {
-            float f[N];
-            LpVec<T>::unpack(x[u], f);
+            uint64_t p[N / 2];
+            LpVec<T>::pairs(x[u], p);
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float y = fmaf(f[j], kLog2e, -r);
-                const float e = ex2(y);
-                s1 += e;
-                s2 = fmaf(e, fmaxf(y, -1e4f), s2);  // e = 0 there: 0 * -inf would be NaN
+            for (int j = 0; j < N / 2; ++j) {
+                const uint64_t y = fma2(p[j], L2, mr);
+                const uint64_t e = pair(ex2(lo_of(y)), ex2(hi_of(y)));
+                a1 = add2(a1, e);
+                a2 = fma2(e, y, a2);
             }
         }
     }
+    float s1 = lo_of(a1) + hi_of(a1), s2 = lo_of(a2) + hi_of(a2);
     if constexpr (TOP) {
         // a value that k of the threads' maxima reach bounds the k-th largest element from below, and
         // only threads whose maximum reaches it hold an element that does
@@ -289,15 +341,15 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
         __syncthreads();
         if (warp == 0) {
             // the largest value of 16 leading bits that at least k of the maxima reach, bit by bit
-            uint32_t o[8], t = 0;
+            uint32_t o[TH / 32], t = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = lp_order(top_s.tmax[lane + 32 * j]);
+            for (int j = 0; j < TH / 32; ++j) o[j] = lp_order(top_s.tmax[lane + 32 * j]);
 #pragma unroll
             for (int bit = 31; bit >= 16; --bit) {
                 const uint32_t want = t | (1u << bit);
                 int n = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) n += o[j] >= want;
+                for (int j = 0; j < TH / 32; ++j) n += o[j] >= want;
                 if (__reduce_add_sync(kFull, n) >= top) t = want;
             }
             if (lane == 0) top_s.thr = (uint64_t)max(t, lp_order(-INFINITY)) << 32;  // (below -inf: NaNs)
@@ -308,22 +360,22 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
         if (m >= tv) top_s.list[atomicAdd(&top_s.listed, 1)] = (uint8_t)tid;
         __syncthreads();
         const int per = iters * kLpVecs, total = top_s.listed * per;
-        for (int i = tid; i < total; i += kLpThreads) {
-            const int v = v0 + (i % per) * kLpThreads + top_s.list[i / per];
+        for (int i = tid; i < total; i += TH) {
+            const int v = v0 + (i % per) * TH + top_s.list[i / per];
             if (v < v1) {
                 const uint4 y = lp_load(row, off + N * v, V);
-                if (lp_max<T>(y) >= tv) lp_push<T>(top_s, y, off + N * v, V, thr, tv);
+                if (LpVec<T>::max(y) >= tv) lp_push<T, TH>(top_s, y, off + N * v, V, thr, tv);
             }
         }
         __syncthreads();
-        if (top_s.cnt > kLpCap) {  // (uniform) many equal values: again, with the threshold rising
+        if (top_s.cnt > LpTop<TH>::kCap) {  // (uniform) many equal values: again, with the threshold rising
             __syncthreads();
             if (tid == 0) top_s.cnt = 0;
             __syncthreads();
             for (int it = 0; it < iters; ++it) {
                 uint4 cx[kLpVecs];  // (not x: what a call takes by address leaves the registers)
                 fetch(it, cx);
-                lp_collect<T>(top_s, cx, v0 + it * kLpVecs * kLpThreads + tid, v1, off, V, top);
+                lp_collect<T, TH>(top_s, cx, v0 + it * kLpVecs * TH + tid, v1, off, V, top);
             }
         }
         lp_rank(top_s, top_s.cnt, top);
@@ -358,7 +410,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
             s2 += q.z;
         }
     };
-    join([&](int i) { return red[i]; }, kLpThreads / 32);
+    join([&](int i) { return red[i]; }, TH / 32);
     if (C > 1) {
         if (tid == 0) part = make_float4(bmax, s1, s2, 0.0f);
         cluster.sync();
@@ -369,7 +421,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
     if (edge) {
         // m log2(e) overflows: this row again, with z - m first
         s1 = s2 = 0.0f;
-        for (int v = v0 + tid; v < v1; v += kLpThreads) {
+        for (int v = v0 + tid; v < v1; v += TH) {
             float f[N];
             LpVec<T>::unpack(lp_load(row, off + N * v, V), f);
 #pragma unroll
@@ -389,7 +441,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
         if (lane == 0) red[warp] = make_float4(0.0f, s1, s2, 0.0f);
         __syncthreads();
         s1 = s2 = 0.0f;
-        for (int w = 0; w < kLpThreads / 32; ++w) {
+        for (int w = 0; w < TH / 32; ++w) {
             s1 += red[w].y;
             s2 += red[w].z;
         }
@@ -424,14 +476,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
             P.stats[2 * rowi + 1] = lsum;
         }
         if constexpr (TOP) {
-            // every CTA's best are in its shared memory; a key's place is the number of larger ones
-            for (int i = tid; i < C * top; i += kLpThreads) {
-                const uint64_t me = cluster.map_shared_rank(&top_s.best[0], i / top)[i % top];
+            // every CTA's best, brought here; a key's place is the number of larger ones
+            const int all = C * top;
+            __syncthreads();
+            for (int i = tid; i < all; i += TH)
+                top_s.buf[i] = cluster.map_shared_rank(&top_s.best[0], i / top)[i % top];
+            __syncthreads();
+            for (int i = tid; i < all; i += TH) {
+                const uint64_t me = top_s.buf[i];
                 int place = 0;
-                for (int c = 0; c < C; ++c) {
-                    const uint64_t* other = cluster.map_shared_rank(&top_s.best[0], c);
-                    for (int j = 0; j < top; ++j) place += other[j] > me;
-                }
+#pragma unroll 4
+                for (int j = 0; j < all; ++j) place += top_s.buf[j] > me;
                 if (me != 0 && place < top && !bad) {
                     const float zt = lp_unorder((uint32_t)(me >> 32));
                     P.top_ids[rowi * top + place] = (int32_t)~(uint32_t)me;
@@ -439,7 +494,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const LpParams P) {
                 }
             }
             if (bad) {
-                for (int i = tid; i < top; i += kLpThreads) {
+                for (int i = tid; i < top; i += TH) {
                     P.top_ids[rowi * top + i] = -1;
                     P.top_logp[rowi * top + i] = NAN;
                 }
@@ -493,8 +548,8 @@ __device__ __forceinline__ uint4 lp_join(uint4 a, uint4 b, int shift) {
                       __funnelshift_r(o[2], o[3], bits), __funnelshift_r(o[3], o[4], bits));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) k_logprobs_bwd(const LpBwdParams P) {
+template <typename T, int TH>
+__global__ void __launch_bounds__(TH) k_logprobs_bwd(const LpBwdParams P) {
     constexpr int N = LpVec<T>::N;
     const int64_t rowi = blockIdx.x / P.segs;
     const int seg = (int)(blockIdx.x % P.segs);
@@ -506,17 +561,17 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs_bwd(const LpBwdParams P
     const int off = -(int)((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T));
     const int shift = (int)(((reinterpret_cast<uintptr_t>(row) & 15u) + 16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u);
     const int nv = (V - off + N - 1) / N;
-    const int vb = seg * (kLpThreads * kLpBwdVecs) + threadIdx.x;
+    const int vb = seg * (TH * kLpBwdVecs) + threadIdx.x;
 
     uint4 x[kLpBwdVecs];
 #pragma unroll
     for (int u = 0; u < kLpBwdVecs; ++u) {
-        const int v = vb + u * kLpThreads;
+        const int v = vb + u * TH;
         const int e0 = off + N * v;
         const int lead = shift / (int)sizeof(T);
         if (v < nv) {
             if (shift == 0) {
-                x[u] = lp_load(row, e0, V);
+                x[u] = (e0 >= 0 && e0 + N <= V) ? __ldcs(reinterpret_cast<const uint4*>(row + e0)) : lp_load(row, e0, V);
             } else if (e0 - lead >= 0 && e0 - lead + 2 * N <= V) {
                 const uint4* p = reinterpret_cast<const uint4*>(row + e0 - lead);
                 x[u] = lp_join(p[0], p[1], shift);
@@ -538,7 +593,7 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs_bwd(const LpBwdParams P
     const float H = P.dentropy ? P.entropy[rowi] : 0.0f;
 #pragma unroll
     for (int u = 0; u < kLpBwdVecs; ++u) {
-        const int v = vb + u * kLpThreads;
+        const int v = vb + u * TH;
         if (v >= nv) break;
         const int e0 = off + N * v;
         float f[N];
@@ -552,7 +607,7 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs_bwd(const LpBwdParams P
             if (e0 + j == t) f[j] += g;
         }
         if (e0 >= 0 && e0 + N <= V) {
-            *reinterpret_cast<uint4*>(out + e0) = LpVec<T>::pack(f);
+            __stcs(reinterpret_cast<uint4*>(out + e0), LpVec<T>::pack(f));
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j)
@@ -563,18 +618,18 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs_bwd(const LpBwdParams P
 
 // ---- host ---------------------------------------------------------------------------
 
-template <typename T>
-static int lp_launch(const LpParams& P, int64_t M, int sms, cudaStream_t stream) {
+template <typename T, int TH>
+static int lp_launch_th(const LpParams& P, int64_t M, int sms, cudaStream_t stream) {
     // CTAs per row: several while there are fewer rows than SMs to share them, as long as each CTA
     // has a full iteration of vectors.  A cluster's launch and joins cost more than an idle slot:
     // 128256 bf16, top 8: 64 rows 18.5 / 11.5 / 13.0 us with 1 / 4 / 8 CTAs, 600 rows 52 / 55 with 1 / 2
-    const int64_t iters = (P.V / LpVec<T>::N + kLpThreads * kLpVecs - 1) / (kLpThreads * kLpVecs);
+    const int64_t iters = (P.V / LpVec<T>::N + TH * kLpVecs - 1) / (TH * kLpVecs);
     int c = 1;
-    while (c < 8 && 2 * M * c < 3 * (int64_t)sms && c < iters) c *= 2;
+    while (TH == kLpThreads && c < 8 && 2 * M * c < 3 * (int64_t)sms && c < iters) c *= 2;
     if (M * c > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(M * c));
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(TH);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -583,10 +638,21 @@ static int lp_launch(const LpParams& P, int64_t M, int sms, cudaStream_t stream)
     cfg.attrs = &at;
     cfg.numAttrs = c > 1;
     if (P.top > 0)
-        SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, true>, P));
+        SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, true, TH>, P));
     else
-        SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, false>, P));
+        SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, false, TH>, P));
     return SHERRY_OK;
+}
+
+template <typename T>
+static int lp_launch(const LpParams& P, int64_t M, int sms, cudaStream_t stream) {
+    // Threads per CTA: a row's joins cost the more the more threads take part, and short rows leave most of
+    // them idle.  top 8, 64 / 128 / 256 threads in us: bf16 4096 x 2000 15 / 22 / 41, 4096 x 16000 41 / 44 / 58,
+    // 4096 x 32000 76 / 69 / 80, 1000 x 4000 7.9 / 7.1 / 12.6, 1000 x 32000 25 / 19 / 21, 300 x 32000 19 / 12.2 / 10.5
+    const int64_t bytes = P.V * (int64_t)sizeof(T);
+    if (M >= 2048 && bytes <= 32 * 1024) return lp_launch_th<T, 64>(P, M, sms, stream);
+    if (bytes <= (M >= 512 ? 64 : 16) * 1024) return lp_launch_th<T, 128>(P, M, sms, stream);
+    return lp_launch_th<T, kLpThreads>(P, M, sms, stream);
 }
 
 int token_logprobs_launch(const void* z, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets, int top,
@@ -596,20 +662,29 @@ int token_logprobs_launch(const void* z, int dtype, int64_t M, int64_t V, int64_
     return dtype == SHERRY_BF16 ? lp_launch<__nv_bfloat16>(P, M, sms, stream) : lp_launch<float>(P, M, sms, stream);
 }
 
+template <typename T, int TH>
+static int bwd_launch_th(LpBwdParams P, int64_t M, cudaStream_t stream) {
+    // a row that starts inside a vector has one more of them
+    const int64_t segs = (P.V / LpVec<T>::N + 2 + TH * kLpBwdVecs - 1) / (TH * kLpBwdVecs);
+    if (M * segs > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
+    P.segs = (int)segs;
+    k_logprobs_bwd<T, TH><<<(unsigned)(M * segs), TH, 0, stream>>>(P);
+    SHERRY_LAUNCH_CHECK();
+    return SHERRY_OK;
+}
+
+template <typename T>
+static int bwd_launch(const LpBwdParams& P, int64_t M, cudaStream_t stream) {
+    // small CTAs waste the fewest threads at a row's end (bf16 20000 x 2000: 31 / 35 / 47 us with 64 / 128 / 256
+    // threads, 2048 x 128256: 172 / 173 / 176); few rows want wide ones (fp32 300 x 1000: 3.0 / 2.5 / 2.3)
+    return M >= 1024 ? bwd_launch_th<T, 64>(P, M, stream) : bwd_launch_th<T, 128>(P, M, stream);
+}
+
 int token_logprobs_bwd_launch(const void* z, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
                               const float* stats, const float* entropy, const float* dlogp, const float* dentropy,
                               void* out, int64_t ldo, cudaStream_t stream) {
-    const int n = dtype == SHERRY_BF16 ? 8 : 4;
-    // a row that starts inside a vector has one more of them
-    const int64_t segs = (V / n + 2 + kLpThreads * kLpBwdVecs - 1) / (kLpThreads * kLpBwdVecs);
-    if (M * segs > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
-    const LpBwdParams P{z, ld, targets, stats, entropy, dlogp, dentropy, out, ldo, (int)V, (int)segs};
-    if (dtype == SHERRY_BF16)
-        k_logprobs_bwd<__nv_bfloat16><<<(unsigned)(M * segs), kLpThreads, 0, stream>>>(P);
-    else
-        k_logprobs_bwd<float><<<(unsigned)(M * segs), kLpThreads, 0, stream>>>(P);
-    SHERRY_LAUNCH_CHECK();
-    return SHERRY_OK;
+    const LpBwdParams P{z, ld, targets, stats, entropy, dlogp, dentropy, out, ldo, (int)V, 0};
+    return dtype == SHERRY_BF16 ? bwd_launch<__nv_bfloat16>(P, M, stream) : bwd_launch<float>(P, M, stream);
 }
 
 }  // namespace sherry

@@ -121,6 +121,49 @@ def test_forward(sw, shape, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2100, 701, 8), (2050, 4003, 20), (2048, 33, 32), (600, 9001, 20), (1100, 31, 5)],
+                         ids=lambda s: f"{s[0]}x{s[1]}-top{s[2]}")
+def test_forward_of_many_short_rows(sw, shape, dt):
+    """The forms with fewer threads per row, odd lengths and alignments."""
+    import torch
+    M, V, top = shape
+    T = torch.float32 if dt == "f32" else torch.bfloat16
+    for pad, off, coarse in ((0, 0, False), (3, 1, True)):
+        buf, z, t = make(M, V, T, pad, off, seed=pad, coarse=coarse)
+        check(sw, z, t, top)
+        check(sw, z, t, 0)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_extremes_in_many_short_rows(sw, dt):
+    import torch
+    T = torch.float32 if dt == "f32" else torch.bfloat16
+    V = 1003
+    low, high = torch.finfo(T).min, torch.finfo(T).max
+    z = (2 * torch.randn((8, V), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")).to(T)
+    z[0] = -math.inf
+    z[1] = low
+    z[2, 1:] = low
+    z[3, ::2] = -math.inf
+    z[4] = high
+    z[5] = -1.05e38          # between the rows' edge and the floor of their elements
+    z[5, 7] = -1.0e38
+    z[6] = -1.2e38
+    z[6, :3] = 0.0
+    z[7] = 0.0
+    t = torch.tensor([3, 3, 0, 1, 9, 7, 500, V - 1], dtype=torch.int32, device="cuda")
+    check(sw, z, t, 20)
+    far = torch.stack([x + z[7] * 0 + s for s in (-1e10, 1e10, -1e9, 1e9, -0.99e8, 1.01e8, -2.1e8, -1e30)
+                       for x in [torch.zeros(V, device="cuda", dtype=T)]])
+    far[:, ::5] *= 2          # a whole row far away, its elements further still
+    check(sw, far, t, 20)
+    z = torch.cat([z, far])
+    t = t.repeat(2)
+    for n in (50, 150):
+        check(sw, z.repeat(n, 1), t.repeat(n), 20)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_ties_and_orders(sw, dt):
     """All equal, few distinct values, ascending and descending rows: every element or none
     passes the running threshold; ties go to the lowest index."""

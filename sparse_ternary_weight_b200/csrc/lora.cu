@@ -205,6 +205,7 @@ __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, con
 __global__ void __launch_bounds__(kPlanThreads) k_lora_plan(const int32_t* ids, int M, int n_adapters,
                                                             const LoraPlan plan) {
     pdl_trigger();
+    pdl_wait();
     if (blockIdx.x == 0) {
         plan_slots(ids, M, n_adapters, plan);
         return;
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_lora_plan(const int32_t* ids, 
 
 int lora_plan_launch(const int32_t* ids, int64_t M, int n_adapters, const LoraPlan& plan, cudaStream_t stream) {
     const unsigned grid = plan.may_permute ? (unsigned)n_adapters + 2u : 1u;
-    return launch_after(k_lora_plan, grid, kPlanThreads, 0, stream, 1, false, ids, (int)M, n_adapters, plan);
+    return launch_after(k_lora_plan, grid, kPlanThreads, 0, stream, 1, true, ids, (int)M, n_adapters, plan);
 }
 
 // ---- rows in the plan's order, or with an aligned length ------------------------------

@@ -33,6 +33,7 @@ struct FewParams {
 
 __global__ void __launch_bounds__(128) k_lora_down_few(const FewParams P) {
     pdl_trigger();
+    pdl_wait();
     __shared__ float red[4][4];
     const int m = blockIdx.y, r0 = 4 * blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -319,9 +320,7 @@ static int few_launch(const FewUpParams& P, int scale, dim3 grid, cudaStream_t s
 int lora_down_few_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, const uint16_t* A, int R,
                          const int32_t* ids, const float* scaling, int n_adapters, float* U, cudaStream_t stream) {
     const FewParams D{d.X, A, scaling, ids, U, (int)M, (int)s.K, R, n_adapters};
-    k_lora_down_few<<<dim3((unsigned)(R / 4), (unsigned)M), 128, 0, stream>>>(D);
-    SHERRY_LAUNCH_CHECK();
-    return SHERRY_OK;
+    return launch_after(k_lora_down_few, dim3((unsigned)(R / 4), (unsigned)M), 128, 0, stream, 1, true, D);
 }
 
 int lora_few_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16, const uint16_t* A,

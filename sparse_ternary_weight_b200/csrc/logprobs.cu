@@ -30,6 +30,7 @@
 // Both are bound by HBM.
 #include "common.cuh"
 #include "lut.cuh"
+#include "tc.cuh"
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -266,6 +267,7 @@ __device__ __noinline__ void lp_collect(LpTop<TH>& s, const uint4 (&xs)[kLpVecs]
 template <typename T, bool TOP, int TH>
 __global__ void __launch_bounds__(TH, 1024 / TH) k_logprobs(const LpParams P) {
     constexpr int N = LpVec<T>::N;
+    pdl_wait();
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int64_t rowi = blockIdx.x / C;
@@ -551,6 +553,7 @@ __device__ __forceinline__ uint4 lp_join(uint4 a, uint4 b, int shift) {
 template <typename T, int TH>
 __global__ void __launch_bounds__(TH) k_logprobs_bwd(const LpBwdParams P) {
     constexpr int N = LpVec<T>::N;
+    pdl_wait();
     const int64_t rowi = blockIdx.x / P.segs;
     const int seg = (int)(blockIdx.x % P.segs);
     const T* row = reinterpret_cast<const T*>(P.z) + rowi * P.ld;
@@ -627,21 +630,8 @@ static int lp_launch_th(const LpParams& P, int64_t M, int sms, cudaStream_t stre
     int c = 1;
     while (TH == kLpThreads && c < 8 && 2 * M * c < 3 * (int64_t)sms && c < iters) c *= 2;
     if (M * c > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(M * c));
-    cfg.blockDim = dim3(TH);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)c;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = c > 1;
-    if (P.top > 0)
-        SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, true, TH>, P));
-    else
-        SHERRY_CUDA_CHECK(cudaLaunchKernelEx(&cfg, k_logprobs<T, false, TH>, P));
-    return SHERRY_OK;
+    auto kernel = P.top > 0 ? k_logprobs<T, true, TH> : k_logprobs<T, false, TH>;
+    return launch_after(kernel, (unsigned)(M * c), TH, 0, stream, c, true, P);
 }
 
 template <typename T>
@@ -668,9 +658,7 @@ static int bwd_launch_th(LpBwdParams P, int64_t M, cudaStream_t stream) {
     const int64_t segs = (P.V / LpVec<T>::N + 2 + TH * kLpBwdVecs - 1) / (TH * kLpBwdVecs);
     if (M * segs > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     P.segs = (int)segs;
-    k_logprobs_bwd<T, TH><<<(unsigned)(M * segs), TH, 0, stream>>>(P);
-    SHERRY_LAUNCH_CHECK();
-    return SHERRY_OK;
+    return launch_after(k_logprobs_bwd<T, TH>, (unsigned)(M * segs), TH, 0, stream, 1, true, P);
 }
 
 template <typename T>

@@ -688,6 +688,7 @@ int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const
         down.ids = ids;
         down.scaling = scaling;
         down.V = u;
+        if (pre) down.beside_ctas = prefill_lora_ctas(s, M, sms);
         if (pre) down.img = LoraImage{reinterpret_cast<uint16_t*>(ws + w.img), lora_rp(rank), lora_terms(y_dtype)};
         if ((st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs))) return st;
         if (pre)
@@ -826,6 +827,8 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     const LoraImage imgu{reinterpret_cast<uint16_t*>(ws + w.imgu), lora_rp(rank), terms};
     LoraDown down{};
     down.ids = ids;
+    const ProbShape s{N, K, granularity, group};
+    if (dX) down.beside_ctas = dgrad_ctas(M, N, K, sms);
     if (dX || dA) {
         down.G = G;
         down.Gp = Gp;
@@ -843,7 +846,6 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     }
     if ((st = lora_down_launch(down, M, rank, n_adapters, plan, sms, cs))) return st;
     const LoraGradArgs args{A, imgp, Gp, rank, n_adapters, plan};
-    const ProbShape s{N, K, granularity, group};
     if (dX && (st = dgrad_launch(s, idx, sgn, scales, G, ld, M, dX, &args, ws + w.part, sms, cs))) return st;
     LoraGradJob jobs[2];
     int count = 0;

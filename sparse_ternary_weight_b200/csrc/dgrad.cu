@@ -160,9 +160,12 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    if constexpr (LORA) {
+    // LORA: the plan, and dY in its order, are ready when this kernel is launched (k_lora_down lets it
+    // start only then); P's image is waited for where it is loaded.  The adapters' gradients, launched
+    // next, may start as soon as the image is there.
+    if (LORA && warp == kGTmaWarp && lane == 1) {
         pdl_wait();
-        pdl_trigger();  // only now: the next kernel reads what this one has waited for
+        pdl_trigger();
     }
     const bool permuted = LORA && P.plan.may_permute && P.plan.head[0] != 0;
 
@@ -317,6 +320,7 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
                     if (++s == ST) { s = 0; ph ^= 1u; }
                 }
                 if constexpr (LORA) {
+                    if (it.sl0 < it.sl1) pdl_wait();
                     for (int sl = it.sl0; sl < it.sl1 && ok; ++sl) {
                         const int a = P.plan.slot_a[sl];
                         for (int u = 0; u < rblocks * tstages; ++u) {
@@ -455,6 +459,11 @@ static GPlan dgrad_plan(int64_t M, int64_t N, int64_t K, int sms) {
 size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int sms) {
     const GPlan g = dgrad_plan(M, N, K, sms);
     return g.splits > 1 ? (size_t)g.splits * (size_t)(M * K) * sizeof(float) : 0;
+}
+
+int64_t dgrad_ctas(int64_t M, int64_t N, int64_t K, int sms) {
+    const GPlan g = dgrad_plan(M, N, K, sms);
+    return std::min<int64_t>((int64_t)g.mtiles * g.ktiles * g.splits, sms);
 }
 
 int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, const float* scales, const uint16_t* dY,

@@ -419,8 +419,8 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
                      "r"(cols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // only now: the next kernel reads the plan and the rows in its order at once, and waits for the rest
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -585,8 +585,11 @@ int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const 
         if (d.Gp && (st = encode_2d(&gpmap, d.Gp, d.ldg, M, kLoraTile))) return st;
         st = d.by_row ? encode_3d(&wmap, d.W, R, d.C, n_adapters, 64) : encode_3d(&wmap, d.W, d.C, R, n_adapters, P.rp);
         if (st) return st;
-        // the sum is split until the slots fill the SMs once
-        while (cl < 8 && est * cl * 2 <= sms && steps >= 8 * cl) cl *= 2;
+        // the sum is split until the slots fill the SMs once; or, where that still gives each slot four
+        // CTAs, the SMs that the next kernel, which starts beside this one, leaves (331 x 2050 x 8192, rank
+        // 8: 51 -> 43 us; with one CTA per slot 1000 x 2048 x 8192, rank 16, backward: 72 -> 78)
+        const int64_t room = d.beside_ctas + 4 * est <= sms ? sms - d.beside_ctas : sms;
+        while (cl < 8 && est * cl * 2 <= room && steps >= 8 * cl) cl *= 2;
     }
     P.stage_bytes = kDnG + (d.by_row ? (P.rp + 63) / 64 * 64 * 128 : (P.rp * 128 + 1023) / 1024 * 1024);
     P.stages = std::min(kDnMaxStages, (kDnHalf - 2048) / P.stage_bytes);

@@ -67,6 +67,8 @@ struct LoraArgs {
 int prefill_lora_launch(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16, const LoraArgs& lora,
                         cudaStream_t stream);
 
+int64_t prefill_lora_ctas(const ProbShape& s, int64_t M, int sms);  // of that launch
+
 // What the input-gradient kernel needs to add P A_a
 struct LoraGradArgs {
     const uint16_t* A;   // bf16 [n_adapters][R][K]
@@ -75,6 +77,7 @@ struct LoraGradArgs {
     int R, n_adapters;
     LoraPlan plan;
 };
+int64_t dgrad_ctas(int64_t M, int64_t N, int64_t K, int sms);
 // dX = dY (T alpha) (+ P A_a): dY bf16 rows ldy apart (a multiple of 8), lora null for the plain gradient (dgrad.cu)
 size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int sms);
 int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, const float* scales, const uint16_t* dY,
@@ -117,6 +120,7 @@ struct LoraDown {
     LoraImage img;       // data may be null
     const float* V2;     // or null
     LoraImage img2;
+    int64_t beside_ctas; // CTAs (one per SM) of the kernel that follows
 };
 int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const LoraPlan& plan, int sms,
                      cudaStream_t stream);

@@ -35,6 +35,8 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 namespace cg = cooperative_groups;
 
 namespace sherry {
@@ -195,7 +197,8 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    if constexpr (LORA) pdl_wait();
+    // LORA: the plan, and X in its order, are ready when this kernel is launched (k_lora_down lets it
+    // start only then); U's image and the slots' masks are waited for where they are read
     const bool permuted = LORA && P.plan.may_permute && P.plan.head[0] != 0;
     // the slots of tile t; every role loads them at the tile's start and uses them at its end
     auto slots_of = [&](int t) {
@@ -215,10 +218,10 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             const int n = (t % ntn) * kPBM + q * 32 + lane;
             const int m0 = (t / ntn) * kPBN + half * kCols;
             const int2 sl = slots_of(t);
-            uint32_t own0[kCols / 32];  // the first slot's tokens among this thread's
+            uint32_t own0[kCols / 32];  // the first slot's tokens among this thread's, once they are there
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c)
-                own0[c] = LORA && sl.x < sl.y ? P.plan.mask[4 * sl.x + half * (kCols / 32) + c] : 0u;
+                own0[c] = LORA && t != (int)tile0 && sl.x < sl.y ? P.plan.mask[4 * sl.x + half * (kCols / 32) + c] : 0u;
             const bool row_ok = n < P.N;
             const bool gsc = !P.row_scale && row_ok;
             const float* srow = P.scales + (int64_t)(row_ok ? n : 0) * P.spr + (LORA && !P.row_scale ? kb / gs : 0);
@@ -258,11 +261,12 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] *= a;
             if constexpr (LORA) {
+                if (sl.x < sl.y) pdl_wait();
                 for (int i = sl.x; i < sl.y; ++i) {
                     uint32_t own[kCols / 32];
 #pragma unroll
                     for (int c = 0; c < kCols / 32; ++c)
-                        own[c] = i == sl.x ? own0[c] : P.plan.mask[4 * i + half * (kCols / 32) + c];
+                        own[c] = i == sl.x && t != (int)tile0 ? own0[c] : P.plan.mask[4 * i + half * (kCols / 32) + c];
                     ok = mbar_wait(acc_full(b), bph, &abort_s);
                     if (!ok) break;
                     tc_fence_after();
@@ -457,6 +461,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                     if (++c == XS) { c = 0; cph ^= 1u; }
                 }
                 if constexpr (LORA) {
+                    pdl_wait();
                     for (int i = sl.x; i < sl.y && ok; ++i) {
                         const int a = i == sl.x ? a0 : i == sl.x + 1 ? a1 : P.plan.slot_a[i];
                         for (int r0 = 0; r0 < P.rp; r0 += 64) {
@@ -639,6 +644,23 @@ bool prefill_eligible(const ProbShape& s, int64_t M) {
 // SMs that clusters of one CTA per SM can fill, in percent: what is left over in a GPC stays empty
 constexpr int kPRoom = 88;
 
+static int64_t prefill_tiles(const ProbShape& s, int64_t M) {
+    return ((s.N + kPBM - 1) / kPBM) * ((M + kPBN - 1) / kPBN);
+}
+
+// Adapters: K is split while that still gives every CTA an SM, and each of them four chunks or more in whole groups
+static int lora_split(const ProbShape& s, int64_t M, int sms) {
+    const int64_t steps = s.K / kPBK, tiles = prefill_tiles(s, M);
+    const int64_t units = s.granularity == SHERRY_PER_GROUP ? s.K / s.group : steps;
+    int cl = 1;
+    while (cl < 8 && tiles * cl * 2 <= sms * kPRoom / 100 && units >= 2 * cl && steps >= 16 * cl) cl *= 2;
+    return cl;
+}
+
+int64_t prefill_lora_ctas(const ProbShape& s, int64_t M, int sms) {
+    return std::min<int64_t>(prefill_tiles(s, M), sms) * lora_split(s, M, sms);
+}
+
 // Wd: the latent bf16 weight for Arenas; lora: the adapters' part of P (null: the plain linear)
 static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, int64_t M, int y_bf16,
                               const uint16_t* Wd, float lambda, const LoraArgs* lora, cudaStream_t stream) {
@@ -690,17 +712,14 @@ static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, i
         return SHERRY_OK;
     });
     if (st) return st;
-    const int64_t tiles = ((s.N + kPBM - 1) / kPBM) * ((M + kPBN - 1) / kPBN);
+    const int64_t tiles = prefill_tiles(s, M);
     const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
     // 16 epilogue warps (32 token columns each) drain a group accumulator faster; measured on the
     // 3B shapes that pays for group scales up to K = 4096 (+6%) and costs at K = 8192 (-15%) and
     // for per-row scales (one drain per tile; -1.5% at 2048 and 4096 tokens)
     const bool epi16 = s.granularity == SHERRY_PER_GROUP && s.K <= 4096;
     if (lora) {
-        // K is split while that still gives every CTA an SM, and each of them two chunks or more in whole groups
-        const int64_t steps = s.K / kPBK, units = P.row_scale ? steps : steps / P.group_steps;
-        int cl = 1;
-        while (cl < 8 && tiles * cl * 2 <= sms * kPRoom / 100 && units >= 2 * cl && steps >= 16 * cl) cl *= 2;
+        const int cl = lora_split(s, M, sms);
         if (epi16)
             return launch_after(k_prefill<16, PMode::kLora>, grid * cl, PRoles<16>::kThreads, kPSmem, stream, cl, true,
                                 map, wmap, bmap, umap, P);

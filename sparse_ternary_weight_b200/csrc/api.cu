@@ -828,7 +828,11 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     LoraDown down{};
     down.ids = ids;
     const ProbShape s{N, K, granularity, group};
-    if (dX) down.beside_ctas = dgrad_ctas(M, N, K, sms);
+    if (dX) {
+        down.A = A;
+        down.K = K;
+        down.beside_ctas = dgrad_ctas(M, N, K, sms);
+    }
     if (dX || dA) {
         down.G = G;
         down.Gp = Gp;

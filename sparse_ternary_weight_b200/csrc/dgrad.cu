@@ -23,6 +23,8 @@
 // atom).  After the last rows come the adapters' stages, one or two per slot and 64
 // ranks, all by TMA: operand B is A_a as it is stored, operand A is P of the tile's
 // tokens, zero for tokens of other adapters, in 2 bf16 terms (16 significant bits).
+// An adapter whose A is not finite would make NaN of those zeros: it gets no stage, and
+// the epilogue adds its product to its own tokens' rows, element by element.
 //   warps 0..7   epilogue: TMEM -> registers -> dX (bf16) or, where n is split over
 //                CTAs, fp32 partial sums that k_dgrad_join adds in order
 //   warps 8..15  decode
@@ -63,6 +65,9 @@ struct GParams {
     int mtiles, ktiles, splits, nstages;
     // adapters (LORA)
     LoraPlan plan;
+    const uint16_t* A;   // bf16 [n_adapters][R][K]
+    const uint16_t* Pi;  // the image of P
+    int R, terms;
     int rp;
     int terms_box;  // terms of P in one tile of 64 columns: 2, or 1
     int rows_box;   // rows of A_a per load
@@ -91,6 +96,7 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
     __shared__ uint64_t bars[3 * kGMaxStages + 5];
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_s;
+    __shared__ volatile int skip_s[kGMaxStages];  // LORA: the stage holds nothing
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = (smem_u32(gsmem) + 1023u) & ~1023u;
@@ -179,6 +185,13 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
         uint32_t bph = 0;
         for (int w = blockIdx.x; w < items; w += gridDim.x) {
             const Item it = item(w);
+            int bad_slot = -1;  // the row's slot where its adapter's A is not finite
+            if (LORA && it.sl0 < it.sl1) {
+                pdl_wait();
+                const int first = TM == 2 && half ? it.slh : it.sl0, last = TM == 2 && !half ? it.slh : it.sl1;
+                for (int sl = first; sl < last; ++sl)
+                    if (P.plan.bad[P.plan.slot_a[sl]] && (P.plan.mask[4 * sl + q] >> lane & 1u)) bad_slot = sl;
+            }
             if (!mbar_wait(acc_full(b), bph, &abort_s)) break;
             tc_fence_after();
             int64_t m = (int64_t)it.mt * (TM * 128) + (TM == 2 ? half * 128 : 0) + q * 32 + lane;
@@ -191,6 +204,18 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
                 SHERRY_TMEM_LD32(t_row + 32 * c, v);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                 const int k = kc + 32 * c;
+                if (LORA && bad_slot >= 0 && k < P.K) {
+                    const uint16_t* pr = P.Pi + ((int64_t)bad_slot * kLoraTile + q * 32 + lane) * (P.terms * P.rp);
+                    const uint16_t* ar = P.A + (int64_t)P.plan.slot_a[bad_slot] * P.R * P.K + k;
+#pragma unroll 1
+                    for (int r = 0; r < P.R; ++r) {
+                        float p = 0.0f;
+                        for (int t = P.terms - 1; t >= 0; --t) p += bf16lo(pr[t * P.rp + r]);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(fmaf(p, bf16lo(ar[(int64_t)r * P.K + j]), __uint_as_float(v[j])));
+                    }
+                }
                 if (m < P.M && k < P.K) {
                     if (P.splits == 1) {
                         uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(P.out) + m * P.K + k);
@@ -323,8 +348,16 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
                     if (it.sl0 < it.sl1) pdl_wait();
                     for (int sl = it.sl0; sl < it.sl1 && ok; ++sl) {
                         const int a = P.plan.slot_a[sl];
+                        const int bad = P.plan.bad[a];
                         for (int u = 0; u < rblocks * tstages; ++u) {
                             if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
+                            skip_s[s] = bad;
+                            if (bad) {
+                                mbar_arrive(full_a(s));
+                                ++issued[s];
+                                if (++s == ST) { s = 0; ph ^= 1u; }
+                                continue;
+                            }
                             const int r0 = 64 * (u / tstages), t0 = u % tstages;
                             const int boxes = 2 / (P.terms_box * tstages);
                             const uint32_t dst = base + (uint32_t)(s * SB);
@@ -382,6 +415,11 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
                         for (int u = 0; u < rblocks * tstages; ++u) {
                             if (!mbar_wait(full_a(s), ph, &abort_s)) { ok = false; break; }
                             tc_fence_after();
+                            if (skip_s[s]) {
+                                mma_commit(empty(s));
+                                if (++s == ST) { s = 0; ph ^= 1u; }
+                                continue;
+                            }
                             const uint64_t dp = smem_desc(base + (uint32_t)(s * SB));
                             const uint64_t da = smem_desc_mn(base + (uint32_t)(s * SB + TM * kGABytes), kGN * 128);
                             const int n16 = min(4, (P.rp - 64 * (u / tstages)) / 16);
@@ -492,6 +530,10 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
     CUtensorMap ypmap = map, pmap = map, amap = map;
     if (lora) {
         P.plan = lora->plan;
+        P.A = lora->A;
+        P.Pi = lora->P.data;
+        P.R = lora->R;
+        P.terms = lora->P.terms;
         P.rp = lora->P.rp;
         P.terms_box = 2 * P.rp <= 64 ? 2 : 1;
         P.rows_box = std::min(P.rp, 64);

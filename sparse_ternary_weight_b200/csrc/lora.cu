@@ -45,7 +45,7 @@ size_t lora_image_bytes(int64_t M, int n_adapters, int R, int terms) {
 
 size_t lora_plan_bytes(int64_t M, int n_adapters) {
     const int64_t s = lora_max_slots(M, n_adapters);
-    return (size_t)(256 + up256(4 * M) + up256(4 * (lora_tiles(M) + 1)) + 3 * up256(4 * s) + up256(4 * (n_adapters + 1)) +
+    return (size_t)(256 + up256(4 * M) + up256(4 * (lora_tiles(M) + 1)) + 3 * up256(4 * s) + 2 * up256(4 * (n_adapters + 1)) +
                     up256(16 * s));
 }
 
@@ -66,6 +66,7 @@ LoraPlan lora_plan_in(void* mem, int64_t M, int n_adapters) {
     plan.slot_t = take(4 * s);
     plan.adap_s = take(4 * s);
     plan.adap_b = take(4 * (n_adapters + 1));
+    plan.bad = take(4 * n_adapters);
     plan.mask = reinterpret_cast<uint32_t*>(take(16 * s));
     plan.max_slots = (int)s;
     plan.may_permute = lora_may_permute(M, n_adapters);
@@ -108,6 +109,7 @@ __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, con
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tiles = (int)plan.tiles;
     cnt[tid] = 0;
+    if (tid < n) plan.bad[tid] = 0;
     int total = 0;
     for (int t0 = 0; t0 < tiles; t0 += 32) {
         const int t = t0 + warp;
@@ -319,6 +321,8 @@ struct DownParams {
     const float* V2;
     uint16_t* img2;
     int M, C, R, rp, terms, terms2, n_adapters;
+    const uint16_t* A;
+    int64_t rk;  // R x K, elements of an adapter's A
     int by_row, product;  // product: there is a W
     int stages, stage_bytes;
 };
@@ -357,9 +361,30 @@ __device__ __forceinline__ void cluster_sum8(cg::cluster_group& cluster, int CL,
     }
 }
 
+// Look through the A of every adapter with a token, 4096 elements a warp at a time.
+__device__ __forceinline__ void down_scan(const DownParams& P, int w0, int ws) {
+    constexpr int kPart = 4096;
+    const int lane = threadIdx.x & 31, parts = (int)((P.rk + kPart - 1) / kPart);
+    for (int64_t u = w0; u < (int64_t)parts * P.n_adapters; u += ws) {
+        const int a = (int)(u / parts);
+        if (P.plan.adap_b[a] == P.plan.adap_b[a + 1]) continue;
+        const int64_t e0 = (u % parts) * kPart, e1 = min(e0 + kPart, P.rk);  // (multiples of 8)
+        const uint4* p = reinterpret_cast<const uint4*>(P.A + a * P.rk);
+        uint32_t found = 0;
+#pragma unroll 8
+        for (int64_t e = e0 / 8 + lane; e < e1 / 8; e += 32) {
+            const uint4 v = __ldg(p + e);
+            found |= __vcmpgeu2(v.x & 0x7fff7fffu, 0x7f807f80u) | __vcmpgeu2(v.y & 0x7fff7fffu, 0x7f807f80u) |
+                     __vcmpgeu2(v.z & 0x7fff7fffu, 0x7f807f80u) | __vcmpgeu2(v.w & 0x7fff7fffu, 0x7f807f80u);
+        }
+        if (__any_sync(kFull, found != 0) && lane == 0) P.plan.bad[a] = 1;  // (all writers write 1)
+    }
+}
+
 // 32 tokens at a time, a warp each: V's zeros for tokens of no adapter, and a quarter of a slot of V2's image
 __device__ __forceinline__ void down_side(const DownParams& P, bool permuted, int slots, int w0, int ws) {
     const int lane = threadIdx.x & 31;
+    if (P.A) down_scan(P, w0, ws);
     if (P.V)
         for (int64_t u = w0; u * 32 < P.M; u += ws) {
             const int64_t m = u * 32 + lane;
@@ -572,6 +597,8 @@ int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const 
     P.terms = d.img.terms;
     P.terms2 = d.img2.terms;
     P.n_adapters = n_adapters;
+    P.A = d.A;
+    P.rk = (int64_t)R * d.K;
     P.by_row = d.by_row;
     P.product = d.W != nullptr;
     CUtensorMap gmap{}, gpmap{}, wmap{};

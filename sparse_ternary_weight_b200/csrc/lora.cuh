@@ -24,6 +24,7 @@ struct LoraPlan {
     int32_t* slot_t;  // [max_slots] its tile
     int32_t* adap_b;  // [n_adapters + 1] where each adapter's slots start in adap_s
     int32_t* adap_s;  // [max_slots] slots, adapter by adapter, in order
+    int32_t* bad;     // [n_adapters] 1 where A_a holds a NaN or an infinity (k_lora_down, for the input gradient)
     uint32_t* mask;   // [max_slots][4] which of the tile's 128 tokens the slot has (written by k_lora_down)
     int64_t tiles;
     int max_slots;
@@ -120,6 +121,8 @@ struct LoraDown {
     LoraImage img;       // data may be null
     const float* V2;     // or null
     LoraImage img2;
+    const uint16_t* A;   // bf16 [n_adapters][R][K] to look through for what is not finite, or null
+    int64_t K;
     int64_t beside_ctas; // CTAs (one per SM) of the kernel that follows
 };
 int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const LoraPlan& plan, int sms,

@@ -261,6 +261,37 @@ def test_an_adapter_that_is_not_finite_stays_alone(sw, orc, M, ids):
     assert not bool(torch.isfinite(y2[own]).any())
 
 
+@pytest.mark.parametrize("M,N,K,ids", [(20, 130, 512, "mixed"), (300, 130, 512, "sorted"), (1000, 130, 512, "mixed"),
+                                       (1500, 328, 6688, "mixed")])
+def test_gradients_beside_an_adapter_that_is_not_finite(sw, orc, M, N, K, ids):
+    """Its own tokens' dX is what the formula gives, every other token's is what it was."""
+    import torch
+    pr = Problem(sw, orc, M, N, K, "tensor", 0, 16, 4, ids)
+    _, U = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+    want = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, U, pr.scaling, torch.float32)
+    A = pr.A.clone()
+    A[1, 3, 5] = float("nan")
+    A[1, 2, 7] = float("inf")
+    dX, dA, dB = sw.linear_lora_backward(pr.G, pr.X, pr.P, A, pr.B, pr.ids, U, pr.scaling, torch.float32)
+    own = pr.ids == 1
+    assert bool(own.any())
+    assert torch.equal(dX[~own], want[0][~own]) and torch.equal(dA, want[1]) and torch.equal(dB, want[2])
+    assert bool(torch.isnan(dX[own][:, 5]).all()) and bool(torch.isinf(dX[own][:, 7]).all())
+    rest = torch.ones(K, dtype=torch.bool, device="cuda")
+    rest[5] = rest[7] = False
+    # the same product summed elsewhere: 2^-15 of its terms, and two roundings to bf16 of half a step each
+    base, ext, _, _ = pr.backward(True)
+    tol = torch.from_numpy(2.0 ** -15 * (base + ext)).cuda()[own] + 2.0 ** -7 * want[0][own].double().abs()
+    assert bool(((dX[own].double() - want[0][own].double()).abs() <= tol)[:, rest].all())
+    # infinities in B reach P, and through it that adapter's rows and gradient alone
+    B = pr.B.clone()
+    B[1, 0, 0] = float("inf")
+    dX, dA, dB = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, B, pr.ids, U, pr.scaling, torch.float32)
+    others = [0, 2, 3]
+    assert torch.equal(dX[~own], want[0][~own]) and torch.equal(dA[others], want[1][others])
+    assert not bool(torch.isfinite(dX[own]).any()) and not bool(torch.isfinite(dA[1, 0]).any())
+
+
 def test_large_backward_tiles(sw, orc):
     """Enough tiles for the 256-token form of the input gradient, ragged in every direction."""
     import torch

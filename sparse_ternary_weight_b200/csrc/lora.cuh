@@ -40,12 +40,14 @@ struct LoraImage {
 };
 static inline int lora_rp(int R) { return (R + 15) / 16 * 16; }
 
-// the term of x that is left after `which` terms are taken out, each the bf16 nearest to what is left:
-// the differences are exact in fp32, so two terms keep 16 significant bits and three all 24
+// the next term of (x, y), each the bf16 nearest to what is left; the differences are exact in fp32, so two
+// terms keep 16 significant bits and three all 24.  An infinity or NaN is its own first term.
 __device__ __forceinline__ uint32_t split_next(float& x, float& y) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     x -= __low2float(h);
     y -= __high2float(h);
+    if (!(fabsf(x) < INFINITY)) x = 0.0f;
+    if (!(fabsf(y) < INFINITY)) y = 0.0f;
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 

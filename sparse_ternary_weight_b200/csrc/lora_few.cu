@@ -32,8 +32,8 @@ struct FewParams {
 };
 
 __global__ void __launch_bounds__(128) k_lora_down_few(const FewParams P) {
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // only now: k_lora_few reads X at once, which the kernel before this one may write
     __shared__ float red[4][4];
     const int m = blockIdx.y, r0 = 4 * blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -391,6 +391,45 @@ def test_autograd(sw, orc):
     assert torch.equal(B2.grad, want)
 
 
+@pytest.mark.parametrize("M", [1, 4, 40, 300])
+def test_calls_that_feed_one_another(sw, orc, M):
+    """Layer after layer without a wait between them, each reading what the one before wrote: kernels
+    start beside the end of others, and must not read ahead of them."""
+    import torch
+    pr = Problem(sw, orc, M, 1024, 1024, "group", 128, 16, 3, "mixed")
+    bf = torch.bfloat16
+
+    def chain(sync):
+        x, us, out = pr.X, [], []
+        for _ in range(6):
+            y, u = sw.linear_lora(x, pr.P, pr.A, pr.B, pr.ids, pr.scaling, bf, return_u=True)
+            if sync:
+                torch.cuda.synchronize()
+            us.append((x, u))
+            x = y
+            out.append(y)
+        g = x
+        for x, u in reversed(us):
+            g, dA, dB = sw.linear_lora_backward(g, x, pr.P, pr.A, pr.B, pr.ids, u, pr.scaling)
+            if sync:
+                torch.cuda.synchronize()
+            out += [g, dA, dB]
+        return out
+
+    want = chain(True)
+    for _ in range(5):
+        assert all(torch.equal(p, q) for p, q in zip(chain(False), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(False)
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_capture_of_a_permuted_call(sw, orc):
     """A replay whose ids make other slots, another order of tokens or none takes them as they then are."""
     import torch

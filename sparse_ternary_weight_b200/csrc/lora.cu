@@ -260,27 +260,48 @@ struct RowsParams {
     int count;
 };
 
-constexpr int kRowsThreads = 1024, kRowsWide = 256;  // four rows at a time
+constexpr int kRowsThreads = 256, kRowsVecs = 4;  // 16-byte pieces of the copy per thread
+
+// elements e0 .. e0 + 8 of rows that are not a multiple of 16 bytes, `n` of them in the row, `all` in the matrix
+__device__ __forceinline__ uint4 rows_piece(const uint16_t* src, int64_t e0, int n, int64_t all) {
+    if (n >= 8 && e0 + 9 <= all) {
+        // whole words: from e0, or shifted by half a word from e0 - 1
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(src + (e0 & ~(int64_t)1));
+        const uint32_t sh = (uint32_t)(e0 & 1) * 16;
+        const uint32_t a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2), d = __ldg(q + 3), e = sh ? __ldg(q + 4) : 0u;
+        return make_uint4(__funnelshift_r(a, b, sh), __funnelshift_r(b, c, sh), __funnelshift_r(c, d, sh),
+                          __funnelshift_r(d, e, sh));
+    }
+    uint32_t h[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = k < n ? __ldg(src + e0 + k) : 0u;
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
 
 __global__ void __launch_bounds__(kRowsThreads) k_lora_rows(const RowsParams P) {
     pdl_trigger();
     pdl_wait();
     const bool permuted = P.head && P.head[0] != 0;
-    constexpr int kRows = kRowsThreads / kRowsWide;
-    const int lane = threadIdx.x % kRowsWide;
     for (int j = 0; j < P.count; ++j) {
         const LoraRows& J = P.job[j];
         if (!permuted && !J.always) continue;
-        for (int64_t p = blockIdx.x * kRows + threadIdx.x / kRowsWide; p < P.M; p += (int64_t)gridDim.x * kRows) {
-            const uint16_t* src = J.src + (permuted ? (int64_t)P.perm[p] : p) * J.N;
-            uint16_t* dst = J.dst + p * J.ld;
-            if (J.N == J.ld) {  // (multiples of 8)
-#pragma unroll 4
-                for (int64_t i = lane; i < J.N / 8; i += kRowsWide)
-                    reinterpret_cast<uint4*>(dst)[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-            } else {
-#pragma unroll 4
-                for (int64_t i = lane; i < J.ld; i += kRowsWide) dst[i] = i < J.N ? __ldg(src + i) : (uint16_t)0;
+        const int vecs = (int)(J.ld / 8), chunks = (vecs + kRowsThreads * kRowsVecs - 1) / (kRowsThreads * kRowsVecs);
+        for (int64_t w = blockIdx.x; w < P.M * chunks; w += gridDim.x) {
+            const int64_t p = w / chunks;
+            const int i0 = (int)(w - p * chunks) * (kRowsThreads * kRowsVecs) + threadIdx.x;
+            const int64_t row = (permuted ? (int64_t)P.perm[p] : p) * J.N;
+            uint4 v[kRowsVecs];
+#pragma unroll
+            for (int u = 0; u < kRowsVecs; ++u) {
+                const int i = i0 + u * kRowsThreads;
+                if (i < vecs)
+                    v[u] = J.N == J.ld ? __ldg(reinterpret_cast<const uint4*>(J.src + row) + i)
+                                       : rows_piece(J.src, row + 8 * i, (int)J.N - 8 * i, P.M * J.N);
+            }
+#pragma unroll
+            for (int u = 0; u < kRowsVecs; ++u) {
+                const int i = i0 + u * kRowsThreads;
+                if (i < vecs) reinterpret_cast<uint4*>(J.dst + p * J.ld)[i] = v[u];
             }
         }
     }
@@ -294,7 +315,9 @@ int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan&
     const bool planned = plan.head && plan.may_permute;
     P.head = planned ? plan.head : nullptr;
     P.perm = plan.perm;
-    const unsigned grid = (unsigned)std::min<int64_t>((M + 3) / 4, 148 * 2);
+    int64_t blocks = 1;
+    for (int j = 0; j < count; ++j) blocks = std::max(blocks, M * ((jobs[j].ld / 8 + kRowsThreads * kRowsVecs - 1) / (kRowsThreads * kRowsVecs)));
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, 148 * 8);
     return launch_after(k_lora_rows, grid, kRowsThreads, 0, stream, 1, plan.head != nullptr, P);
 }
 
@@ -400,6 +423,7 @@ __device__ __forceinline__ void down_side(const DownParams& P, bool permuted, in
             const int m = slot_token(P, permuted, (int64_t)P.plan.slot_t[s] * kLoraTile + 32 * q + lane, P.plan.slot_a[s]);
             const unsigned in = __ballot_sync(kFull, m >= 0);
             if (lane == 0) P.plan.mask[u] = in;
+#pragma unroll 2
             for (int r = 0; r < P.rp; r += 8) {
                 float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
                 if (m >= 0 && r < P.R) {
@@ -450,8 +474,8 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    const int slot0 = blockIdx.x / CL;  // (below max_slots: the grid has no more clusters)
-    int a = P.plan.slot_a[slot0], tile = P.plan.slot_t[slot0];  // loaded beside the head, in vain past the last slot
+    const int slot0 = blockIdx.x / CL, held = min(slot0, P.plan.max_slots - 1);
+    int a = P.plan.slot_a[held], tile = P.plan.slot_t[held];  // loaded beside the head, in vain past the last slot
     const bool permuted = P.plan.may_permute && P.plan.head[0] != 0;
     const int slots = P.plan.head[1];
     const int steps = (P.C + 63) / 64;
@@ -621,7 +645,10 @@ int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const 
     P.stage_bytes = kDnG + (d.by_row ? (P.rp + 63) / 64 * 64 * 128 : (P.rp * 128 + 1023) / 1024 * 1024);
     P.stages = std::min(kDnMaxStages, (kDnHalf - 2048) / P.stage_bytes);
     const int smem = std::max(P.stages * P.stage_bytes, P.rp * kLoraTile * 4) + 1024;
-    const int64_t grid = std::min<int64_t>(est, 4 * sms / cl) * cl;
+    // clusters beyond the slots share the side work: units of a warp
+    const int64_t units = (d.V ? (M + 31) / 32 : 0) + (d.V2 ? 4 * est : 0) + (d.A ? (P.rk + 4095) / 4096 * n_adapters : 0);
+    const int64_t clusters = std::max(est, std::min<int64_t>(units / (4 * cl), sms / cl));
+    const int64_t grid = std::min<int64_t>(clusters, 4 * sms / cl) * cl;
     if ((int64_t)plan.max_slots * 4 > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     static PerDevice once;
     int v = 0;

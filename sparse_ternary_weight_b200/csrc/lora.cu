@@ -278,30 +278,31 @@ __device__ __forceinline__ uint4 rows_piece(const uint16_t* src, int64_t e0, int
     return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
+template <typename I>  // of the pieces' numbers
 __global__ void __launch_bounds__(kRowsThreads) k_lora_rows(const RowsParams P) {
     pdl_trigger();
     pdl_wait();
     const bool permuted = P.head && P.head[0] != 0;
+    const I stride = (I)gridDim.x * kRowsThreads;
     for (int j = 0; j < P.count; ++j) {
         const LoraRows& J = P.job[j];
         if (!permuted && !J.always) continue;
-        const int vecs = (int)(J.ld / 8), chunks = (vecs + kRowsThreads * kRowsVecs - 1) / (kRowsThreads * kRowsVecs);
-        for (int64_t w = blockIdx.x; w < P.M * chunks; w += gridDim.x) {
-            const int64_t p = w / chunks;
-            const int i0 = (int)(w - p * chunks) * (kRowsThreads * kRowsVecs) + threadIdx.x;
-            const int64_t row = (permuted ? (int64_t)P.perm[p] : p) * J.N;
+        const I vecs = (I)(J.ld / 8), total = (I)P.M * vecs;
+        for (I i0 = (I)blockIdx.x * kRowsThreads + threadIdx.x; i0 < total; i0 += kRowsVecs * stride) {
             uint4 v[kRowsVecs];
 #pragma unroll
             for (int u = 0; u < kRowsVecs; ++u) {
-                const int i = i0 + u * kRowsThreads;
-                if (i < vecs)
-                    v[u] = J.N == J.ld ? __ldg(reinterpret_cast<const uint4*>(J.src + row) + i)
-                                       : rows_piece(J.src, row + 8 * i, (int)J.N - 8 * i, P.M * J.N);
+                const I i = i0 + u * stride, p = i / vecs, c = i - p * vecs;
+                if (i < total) {
+                    const int64_t row = (permuted ? (int64_t)P.perm[p] : (int64_t)p) * J.N;
+                    v[u] = J.N == J.ld ? __ldg(reinterpret_cast<const uint4*>(J.src + row) + c)
+                                       : rows_piece(J.src, row + 8 * c, (int)(J.N - 8 * c), P.M * J.N);
+                }
             }
 #pragma unroll
             for (int u = 0; u < kRowsVecs; ++u) {
-                const int i = i0 + u * kRowsThreads;
-                if (i < vecs) reinterpret_cast<uint4*>(J.dst + p * J.ld)[i] = v[u];
+                const I i = i0 + u * stride;
+                if (i < total) reinterpret_cast<uint4*>(J.dst)[i] = v[u];  // (rows of dst stand close)
             }
         }
     }
@@ -315,10 +316,11 @@ int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan&
     const bool planned = plan.head && plan.may_permute;
     P.head = planned ? plan.head : nullptr;
     P.perm = plan.perm;
-    int64_t blocks = 1;
-    for (int j = 0; j < count; ++j) blocks = std::max(blocks, M * ((jobs[j].ld / 8 + kRowsThreads * kRowsVecs - 1) / (kRowsThreads * kRowsVecs)));
-    const unsigned grid = (unsigned)std::min<int64_t>(blocks, 148 * 8);
-    return launch_after(k_lora_rows, grid, kRowsThreads, 0, stream, 1, plan.head != nullptr, P);
+    int64_t pieces = 1;
+    for (int j = 0; j < count; ++j) pieces = std::max(pieces, M * (jobs[j].ld / 8));
+    const unsigned grid = (unsigned)std::min<int64_t>((pieces + kRowsThreads - 1) / kRowsThreads, 148 * 8);
+    auto kernel = pieces < (int64_t)1 << 29 ? k_lora_rows<uint32_t> : k_lora_rows<uint64_t>;
+    return launch_after(kernel, grid, kRowsThreads, 0, stream, 1, plan.head != nullptr, P);
 }
 
 // ---- into rank space -----------------------------------------------------------------
@@ -979,10 +981,10 @@ int lora_grad_launch(const LoraGradJob* jobs, int count, int R, int n_adapters, 
     P.n_adapters = n_adapters;
     P.out_bf16 = out_bf16;
     P.vboxes = (P.terms * P.rp + 63) / 64;
-    // tokens split until there are CTAs enough, each with a few stages on average
+    // tokens split while three CTAs per SM hold them all, each with a few stages on average
     const int64_t avg = 2 * ((plan.tiles + n_adapters - 1) / n_adapters);
     int cl = 1;
-    while (cl < 8 && blocks * cl < 2 * (int64_t)sms && avg >= 4 * cl) cl *= 2;
+    while (cl < 8 && blocks * cl * 2 <= 3 * (int64_t)sms && avg >= 4 * cl) cl *= 2;
     if (blocks * cl > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     // as many CTAs per SM as make one wave, or as have two stages each and TMEM; the stages that fit then
     const int SB = kGrG + P.vboxes * kGrV, smem_sm = 228 * 1024, sum = kGrCols * P.rp * 4;

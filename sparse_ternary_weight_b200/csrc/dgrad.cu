@@ -27,8 +27,9 @@
 // the epilogue adds its product to its own tokens' rows, element by element.
 //   warps 0..7   epilogue: TMEM -> registers -> dX (bf16) or, where n is split over
 //                CTAs, fp32 partial sums that k_dgrad_join adds in order
-//   warps 8..15  decode
-//   warp 16      TMA, warp 17 MMA issue
+//   warps 8..23  decode, two groups that take the stages in turn: a stage's waits, lookups and
+//                fences are a chain of some 1500 cycles (4096 x 8192 x 2048: 116 -> 107 us)
+//   warp 24      TMA, warp 25 MMA issue
 // n is split where there are fewer tiles than SMs.
 #include "common.cuh"
 #include "lora.cuh"
@@ -41,8 +42,9 @@
 
 namespace sherry {
 
-constexpr int kGThreads = 32 * 18;
-constexpr int kGTmaWarp = 16, kGMmaWarp = 17;
+constexpr int kGDecGroups = 2;               // groups of eight decode warps, a stage each in turn
+constexpr int kGTmaWarp = 8 + 8 * kGDecGroups, kGMmaWarp = kGTmaWarp + 1;
+constexpr int kGThreads = 32 * (kGMmaWarp + 1);
 constexpr int kGK = 256;                     // k columns per tile
 constexpr int kGN = 64;                      // weight rows per stage
 constexpr int kGBBytes = kGN * kGK * 2;      // 32 KB of decoded weights per stage
@@ -247,12 +249,13 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
     } else if (warp < kGTmaWarp) {
         // ---------------- decode: 64 rows x four blocks of 64 k; eight lanes = the eight rows
         // of one swizzle atom, so their 16-byte stores cover all banks ----------------
-        const int dt = threadIdx.x - 256;
+        const int dt = threadIdx.x & 255, group = (warp - 8) >> 3;
         const int r = (dt >> 5) * 8 + (lane & 7), blk = lane >> 3;
         const uint32_t brow = (uint32_t)(TM * kGABytes + blk * (kGN * 128) + (r >> 3) * 1024 + (r & 7) * 128);
         const float inv = 1.0f / dgrad_unit(P.scales);
         int s = 0;
         uint32_t ph = 0;
+        int turn = 0;  // stages so far: a group waits for one of two, and so for every one before it
         bool ok = true;
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const Item it = item(w);
@@ -278,11 +281,15 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
             };
             uint32_t wd[2], sg[2];
             float al[2];
-            fetch(it.st0, wd, sg, al);
-            for (int st = it.st0; st < it.st1; ++st) {
+            fetch(it.st0 + ((turn ^ group) & 1), wd, sg, al);
+            for (int st = it.st0; st < it.st1; ++st, ++turn) {
+                if (kGDecGroups > 1 && ((turn ^ group) & 1)) {  // the other group's
+                    if (++s == ST) { s = 0; ph ^= 1u; }
+                    continue;
+                }
                 uint32_t nwd[2], nsg[2];
                 float nal[2];
-                fetch(st + 1, nwd, nsg, nal);
+                fetch(st + kGDecGroups, nwd, nsg, nal);
                 if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
                 const uint32_t dst = base + (uint32_t)(s * SB) + brow;
 #pragma unroll
@@ -319,7 +326,7 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
             if constexpr (LORA) {
                 // the adapters' stages take their turns without this warp, which waits for them all
                 // the same: no barrier gets two phases ahead of it
-                for (int i = (it.sl1 - it.sl0) * rblocks * tstages; i > 0 && ok; --i) {
+                for (int i = (it.sl1 - it.sl0) * rblocks * tstages; i > 0 && ok; --i, ++turn) {
                     ok = mbar_wait(empty(s), ph ^ 1u, &abort_s);
                     if (++s == ST) { s = 0; ph ^= 1u; }
                 }
@@ -461,6 +468,7 @@ __global__ void __launch_bounds__(256) k_dgrad_join(const float* part, int split
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= total) return;  // total = M * K, a multiple of 32
     float4 a = *reinterpret_cast<const float4*>(part + i);
+#pragma unroll 8
     for (int s = 1; s < splits; ++s) {
         const float4 b = *reinterpret_cast<const float4*>(part + (int64_t)s * total + i);
         a.x += b.x;

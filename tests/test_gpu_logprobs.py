@@ -290,6 +290,25 @@ def test_backward(sw, shape, dt):
         assert torch.equal(buf.view(torch.uint8), before.view(torch.uint8))
 
 
+def test_other_forms_of_the_arguments(sw):
+    """int64 targets, columns that are not next to each other: converted, with the same bits."""
+    import torch
+    _, z, t = make(9, 701, torch.bfloat16)
+    z = z.contiguous()
+    want = sw.token_logprobs(z, t, top=4)
+    wide = torch.zeros((9, 1402), dtype=z.dtype, device="cuda")
+    wide[:, ::2] = z
+    got = sw.token_logprobs(wide[:, ::2], t.long() - 2 ** 40 * (t < 0), top=4)
+    for a, b in ((got.logp, want.logp), (got.entropy, want.entropy), (got.stats, want.stats), (got.top_ids, want.top_ids),
+                 (got.top_logp, want.top_logp)):
+        assert torch.equal(a, b)
+    g = torch.rand(9, device="cuda")
+    dz = sw.token_logprobs_backward(z, t, want.stats, want.entropy, g, g)
+    two = torch.stack([want.stats, want.stats], 2)[:, :, 0]
+    assert not two.is_contiguous()
+    assert torch.equal(sw.token_logprobs_backward(wide[:, ::2], t.long(), two, want.entropy, g, g), dz)
+
+
 def test_differences(sw):
     """sum(g logp + h H) at z +- a step against the gradient along it."""
     import torch

@@ -391,6 +391,31 @@ def test_autograd(sw, orc):
     assert torch.equal(B2.grad, want)
 
 
+@pytest.mark.parametrize("M", [5, 300])
+def test_other_forms_of_the_arguments(sw, orc, M):
+    """Strided tensors, int64 ids, results into given tensors: converted, with the same bits."""
+    import torch
+    pr = Problem(sw, orc, M, 136, 512, "group", 128, 16, 3, "mixed")
+    y, u = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+    grads = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, u, pr.scaling)
+
+    def strided(t):
+        wide = torch.full((*t.shape[:-1], 2 * t.shape[-1]), 7, dtype=t.dtype, device="cuda")
+        wide[..., ::2] = t
+        return wide[..., ::2]
+
+    out = torch.empty_like(y)
+    X, A, B, G, U, s, ids = (strided(t) for t in (pr.X, pr.A, pr.B, pr.G, u, pr.scaling, pr.ids.long()))
+    far = torch.where(ids < 0, ids - 2 ** 40, ids)  # no adapter, beyond int32
+    assert not X.is_contiguous() and not ids.is_contiguous()
+    assert torch.equal(sw.linear_lora(X, pr.P, A, B, far, s, out=out), y) and torch.equal(out, y)
+    y2, u2 = sw.linear_lora(X, pr.P, A, B, ids, s, return_u=True)
+    assert torch.equal(y2, y) and torch.equal(u2, u)
+    assert all(torch.equal(p, q) for p, q in zip(sw.linear_lora_backward(G, X, pr.P, A, B, ids, U, s), grads))
+    dX = torch.empty_like(pr.X)
+    assert torch.equal(sw.linear_backward(G, pr.P, out=dX), sw.linear_backward(pr.G, pr.P))
+
+
 @pytest.mark.parametrize("M", [1, 4, 40, 300])
 def test_calls_that_feed_one_another(sw, orc, M):
     """Layer after layer without a wait between them, each reading what the one before wrote: kernels

@@ -89,7 +89,7 @@ struct PParams {
     float lambda;     // Arenas: weight of the dense product
     // adapters (PMode::kLora)
     LoraPlan plan;
-    int R, rp, terms;  // rank, rounded up to 16; bf16 terms that U is split into
+    int rp, terms;     // the rank rounded up to 16, and the bf16 terms that U is split into
 };
 
 // Arenas (ARN): the same kernel also accumulates X W^T for a dense bf16 latent
@@ -687,7 +687,6 @@ static int prefill_launch_any(const ProbShape& s, const sherry_linear_desc& d, i
     P.lambda = lambda;
     if (lora) {
         P.plan = lora->plan;
-        P.R = lora->R;
         P.rp = lora->U.rp;
         P.terms = lora->U.terms;
         if (lora->Xp && (st = encode_2d(&wmap, lora->Xp, s.K, M, kPBN))) return st;

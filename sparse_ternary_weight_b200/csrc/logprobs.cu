@@ -587,13 +587,17 @@ __global__ void __launch_bounds__(TH) k_logprobs_bwd(const LpBwdParams P) {
             }
         }
     }
-    const float m = P.stats[2 * rowi], lsum = P.stats[2 * rowi + 1];
+    float m = P.stats[2 * rowi], lsum = P.stats[2 * rowi + 1];
     const int t0 = P.targets ? P.targets[rowi] : -1;
     const int t = (t0 >= 0 && t0 < V) ? t0 : -1;
     const bool dead = m == -INFINITY;
+    if (dead) m = 0.0f, lsum = INFINITY;  // every p is 0
     const float g = (t < 0 || dead) ? 0.0f : P.dlogp[rowi];
     const float h = P.dentropy ? P.dentropy[rowi] : 0.0f;
     const float H = P.dentropy ? P.entropy[rowi] : 0.0f;
+    // -p (g + h (log p + H)), two elements an instruction
+    const float k = -fmaf(h, H, g);
+    const uint64_t m2 = pair(-m, -m), l2 = pair(-lsum, -lsum), h2 = pair(-h, -h), k2 = pair(k, k), L2 = pair(kLog2e, kLog2e);
 #pragma unroll
     for (int u = 0; u < kLpBwdVecs; ++u) {
         const int v = vb + u * TH;
@@ -602,12 +606,20 @@ __global__ void __launch_bounds__(TH) k_logprobs_bwd(const LpBwdParams P) {
         float f[N];
         LpVec<T>::unpack(x[u], f);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float lp = (f[j] - m) - lsum;
-            const float p = dead ? 0.0f : ex2(lp * kLog2e);
-            // p = 0 where z = -inf: its log p would make 0 * -inf
-            f[j] = p == 0.0f ? 0.0f : -p * fmaf(h, lp + H, g);
-            if (e0 + j == t) f[j] += g;
+        for (int j = 0; j < N; j += 2) {
+            const uint64_t d = add2(add2(pair(f[j], f[j + 1]), m2), l2);
+            // below -200 p is 0: held there (NaN stays), 0 * -inf would be NaN
+            float a, b;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(lo_of(d)), "f"(-200.0f));
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(hi_of(d)), "f"(-200.0f));
+            const uint64_t lp = pair(a, b), y = fma2(lp, L2, 0);
+            const uint64_t o = fma2(pair(ex2(lo_of(y)), ex2(hi_of(y))), fma2(h2, lp, k2), 0);
+            f[j] = lo_of(o);
+            f[j + 1] = hi_of(o);
+        }
+        if ((uint32_t)(t - e0) < (uint32_t)N && t >= 0) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) f[j] += e0 + j == t ? g : 0.0f;
         }
         if (e0 >= 0 && e0 + N <= V) {
             __stcs(reinterpret_cast<uint4*>(out + e0), LpVec<T>::pack(f));

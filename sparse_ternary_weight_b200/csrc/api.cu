@@ -718,7 +718,7 @@ static BwdWs backward_ws(int64_t M, int64_t N, int64_t K, int n_adapters, int ra
     w.g = at;
     if (ld != N || permute) at += up256((size_t)(M * ld) * 2);
     w.part = at;
-    at += up256(dgrad_workspace_bytes(M, N, K, device_sms()));
+    at += up256(dgrad_workspace_bytes(M, N, K, n_adapters, rank, device_sms()));
     if (n_adapters > 0) {
         w.xp = at;
         if (permute) at += up256((size_t)(M * K) * 2);
@@ -775,7 +775,7 @@ int sherry_linear_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, 
     }
     const ProbShape s{N, K, granularity, group};
     if ((st = dgrad_launch(s, idx, sgn, scales, G, ld, M, dX, nullptr, ws + w.part, device_sms(), cs))) return st;
-    return dgrad_join_launch(s, scales, M, dX, ws + w.part, device_sms(), cs);
+    return dgrad_join_launch(s, scales, M, dX, ws + w.part, 0, 0, device_sms(), cs);
 }
 
 size_t sherry_linear_lora_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int n_adapters, int rank) {
@@ -831,7 +831,7 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     if (dX) {
         down.A = A;
         down.K = K;
-        down.beside_ctas = dgrad_ctas(M, N, K, sms);
+        down.beside_ctas = dgrad_ctas(M, N, K, n_adapters, rank, sms);
     }
     if (dX || dA) {
         down.G = G;
@@ -858,7 +858,7 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     if (count &&
         (st = lora_grad_launch(jobs, count, rank, n_adapters, M, plan, grad_dtype == SHERRY_BF16, dX != nullptr, sms, cs)))
         return st;
-    return dX ? dgrad_join_launch(s, scales, M, dX, ws + w.part, sms, cs) : SHERRY_OK;
+    return dX ? dgrad_join_launch(s, scales, M, dX, ws + w.part, n_adapters, rank, sms, cs) : SHERRY_OK;
 }
 
 static int check_logits(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld) {

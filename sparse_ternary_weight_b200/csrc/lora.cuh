@@ -80,15 +80,15 @@ struct LoraGradArgs {
     int R, n_adapters;
     LoraPlan plan;
 };
-int64_t dgrad_ctas(int64_t M, int64_t N, int64_t K, int sms);
+int64_t dgrad_ctas(int64_t M, int64_t N, int64_t K, int n_adapters, int R, int sms);  // 0 adapters: the plain gradient
 // dX = dY (T alpha) (+ P A_a): dY bf16 rows ldy apart (a multiple of 8), lora null for the plain gradient (dgrad.cu)
-size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int sms);
+size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int n_adapters, int R, int sms);
 int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, const float* scales, const uint16_t* dY,
                  int64_t ldy, int64_t M, uint16_t* dX, const LoraGradArgs* lora, void* workspace, int sms,
                  cudaStream_t stream);
 // where the rows were split over CTAs: dX from their partial sums; otherwise nothing
-int dgrad_join_launch(const ProbShape& s, const float* scales, int64_t M, uint16_t* dX, const void* workspace, int sms,
-                      cudaStream_t stream);
+int dgrad_join_launch(const ProbShape& s, const float* scales, int64_t M, uint16_t* dX, const void* workspace,
+                      int n_adapters, int R, int sms, cudaStream_t stream);
 
 // bytes of a plan, and the plan laid out in `mem` (256-byte aligned); false where it is too large
 size_t lora_plan_bytes(int64_t M, int n_adapters);

@@ -262,11 +262,17 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             for (int j = 0; j < kCols; ++j) acc[j] *= a;
             if constexpr (LORA) {
                 if (sl.x < sl.y) pdl_wait();
-                for (int i = sl.x; i < sl.y; ++i) {
-                    uint32_t own[kCols / 32];
+                if (t == (int)tile0 && sl.x < sl.y) {
 #pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c)
-                        own[c] = i == sl.x && t != (int)tile0 ? own0[c] : P.plan.mask[4 * i + half * (kCols / 32) + c];
+                    for (int c = 0; c < kCols / 32; ++c) own0[c] = P.plan.mask[4 * sl.x + half * (kCols / 32) + c];
+                }
+                for (int i = sl.x; i < sl.y; ++i) {
+                    uint32_t own[kCols / 32];  // the next slot's are loaded ahead
+#pragma unroll
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        own[c] = own0[c];
+                        own0[c] = P.plan.mask[4 * min(i + 1, sl.y - 1) + half * (kCols / 32) + c];
+                    }
                     ok = mbar_wait(acc_full(b), bph, &abort_s);
                     if (!ok) break;
                     tc_fence_after();
@@ -463,7 +469,9 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 if constexpr (LORA) {
                     pdl_wait();
                     for (int i = sl.x; i < sl.y && ok; ++i) {
-                        const int a = i == sl.x ? a0 : i == sl.x + 1 ? a1 : P.plan.slot_a[i];
+                        const int a = a0;  // the next slots' adapters are loaded ahead
+                        a0 = a1;
+                        a1 = P.plan.slot_a[min(i + 2, sl.y - 1)];
                         for (int r0 = 0; r0 < P.rp; r0 += 64) {
                             if (!mbar_wait(chunk_empty(c), cph ^ 1u, &abort_s)) {
                                 ok = false;

@@ -270,7 +270,7 @@ float sherry_arenas_lambda(int64_t step, int64_t total, float lambda0);
  *   workspace  sherry_linear_backward_workspace_bytes(M, N, K) bytes of scratch
  *            (no tickets; need not be zero)
  * Accumulated in fp32.  alpha varies along the sum, so it is rounded to bf16 (in a
- * unit where the first scale is 1.875, so that a per-tensor scale is exact): each
+ * unit where the mean of 32 scales is 1.72; a per-tensor scale is exact): each
  * term carries a relative error of up to 2^-8 of its own, typically below 2^-9.
  * Any valid shape. */
 int sherry_linear_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K,

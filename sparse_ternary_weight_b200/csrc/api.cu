@@ -842,6 +842,7 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
         down.by_row = 1;
         down.scaling = scaling;
         down.unit = scales;
+        down.unit_n = scale_count(s);
         down.img = imgp;
     }
     if (dB) {
@@ -853,8 +854,8 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     if (dX && (st = dgrad_launch(s, idx, sgn, scales, G, ld, M, dX, &args, ws + w.part, sms, cs))) return st;
     LoraGradJob jobs[2];
     int count = 0;
-    if (dB) jobs[count++] = LoraGradJob{imgu, G, Gp, ld, N, dB, nullptr, 1};
-    if (dA) jobs[count++] = LoraGradJob{imgp, X, plan.may_permute ? xp : nullptr, K, K, dA, scales, 0};
+    if (dB) jobs[count++] = LoraGradJob{imgu, G, Gp, ld, N, dB, nullptr, 0, 1};
+    if (dA) jobs[count++] = LoraGradJob{imgp, X, plan.may_permute ? xp : nullptr, K, K, dA, scales, scale_count(s), 0};
     if (count &&
         (st = lora_grad_launch(jobs, count, rank, n_adapters, M, plan, grad_dtype == SHERRY_BF16, dX != nullptr, sms, cs)))
         return st;

@@ -346,6 +346,7 @@ struct DownParams {
     const int32_t* ids;
     const float* scaling;
     const float* unit;
+    int64_t unit_n;
     float* V;
     uint16_t* img;
     const float* V2;
@@ -490,6 +491,7 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
     const int wboxes = P.by_row ? (P.rp + 63) / 64 : 1;
     const uint32_t wbytes = P.by_row ? (uint32_t)wboxes * 64 * 128 : (uint32_t)P.rp * 128;
     float* sum = reinterpret_cast<float*>(dsm + (base - smem_u32(dsm)));
+    const float inv = P.unit ? 1.0f / dgrad_unit(P.unit, P.unit_n) : 1.0f;
     if (warp < 4 && !P.product) down_side(P, permuted, slots, 4 * blockIdx.x + warp, 4 * gridDim.x);
 
     int c = 0;  // stage and its phase, of the TMA and the MMA thread
@@ -555,7 +557,6 @@ k_lora_down(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CU
         tc_fence_after();
         // lane = token: eight ranks at a time, straight from TMEM or as [rank][token] for the cluster
         const float scale = P.scaling ? P.scaling[a] : 1.0f;
-        const float inv = P.unit ? 1.0f / dgrad_unit(P.unit) : 1.0f;
         auto put = [&](int r, float* f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = m >= 0 ? f[i] * scale : 0.0f;
@@ -617,6 +618,7 @@ int lora_down_launch(const LoraDown& d, int64_t M, int R, int n_adapters, const 
     P.ids = d.ids;
     P.scaling = d.scaling;
     P.unit = d.unit;
+    P.unit_n = d.unit_n;
     P.V = d.V;
     P.img = d.img.data;
     P.V2 = d.V2;
@@ -731,6 +733,7 @@ struct GradParams {
     LoraPlan plan;
     void* out[2];
     const float* unit[2];
+    int64_t unit_n[2];
     int64_t C[2];
     int by_column[2], cblocks[2];
     int R, rp, terms, n_adapters, out_bf16;
@@ -885,7 +888,7 @@ k_lora_grad(const __grid_constant__ GradMaps maps, const __grid_constant__ GradP
     // lane = column: eight ranks at a time, straight from TMEM or as [rank][column] for the cluster
     const int R = P.R;
     const int64_t C = P.C[j], cc = c0 + tid;
-    const float unit = P.unit[j] ? dgrad_unit(P.unit[j]) : 1.0f;
+    const float unit = P.unit[j] ? dgrad_unit(P.unit[j], P.unit_n[j]) : 1.0f;
     float* sum = reinterpret_cast<float*>(gsm + (base - smem_u32(gsm)));
     auto put = [&](int r, float* f) {
         if (cc >= C || r >= R) return;
@@ -971,6 +974,7 @@ int lora_grad_launch(const LoraGradJob* jobs, int count, int R, int n_adapters, 
         const LoraGradJob& J = jobs[j];
         P.out[j] = J.out;
         P.unit[j] = J.unit;
+        P.unit_n[j] = J.unit_n;
         P.C[j] = J.C;
         P.by_column[j] = J.by_column;
         P.cblocks[j] = (int)((J.C + kGrCols - 1) / kGrCols);

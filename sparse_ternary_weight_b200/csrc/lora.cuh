@@ -51,12 +51,18 @@ __device__ __forceinline__ uint32_t split_next(float& x, float& y) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The input gradient multiplies bf16(alpha / unit): unit = alpha(0,0) / 1.875 (dgrad.cu), or 1 where
-// that is no ordinary number.  P is held in the same unit.
-constexpr float kGTop = 1.875f;
-__device__ __forceinline__ float dgrad_unit(const float* scales) {
-    const float a = __ldg(scales);
+// The input gradient multiplies bf16(alpha / unit): unit = (the mean of 32 scales spread over the weight's n) / kGTop
+// (dgrad.cu), or 1 where that is no ordinary number.  P is held in the same unit.  Called by whole warps.
+constexpr float kGTop = 1.71875f;
+__device__ __forceinline__ float dgrad_unit(const float* scales, int64_t n) {
+    float a = __ldg(scales + n * (int64_t)(threadIdx.x & 31) / 32);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
+    a *= 1.0f / 32.0f;  // (a per-tensor scale: itself, exactly)
     return (a > 1e-30f && a < 1e30f) ? a / kGTop : 1.0f;
+}
+static inline int64_t scale_count(const ProbShape& s) {
+    return s.granularity == SHERRY_PER_TENSOR ? 1 : s.granularity == SHERRY_PER_CHANNEL ? s.N : s.N * (s.K / s.group);
 }
 
 // What the prefill kernel needs to add the adapters' product
@@ -119,6 +125,7 @@ struct LoraDown {
     const int32_t* ids;
     const float* scaling;
     const float* unit;   // scales of the packed weight: the image holds V / dgrad_unit; or null
+    int64_t unit_n;
     float* V;            // or null
     LoraImage img;       // data may be null
     const float* V2;     // or null
@@ -150,6 +157,7 @@ struct LoraGradJob {
     int64_t ldg, C;
     void* out;            // fp32 or bf16
     const float* unit;
+    int64_t unit_n;
     int by_column;
 };
 // `beside`: right after dgrad_launch's kernel, whose idle SMs it takes

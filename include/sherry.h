@@ -269,10 +269,9 @@ float sherry_arenas_lambda(int64_t step, int64_t total, float lambda0);
  *   dX       bf16 [M][K]; fully overwritten
  *   workspace  sherry_linear_backward_workspace_bytes(M, N, K) bytes of scratch
  *            (no tickets; need not be zero)
- * Accumulated in fp32.  alpha varies along the sum, so it is rounded to bf16 (in a
- * unit where the mean of 32 scales is 1.72; a per-tensor scale is exact): each
- * term carries a relative error of up to 2^-8 of its own, typically below 2^-9.
- * Any valid shape. */
+ * Accumulated in fp32 and rounded once.  alpha varies along the sum, so it enters the
+ * products as two bf16 terms that keep it to 2^-18 of itself (a per-tensor scale is
+ * exact in one).  Any valid shape. */
 int sherry_linear_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K,
                            const uint32_t* idx, const uint8_t* sgn, const float* scales, int granularity, int group,
                            uint16_t* dX, void* workspace, size_t workspace_bytes, void* stream);
@@ -315,6 +314,8 @@ int sherry_linear_lora_needs_tickets(int64_t M, int64_t N, int64_t K, int granul
  * An adapter without tokens gets zeros.  X may be NULL when dA is.  Rows of X and dY of
  * tokens without an adapter may hold anything, and what is not finite in one adapter
  * stays in its own gradients and its own tokens' dX.
+ * P enters dX as bf16 terms that keep 16 significant bits; P and U enter dA and dB with
+ * 16 (bf16 gradients) or 24 (fp32 gradients).
  *   workspace  sherry_linear_lora_backward_workspace_bytes(...) bytes of scratch (no
  *            tickets; need not be zero; 256-byte aligned) */
 int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t N, int64_t K,

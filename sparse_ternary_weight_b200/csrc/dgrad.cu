@@ -7,20 +7,18 @@
 //
 // The sum runs over weight rows n, whose scale changes with every n: unlike in the
 // forward pass alpha cannot be taken out of a group's sum, so it enters the bf16
-// operand, t * bf16(alpha * c).  The factor c is undone in fp32 at the end: the
-// scales of a weight are close to each other, and c puts their mean (of 32 of them)
-// at 1.72, where bf16's half step is 2^-8.8 of the value and few scales pass 2 (a
-// per-tensor scale becomes 1.71875 exactly).  A spread of 8% gives an error of 0.0013 in
-// the mean square, and 0.0021 with the rounding of a bf16 dX, against 0.0017 of that
-// alone; by the first scale instead of the mean it was up to 0.0025.  Rounding alpha, not splitting
-// it in two bf16 terms, halves the tensor work; its error averages out over the n of
-// a sum and stays below that of the bf16 dX.
+// operand, as T = 2 terms, t hi and t lo with hi = bf16(alpha / unit) and lo = bf16 of
+// what is left.  They keep alpha to 2^-18 of itself, below the fp32 sums' own error, so
+// that dX is rounded once, to its bf16 (one term instead would halve the tensor work, but
+// an error of 0.0013 in the mean square beside the rounding's 0.0017).  A per-tensor
+// scale needs one term: unit makes it 1.71875 exactly, and is undone in fp32 at the end.
 //
 // CTA tile: 128 TM tokens x 256 k (TM = 1 or 2 MMAs of 128 x 256 that share the
-// decoded operand); n runs in stages of 64 rows.  dY is operand A, K-major, by TMA.
+// decoded operand); n runs in stages of 64 / T rows, 64 operand rows with the second
+// terms after the first.  dY is operand A, K-major, by TMA, and multiplied by both.
 // The weights are operand B in the layout they unpack to, k contiguous (MN-major,
-// 128-byte swizzle): a decode thread owns 64 consecutive k of a row, looks each
-// block of 4 up in the 32 patterns, scales it with one packed multiply per pair and
+// 128-byte swizzle): a decode thread owns 64 / T consecutive k of a row, looks each
+// block of 4 up in the 32 patterns, scales it with one packed multiply per pair and term and
 // stores 16 bytes at a time, conflict-free (eight lanes take the eight rows of a swizzle
 // atom).  After the last rows come the adapters' stages, one or two per slot and 64
 // ranks, all by TMA: operand B is A_a as it is stored, operand A is P of the tile's
@@ -48,10 +46,10 @@ constexpr int kGDecGroups = 2;               // groups of eight decode warps, a 
 constexpr int kGTmaWarp = 8 + 8 * kGDecGroups, kGMmaWarp = kGTmaWarp + 1;
 constexpr int kGThreads = 32 * (kGMmaWarp + 1);
 constexpr int kGK = 256;                     // k columns per tile
-constexpr int kGN = 64;                      // weight rows per stage
+constexpr int kGN = 64;                      // operand rows per stage: weight rows x terms of alpha
 constexpr int kGBBytes = kGN * kGK * 2;      // 32 KB of decoded weights per stage
-constexpr int kGABytes = 128 * kGN * 2;      // 16 KB of dY per 128 tokens and stage
-constexpr int kGStageSum = 192 * 1024;       // 3 stages of 64 KB (TM = 2) or 4 of 48 KB (TM = 1)
+constexpr int kGABytes = 128 * kGN * 2;      // 16 KB: 64 columns of dY, or of P, for 128 tokens
+constexpr int kGStageSum = 192 * 1024;       // 3 stages of 64 KB (TM = 2, one term) or 4 of 48 KB
 constexpr int kGSmem = kGStageSum + 256 + 1024;
 constexpr int kGMaxStages = 4;
 static_assert(128 * (kGK * 4 + 16) <= kGStageSum && 256 * (kGK * 2 + 16) <= kGStageSum, "results fit the stages");
@@ -89,15 +87,18 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
-template <int TM, bool LORA>
+template <int TM, bool LORA, int T>
 __global__ void __launch_bounds__(kGThreads, 1)
 k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap ypmap,
         const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap amap,
         const __grid_constant__ GParams P) {
-    constexpr int ST = TM == 2 ? 3 : 4;                // stages
-    constexpr int SB = TM * kGABytes + kGBBytes;       // bytes per stage
+    constexpr int ROWS = kGN / T;                      // weight rows per stage
+    constexpr int YB = 128 * ROWS * 2;                 // bytes of dY per 128 tokens and stage
+    constexpr int AB = TM * YB > kGABytes ? TM * YB : kGABytes;  // bytes of operand A: dY, or P's tiles
+    constexpr int SB = AB + kGBBytes;                  // bytes per stage
+    constexpr int ST = kGStageSum / SB;                // stages
     constexpr int AC = 2 / TM;                         // accumulators of TM x 256 columns in TMEM
-    static_assert(ST * SB <= kGStageSum && ST <= kGMaxStages, "stage plan");
+    static_assert(ST <= kGMaxStages && SB % 1024 == 0, "stage plan");
     extern __shared__ __align__(1024) unsigned char gsmem[];
     __shared__ uint64_t bars[3 * kGMaxStages + 5];
     __shared__ uint32_t tmem_base_s;
@@ -122,8 +123,8 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
         int mt, kt, sp, st0, st1, sl0, slh, sl1;
     };
     const int rblocks = LORA ? (P.rp + 63) / 64 : 0;
-    // stages per slot and 64 ranks: P's terms in one stage (as one tile or TM = 2 of them), or one after the other
-    const int tstages = LORA && TM == 1 && P.terms_box == 1 ? 2 : 1;
+    // stages per slot and 64 ranks: P's terms in one stage (as one tile or, with room, two), or one after the other
+    const int tstages = LORA && AB < 2 * kGABytes && P.terms_box == 1 ? 2 : 1;
     auto item = [&](int w) {
         Item it;
         it.kt = w % P.ktiles;
@@ -290,11 +291,13 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
             if (++b == AC) { b = 0; bph ^= 1u; }
         }
     } else if (warp < kGTmaWarp) {
-        // ---------------- decode: 64 rows x four blocks of 64 k; eight lanes = the eight rows
-        // of one swizzle atom, so their 16-byte stores cover all banks ----------------
+        // ---------------- decode: eight lanes = the eight rows of one swizzle atom, so their 16-byte
+        // stores cover all banks; a thread has two words of a row, or (T = 2) both terms of one ----------------
         const int dt = threadIdx.x & 255, group = (warp - 8) >> 3;
-        const int r = (dt >> 5) * 8 + (lane & 7), blk = lane >> 3;
-        const uint32_t brow = (uint32_t)(TM * kGABytes + blk * (kGN * 128) + (r >> 3) * 1024 + (r & 7) * 128);
+        constexpr int W = 2 / T;  // words of a thread
+        const int r = (T == 1 ? dt >> 5 : (dt >> 5) & 3) * 8 + (lane & 7);
+        const int word = T == 1 ? 2 * (lane >> 3) : 4 * (dt >> 7) + (lane >> 3);  // (of the tile's eight)
+        const uint32_t brow = (uint32_t)(AB + (word >> 1) * (kGN * 128) + (r >> 3) * 1024 + (r & 7) * 128);
         const float inv = 1.0f / dgrad_unit(P.scales, P.nscales);
         int s = 0;
         uint32_t ph = 0;
@@ -302,65 +305,65 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
         bool ok = true;
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const Item it = item(w);
-            const int kw = it.kt * (kGK / 32) + 2 * blk;  // first of this thread's two words
-            int sc0 = 0, sc1 = 0;                          // their scales' places within a row
-            if (P.gran == SHERRY_PER_GROUP) {
-                sc0 = 32 * kw / P.group;
-                sc1 = 32 * (kw + 1) / P.group;
-            }
-            auto fetch = [&](int st, uint32_t* wd, uint32_t* sg, float* al) {
-                const int64_t n = (int64_t)st * kGN + r;
+            const int kw = it.kt * (kGK / 32) + word;  // first of this thread's words
+            int sc[W];                                 // their scales' places within a row
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < W; ++h) sc[h] = P.gran == SHERRY_PER_GROUP ? 32 * (kw + h) / P.group : 0;
+            auto fetch = [&](int st, uint32_t* wd, uint32_t* sg, float* al) {
+                const int64_t n = (int64_t)st * ROWS + r;
+#pragma unroll
+                for (int h = 0; h < W; ++h) {
                     wd[h] = 0u;
                     sg[h] = 0u;
                     al[h] = 0.0f;
                     if (st < it.st1 && n < P.N && kw + h < P.words) {
                         wd[h] = __ldg(P.idx + n * P.words + kw + h);
                         sg[h] = __ldg(P.sgn + n * P.words + kw + h);
-                        al[h] = __ldg(P.scales + (P.gran == SHERRY_PER_TENSOR ? 0 : n * P.spr + (h ? sc1 : sc0)));
+                        al[h] = __ldg(P.scales + (P.gran == SHERRY_PER_TENSOR ? 0 : n * P.spr + sc[h]));
                     }
                 }
             };
-            uint32_t wd[2], sg[2];
-            float al[2];
+            uint32_t wd[W], sg[W];
+            float al[W];
             fetch(it.st0 + ((turn ^ group) & 1), wd, sg, al);
             for (int st = it.st0; st < it.st1; ++st, ++turn) {
                 if (kGDecGroups > 1 && ((turn ^ group) & 1)) {  // the other group's
                     if (++s == ST) { s = 0; ph ^= 1u; }
                     continue;
                 }
-                uint32_t nwd[2], nsg[2];
-                float nal[2];
+                uint32_t nwd[W], nsg[W];
+                float nal[W];
                 fetch(st + kGDecGroups, nwd, nsg, nal);
                 if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
                 const uint32_t dst = base + (uint32_t)(s * SB) + brow;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < W; ++h) {
                     uint32_t ev, od;
                     spread_word(wd[h], sg[h], ev, od);
-                    const __nv_bfloat162 a2 = __float2bfloat162_rn(al[h] * inv);
-                    const uint32_t a = *reinterpret_cast<const uint32_t*>(&a2);
                     uint32_t v[16];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const uint32_t at = __byte_perm((j & 1) ? od : ev, table, (uint32_t)(j >> 1) | 0x7650u);
-                        uint32_t lo, hi;
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo) : "r"(at));
-                        asm volatile("ld.shared.u32 %0, [%1+128];" : "=r"(hi) : "r"(at));
-                        v[2 * j] = mul_bf16x2(lo, a);
-                        v[2 * j + 1] = mul_bf16x2(hi, a);
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[2 * j]) : "r"(at));
+                        asm volatile("ld.shared.u32 %0, [%1+128];" : "=r"(v[2 * j + 1]) : "r"(at));
                     }
+                    float x = al[h] * inv, same = x;
+                    const int half = T == 1 ? h : word & 1;  // of the 64 k that stand together
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        sts128(dst + (uint32_t)(((4 * h + c) ^ (r & 7)) * 16),
-                               make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
+                    for (int t = 0; t < T; ++t) {
+                        const uint32_t a = split_next(x, same);  // the term twice; x keeps what is left
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            sts128(dst + (uint32_t)(t * (ROWS * 128) + ((4 * half + c) ^ (r & 7)) * 16),
+                                   make_uint4(mul_bf16x2(v[4 * c], a), mul_bf16x2(v[4 * c + 1], a),
+                                              mul_bf16x2(v[4 * c + 2], a), mul_bf16x2(v[4 * c + 3], a)));
+                    }
                 }
                 fence_proxy_async();
                 mbar_arrive(full_b(s));
                 if (++s == ST) { s = 0; ph ^= 1u; }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < W; ++h) {
                     wd[h] = nwd[h];
                     sg[h] = nsg[h];
                     al[h] = nal[h];
@@ -376,7 +379,7 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
             }
         }
     } else if (warp == kGTmaWarp) {
-        // ---------------- TMA: dY tiles; in an adapters' stage the decode warps write both operands ----------------
+        // ---------------- TMA: dY tiles; in an adapters' stage both operands, P and A_a ----------------
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;
@@ -386,10 +389,10 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
                 const Item it = item(w);
                 for (int st = it.st0; st < it.st1; ++st) {
                     if (!mbar_wait(empty(s), ph ^ 1u, &abort_s)) { ok = false; break; }
-                    mbar_expect_tx(full_a(s), TM * kGABytes);
+                    mbar_expect_tx(full_a(s), TM * YB);
 #pragma unroll
                     for (int h = 0; h < TM; ++h)
-                        tma_load_2d(base + (uint32_t)(s * SB + h * kGABytes), LORA && permuted ? &ypmap : &ymap, st * kGN,
+                        tma_load_2d(base + (uint32_t)(s * SB + h * YB), LORA && permuted ? &ypmap : &ymap, st * ROWS,
                                     (it.mt * TM + h) * 128, full_a(s));
                     ++issued[s];
                     if (++s == ST) { s = 0; ph ^= 1u; }
@@ -425,7 +428,7 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
                                 tma_load_2d(dst + (uint32_t)(i * kGABytes), &pmap, (t0 + i) * P.rp + r0, sl * kLoraTile,
                                             full_a(s));
                             for (int c = 0; c < kGK / 64; ++c)
-                                tma_load_3d(dst + (uint32_t)(TM * kGABytes + c * kGN * 128), &amap, it.kt * kGK + 64 * c,
+                                tma_load_3d(dst + (uint32_t)(AB + c * kGN * 128), &amap, it.kt * kGK + 64 * c,
                                             r0, a, full_a(s));
                             ++issued[s];
                             if (++s == ST) { s = 0; ph ^= 1u; }
@@ -455,14 +458,14 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
                     }
                     bmask ^= 1u << s;
                     tc_fence_after();
-                    const uint64_t da = smem_desc(base + (uint32_t)(s * SB));
-                    const uint64_t db = smem_desc_mn(base + (uint32_t)(s * SB + TM * kGABytes), kGN * 128);
+                    const uint64_t da = T == 1 ? smem_desc(base + (uint32_t)(s * SB)) : smem_desc_64(base + (uint32_t)(s * SB));
+                    const uint64_t db = smem_desc_mn(base + (uint32_t)(s * SB + AB), kGN * 128);
 #pragma unroll
                     for (int kk = 0; kk < kGN / 16; ++kk)  // 16 rows: +32 bytes in A's row, two 8-row atoms of B
 #pragma unroll
                         for (int h = 0; h < TM; ++h)
                             mma_bf16_ss(tmem + (uint32_t)((TM == 2 ? h : b) * kGK),
-                                        da + (uint64_t)((h * kGABytes) >> 4) + (uint64_t)(2 * kk),
+                                        da + (uint64_t)((h * YB) >> 4) + (uint64_t)(2 * (kk % (ROWS / 16))),
                                         db + (uint64_t)(2 * kk * (1024 >> 4)), kGIdesc,
                                         (st == it.st0 && kk == 0) ? 0u : 1u);
                     mma_commit(empty(s));
@@ -480,7 +483,7 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
                                 continue;
                             }
                             const uint64_t dp = smem_desc(base + (uint32_t)(s * SB));
-                            const uint64_t da = smem_desc_mn(base + (uint32_t)(s * SB + TM * kGABytes), kGN * 128);
+                            const uint64_t da = smem_desc_mn(base + (uint32_t)(s * SB + AB), kGN * 128);
                             const int n16 = min(4, (P.rp - 64 * (u / tstages)) / 16);
                             for (int i = 0; i < 2 / tstages; ++i) {  // the stage's terms: in one tile, or one tile each
                                 const uint64_t term = (uint64_t)(P.terms_box == 2 ? i * P.rp / 8 : (i * kGABytes) >> 4);
@@ -544,23 +547,23 @@ static int lora_stages(int64_t M, int n_adapters, int R) {
 }
 
 struct GPlan {
-    int tm, mtiles, ktiles, splits, nstages;
+    int tm, mtiles, ktiles, splits;
 };
 
 // Two 128-token MMAs per CTA once that still gives every SM a tile (the decoded operand is then used
-// twice); rows split over CTAs where there are fewer tiles than SMs, at least 4 stages each.  (256-token tiles
+// twice); rows split over CTAs where there are fewer tiles than SMs, at least 256 each.  (256-token tiles
 // with split rows instead: 256 x 2048 x 2048 15 -> 20 us, 2171 x 2444 x 1920 43 -> 41 + 8 for the partial sums.)
 // lstages: stages of a token tile's adapters (at a time when its slots are not known)
 static GPlan dgrad_plan(int64_t M, int64_t N, int64_t K, int lstages, int sms) {
     GPlan g;
     g.ktiles = (int)((K + kGK - 1) / kGK);
-    g.nstages = (int)((N + kGN - 1) / kGN);
     g.tm = ((M + 255) / 256) * g.ktiles * 10 >= (int64_t)sms * 7 ? 2 : 1;
     g.mtiles = (int)((M + 128 * g.tm - 1) / (128 * g.tm));
     const int64_t tiles = (int64_t)g.mtiles * g.ktiles;
+    const int64_t parts = (N + 63) / 64;
     g.splits = 1;
     if (g.tm == 1 && tiles * 2 <= sms)
-        g.splits = (int)std::max<int64_t>(1, std::min<int64_t>({sms / tiles, (g.nstages + lstages) / 4, g.nstages}));
+        g.splits = (int)std::max<int64_t>(1, std::min<int64_t>({sms / tiles, (parts + lstages) / 4, parts}));
     return g;
 }
 
@@ -578,8 +581,9 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
                  int64_t ldy, int64_t M, uint16_t* dX, const LoraGradArgs* lora, void* workspace, int sms,
                  cudaStream_t stream) {
     const GPlan g = dgrad_plan(M, s.N, s.K, lora ? lora_stages(M, lora->n_adapters, lora->R) : 0, sms);
+    const int terms = s.granularity == SHERRY_PER_TENSOR ? 1 : 2;  // of alpha
     CUtensorMap map;
-    int st = encode_2d(&map, dY, ldy, M, 128);
+    int st = encode_2d(&map, dY, ldy, M, 128, kGN / terms);
     if (st) return st;
     GParams P{};
     P.idx = idx;
@@ -597,7 +601,7 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
     P.mtiles = g.mtiles;
     P.ktiles = g.ktiles;
     P.splits = g.splits;
-    P.nstages = g.nstages;
+    P.nstages = (int)((s.N * terms + kGN - 1) / kGN);
     CUtensorMap ypmap = map, pmap = map, amap = map;
     if (lora) {
         P.plan = lora->plan;
@@ -608,7 +612,7 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
         P.rp = lora->P.rp;
         P.terms_box = 2 * P.rp <= 64 ? 2 : 1;
         P.rows_box = std::min(P.rp, 64);
-        if (lora->Gp && (st = encode_2d(&ypmap, lora->Gp, ldy, M, 128))) return st;
+        if (lora->Gp && (st = encode_2d(&ypmap, lora->Gp, ldy, M, 128, kGN / terms))) return st;
         st = encode_2d(&pmap, lora->P.data, lora->P.terms * P.rp, (int64_t)lora->plan.max_slots * kLoraTile, 128);
         if (!st) st = encode_3d(&amap, lora->A, s.K, lora->R, lora->n_adapters, P.rows_box);
         if (st) return st;
@@ -616,10 +620,9 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
     static PerDevice once;
     int v = 0;
     st = per_device(once, &v, [](int& x) {
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_dgrad<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_dgrad<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_dgrad<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
-        SHERRY_CUDA_CHECK(cudaFuncSetAttribute(k_dgrad<2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
+        for (auto kernel : {k_dgrad<1, false, 1>, k_dgrad<1, false, 2>, k_dgrad<1, true, 1>, k_dgrad<1, true, 2>,
+                            k_dgrad<2, false, 1>, k_dgrad<2, false, 2>, k_dgrad<2, true, 1>, k_dgrad<2, true, 2>})
+            SHERRY_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem));
         x = 1;
         return SHERRY_OK;
     });
@@ -627,7 +630,9 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
     const int64_t items = (int64_t)g.mtiles * g.ktiles * g.splits;
     if (items > 0x7fffffff) return SHERRY_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)std::min<int64_t>(items, sms);
-    auto kernel = g.tm == 2 ? (lora ? k_dgrad<2, true> : k_dgrad<2, false>) : (lora ? k_dgrad<1, true> : k_dgrad<1, false>);
+    auto of = [&](auto one, auto two) { return terms == 1 ? one : two; };
+    auto kernel = g.tm == 2 ? (lora ? of(k_dgrad<2, true, 1>, k_dgrad<2, true, 2>) : of(k_dgrad<2, false, 1>, k_dgrad<2, false, 2>))
+                            : (lora ? of(k_dgrad<1, true, 1>, k_dgrad<1, true, 2>) : of(k_dgrad<1, false, 1>, k_dgrad<1, false, 2>));
     return launch_after(kernel, grid, kGThreads, kGSmem, stream, 1, lora != nullptr, map, ypmap, pmap, amap, P);
 }
 

@@ -51,8 +51,9 @@ __device__ __forceinline__ uint32_t split_next(float& x, float& y) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The input gradient multiplies bf16(alpha / unit): unit = (the mean of 32 scales spread over the weight's n) / kGTop
-// (dgrad.cu), or 1 where that is no ordinary number.  P is held in the same unit.  Called by whole warps.
+// The input gradient multiplies alpha / unit: unit = (the mean of 32 scales spread over the weight's n) / kGTop, so that
+// a per-tensor scale is one bf16 (dgrad.cu), or 1 where that is no ordinary number.  P is held in the same unit.
+// Called by whole warps.
 constexpr float kGTop = 1.71875f;
 __device__ __forceinline__ float dgrad_unit(const float* scales, int64_t n) {
     float a = __ldg(scales + n * (int64_t)(threadIdx.x & 31) / 32);

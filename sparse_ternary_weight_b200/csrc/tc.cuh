@@ -101,6 +101,17 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
     return d;
 }
 
+// K-major, 64-byte swizzled operand (rows of 64 bytes): 8-row atoms of 512 bytes
+__device__ __forceinline__ uint64_t smem_desc_64(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3fff);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)(512 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)4 << 61;  // SWIZZLE_64B
+    return d;
+}
+
 // MN-major, 128-byte swizzled operand (the contiguous axis is the one that is not summed over): atoms
 // of 64 elements x 8 rows (1024 B); the next 64 elements are `leading` bytes on, the next 8 rows 1024
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t leading) {
@@ -201,16 +212,17 @@ static EncodeTiled encode_fn() {
     return fn;
 }
 
-// bf16 [rows][inner] row-major, boxes of 64 elements (128 bytes, swizzled) x box_rows rows
-static int encode_2d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int box_rows) {
+// bf16 [rows][inner] row-major, boxes of 64 or 32 elements (128 or 64 bytes, swizzled) x box_rows rows
+static int encode_2d(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int box_rows, int box_cols = 64) {
     EncodeTiled enc = encode_fn();
     if (!enc) return SHERRY_ERR_UNSUPPORTED;
     const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SHERRY_OK : SHERRY_ERR_UNSUPPORTED;
 }

@@ -1,0 +1,72 @@
+"""Adapters, the input gradient and token log probabilities where they went wrong once:
+each test names the fault that it keeps out (needs a B200)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from tests.test_gpu_lora import Problem, host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sw():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_ternary_weight_b200.build import build
+    build()
+    import sparse_ternary_weight_b200 as sw
+    return sw
+
+
+# one and two 128-token halves per tile, rows split over CTAs or not, N that ends inside a stage
+ROUNDED = [
+    (1, 33, 256, "group", 128),
+    (64, 512, 2048, "group", 128),
+    (130, 100, 512, "channel", 0),
+    (200, 1000, 320, "group", 32),
+    (300, 65, 1024, "tensor", 0),
+    (1500, 97, 6688, "group", 32),
+    (1500, 160, 6656, "channel", 0),
+]
+
+
+@pytest.mark.parametrize("adapters", [False, True], ids=["plain", "adapters"])
+@pytest.mark.parametrize("case", ROUNDED, ids=lambda c: f"M{c[0]}-{c[1]}x{c[2]}-{c[3]}{c[4]}")
+def test_the_input_gradient_is_rounded_once(sw, orc, case, adapters):
+    """The scales enter dX with (more than) fp32 sums' own error: what is left is one rounding to bf16, 2^-8
+    of the value, beside 2^-15 of the terms' magnitudes for the fp32 sums and the split terms.  A scale rounded
+    to bf16 would be off by up to 2^-8 of every term."""
+    import torch
+    M, N, K, gname, group = case
+    pr = Problem(sw, orc, M, N, K, gname, group, 16, 3, "mixed")
+    if adapters:
+        dX = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, None, pr.scaling, torch.float32,
+                                     need=(True, False, False))[0]
+    else:
+        dX = sw.linear_backward(pr.G, pr.P)
+    assert sw.device_status() == 0
+    base, extra, _, _ = pr.backward()
+    mb, me, _, _ = pr.backward(True)
+    ref = base + (extra if adapters else 0)
+    sums = 2.0 ** -15 * (mb + (me if adapters else 0))
+    err = np.abs(host(dX) - ref)
+    assert np.all(err <= sums + 2.0 ** -8 * (np.abs(ref) + sums) + 1e-30), float((err / (sums + 2.0 ** -8 * np.abs(ref))).max())
+
+
+def test_scales_far_apart_keep_their_own_precision(sw, orc):
+    """Scales over 40 binades, zeros among them: each is kept to its own size, not to the largest's."""
+    import torch
+    pr = Problem(sw, orc, 40, 96, 512, "group", 128, 8, 2, "mixed")
+    rng = np.random.default_rng(8)
+    factor = 2.0 ** rng.integers(-30, 10, pr.P.scales.numel()).astype(np.float32)
+    factor[::13] = 0.0
+    pr.P.scales.mul_(torch.from_numpy(factor.astype(np.float32)).cuda())
+    pr.W = pr.W * np.repeat(factor, 128).reshape(96, 512)
+    dX = sw.linear_backward(pr.G, pr.P)
+    base = pr.backward()[0]
+    sums = 2.0 ** -15 * pr.backward(True)[0]
+    err = np.abs(host(dX) - base)
+    assert np.all(err <= sums + 2.0 ** -8 * (np.abs(base) + sums) + 1e-30)

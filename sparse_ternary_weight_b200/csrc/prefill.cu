@@ -218,7 +218,7 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             const int n = (t % ntn) * kPBM + q * 32 + lane;
             const int m0 = (t / ntn) * kPBN + half * kCols;
             const int2 sl = slots_of(t);
-            uint32_t own0[kCols / 32];  // the first slot's tokens among this thread's, once they are there
+            uint32_t own0[kCols / 32];  // the first slot's tokens among this thread's; of the first tile after the wait
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c)
                 own0[c] = LORA && t != (int)tile0 && sl.x < sl.y ? P.plan.mask[4 * sl.x + half * (kCols / 32) + c] : 0u;
@@ -261,7 +261,8 @@ k_prefill(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] *= a;
             if constexpr (LORA) {
-                if (sl.x < sl.y) pdl_wait();
+                // at the first tile, whether it has slots or not: from the second on the masks are read at the tile's start
+                if (t == (int)tile0) pdl_wait();
                 if (t == (int)tile0 && sl.x < sl.y) {
 #pragma unroll
                     for (int c = 0; c < kCols / 32; ++c) own0[c] = P.plan.mask[4 * sl.x + half * (kCols / 32) + c];

@@ -5,7 +5,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
-from tests.test_gpu_lora import Problem, host
+from tests.test_gpu_lora import Problem, check_dx, check_sum, host
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,51 @@ def test_scales_far_apart_keep_their_own_precision(sw, orc):
     sums = 2.0 ** -15 * pr.backward(True)[0]
     err = np.abs(host(dX) - base)
     assert np.all(err <= sums + 2.0 ** -8 * (np.abs(base) + sums) + 1e-30)
+
+
+def litter(value):
+    """Freed memory full of `value`, where the next calls' scratch lies."""
+    import torch
+    junk = [torch.full((n,), value, dtype=torch.uint8, device="cuda") for n in (1 << 18, 1 << 20, 4 << 20, 32 << 20)]
+    torch.cuda.synchronize()
+    del junk
+
+
+# more 128 x 128 tiles than SMs: several tiles per CTA, and phases that run on past adapters' chunks
+MANY = [
+    ("lead", 700, 4200, 256, "group", 128, 16, 3),
+    ("lead", 700, 4200, 256, "channel", 0, 128, 3),
+    ("lead", 900, 2700, 320, "group", 64, 72, 2),
+    ("lead", 640, 4300, 4352, "group", 128, 24, 2),
+    ("mixed", 700, 4200, 256, "group", 128, 16, 20),
+    ("gaps", 1100, 2690, 512, "tensor", 0, 40, 4),
+]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"{c[0]}-M{c[1]}-{c[2]}x{c[3]}-{c[4]}{c[5]}-r{c[6]}x{c[7]}")
+def test_more_tiles_than_sms(sw, orc, case, dt):
+    """CTAs that begin with a tile of tokens without an adapter and go on to tiles that have one: the slots' masks
+    are another kernel's results and are waited for all the same."""
+    import torch
+    kind, M, N, K, gname, group, R, n = case
+    pr = Problem(sw, orc, M, N, K, gname, group, R, n, "mixed" if kind == "mixed" else "sorted")
+    if kind != "mixed":
+        pr.ids[:256] = -1
+        pr.idsh[:256] = -1
+        if kind == "gaps":
+            pr.ids[512:768] = -1
+            pr.idsh[512:768] = -1
+    T = torch.float32 if dt == "f32" else torch.bfloat16
+    ref, U = pr.forward()
+    mag, Um = pr.forward(True)
+    first = None
+    for value in (0, 255, 85, 255):
+        litter(value)
+        y, u = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, T, return_u=True)
+        if first is None:
+            first = (y, u)
+            assert sw.device_status() == 0
+            check_sum(y, ref, mag, "Y", bf16=dt == "bf16")
+            check_sum(u, U, Um, "U")
+        assert torch.equal(y, first[0]) and torch.equal(u, first[1])

@@ -30,13 +30,16 @@ static inline int64_t lora_tiles(int64_t M) { return (M + kLoraTile - 1) / kLora
 // Slots that a call has room for.  One adapter after the other they are at most tiles + n_adapters;
 // tokens stay in place while they make no more than this: a slot too many costs each product a
 // masked pass over its tile, taking tokens in another order a copy of X or dY.
+// A slot holds a token, so in either order there are no more than M, however many adapters there are.
+static inline int64_t lora_slots_in_place(int64_t M, int n_adapters) {
+    return std::min(lora_tiles(M) * n_adapters, M);
+}
 static inline int64_t lora_max_slots(int64_t M, int n_adapters) {
-    const int64_t t = lora_tiles(M);
-    return std::min<int64_t>(2 * t + n_adapters, t * n_adapters);
+    return std::min(2 * lora_tiles(M) + n_adapters, lora_slots_in_place(M, n_adapters));
 }
 
 bool lora_may_permute(int64_t M, int n_adapters) {
-    return lora_tiles(M) * n_adapters > lora_max_slots(M, n_adapters);
+    return lora_slots_in_place(M, n_adapters) > lora_max_slots(M, n_adapters);
 }
 
 size_t lora_image_bytes(int64_t M, int n_adapters, int R, int terms) {

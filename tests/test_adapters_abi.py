@@ -116,3 +116,15 @@ def test_binding_rejects_cpu_tensors():
                  lambda: sw.linear_lora(x, P, a, b, ids)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_scratch_goes_by_the_tokens(L):
+    """A bank of many adapters costs a few tokens no more than the slots (tile, adapter) that they can make."""
+    fwd = lambda M, n, R=128: L.sherry_linear_lora_workspace_bytes(M, 8192, 4096, _abi.PER_GROUP, 128, n, R, _abi.BF16)  # noqa: E731
+    bwd = lambda M, n, R=128: L.sherry_linear_lora_backward_workspace_bytes(M, 8192, 4096, n, R)  # noqa: E731
+    # 100 tokens: at most 100 slots of 128 rows, two terms of U (bf16 Y), three of P and of U
+    slots = 100 * 128 * 128 * 2
+    base = fwd(100, 1) + 256 * 1024
+    assert fwd(100, 1024) <= base + 2 * slots + 64 * 1024
+    assert bwd(100, 1024) <= bwd(100, 1) + 2 * 3 * slots + 64 * 1024
+    assert fwd(100, 1024) - fwd(100, 512) <= 8 * 1024  # the plan's counts alone

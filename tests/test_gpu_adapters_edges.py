@@ -118,3 +118,21 @@ def test_more_tiles_than_sms(sw, orc, case, dt):
             check_sum(y, ref, mag, "Y", bf16=dt == "bf16")
             check_sum(u, U, Um, "U")
         assert torch.equal(y, first[0]) and torch.equal(u, first[1])
+
+
+@pytest.mark.parametrize("M", [90, 300])
+def test_a_large_bank_for_few_tokens(sw, orc, M):
+    """About as many slots as tokens: the scratch holds no more, and no token is lost."""
+    import torch
+    pr = Problem(sw, orc, M, 130, 256, "group", 128, 16, 1024, "mixed")
+    ref, U = pr.forward()
+    mag, Um = pr.forward(True)
+    y, u = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+    assert sw.device_status() == 0
+    check_sum(y, ref, mag, "Y")
+    check_sum(u, U, Um, "U")
+    dX, dA, dB = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, u, pr.scaling, torch.float32)
+    assert sw.device_status() == 0
+    check_dx(pr, dX)
+    for got, want, size in zip((dA, dB), pr.backward()[2:], pr.backward(True)[2:]):
+        check_sum(got, want, size, "gradient")

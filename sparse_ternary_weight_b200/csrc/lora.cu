@@ -77,7 +77,8 @@ LoraPlan lora_plan_in(void* mem, int64_t M, int n_adapters) {
 }
 
 // ---- plan ----------------------------------------------------------------------------
-// CTA 0 lists the slots, 32 tiles at a time: a warp marks its tile's adapters in a bitmap.
+// CTA 0 lists the slots, 32 tiles at a time: a warp marks its tile's adapters in a bitmap, whose
+// columns place each slot among its adapter's (work linear in the slots).
 // Where the plan may permute, one further CTA per bucket (an adapter, or none) reads all
 // ids: the tokens of smaller buckets are its offset, its own are compacted in order
 // (ballots), so the order depends on the ids alone.  ids stay in L2; one launch.
@@ -108,7 +109,9 @@ __device__ __forceinline__ int block_scan(int x, int* ws) {
 __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, const LoraPlan& plan) {
     __shared__ uint32_t bits[32][32];
     __shared__ int ws[32], cnt[SHERRY_MAX_ADAPTERS], found;
-    __shared__ uint16_t held[kPlanHeld];  // the first slots' adapters
+    __shared__ uint32_t col[SHERRY_MAX_ADAPTERS];  // which of the 32 tiles hold the adapter
+    __shared__ uint32_t held[kPlanHeld];  // the first slots' adapters, and their places << 10 among the adapter's slots
+    static_assert(SHERRY_MAX_ADAPTERS <= 1024 && kPlanHeld <= 1 << 22, "an adapter and a place in a word");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tiles = (int)plan.tiles;
     cnt[tid] = 0;
@@ -126,6 +129,12 @@ __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, con
             if (a < n && lane == __ffs(same) - 1) atomicOr(&bits[warp][a >> 5], 1u << (a & 31));
         }
         __syncthreads();
+        uint32_t tiles_of = 0;  // adapter tid's
+        if (32 * warp < n) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) tiles_of |= (bits[j][warp] >> lane & 1u) << j;
+        }
+        col[tid] = tiles_of;
         const uint32_t word = bits[warp][lane];
         const int mine = __popc(word), at = total + block_scan(mine, ws) - mine;
         if (lane == 0 && t < tiles) plan.tile_b[t] = at;
@@ -134,16 +143,19 @@ __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, con
             const uint32_t ws32 = __shfl_sync(kFull, word, w);
             const int s = __shfl_sync(kFull, at, w) + __popc(ws32 & ((1u << lane) - 1u)), a = 32 * w + lane;
             if (ws32 >> lane & 1u) {
+                const uint32_t place = (uint32_t)cnt[a] + __popc(col[a] & ((1u << warp) - 1u));
                 if (s < plan.max_slots) {
                     plan.slot_a[s] = a;
                     plan.slot_t[s] = t;
+                    if (s >= kPlanHeld) plan.mask[4 * (int64_t)s] = place;  // (the masks come later)
                 }
-                if (s < kPlanHeld) held[s] = (uint16_t)a;
-                atomicAdd(&cnt[a], 1);
+                if (s < kPlanHeld) held[s] = (uint32_t)a | place << 10;
             }
         }
         const int all = __reduce_add_sync(kFull, ws[lane]);
         total += all;
+        __syncthreads();
+        cnt[tid] += __popc(tiles_of);
     }
     __syncthreads();
     if (total <= plan.max_slots) {
@@ -153,12 +165,9 @@ __device__ __forceinline__ void plan_slots(const int32_t* ids, int M, int n, con
         if (tid == n - 1) plan.adap_b[n] = end;
         __syncthreads();
         for (int s = tid; s < total; s += kPlanThreads) {
-            const int a = s < kPlanHeld ? held[s] : plan.slot_a[s];
-            int before = 0;
-#pragma unroll 8
-            for (int j = 0; j < min(s, kPlanHeld); ++j) before += held[j] == a;
-            for (int j = kPlanHeld; j < s; ++j) before += plan.slot_a[j] == a;
-            plan.adap_s[cnt[a] + before] = s;
+            const uint32_t h = s < kPlanHeld ? held[s] : 0u;
+            const int a = s < kPlanHeld ? (int)(h & 1023u) : plan.slot_a[s];
+            plan.adap_s[cnt[a] + (s < kPlanHeld ? h >> 10 : plan.mask[4 * (int64_t)s])] = s;
         }
         if (tid == 0) {
             plan.head[0] = 0;

@@ -136,3 +136,22 @@ def test_a_large_bank_for_few_tokens(sw, orc, M):
     check_dx(pr, dX)
     for got, want, size in zip((dA, dB), pr.backward()[2:], pr.backward(True)[2:]):
         check_sum(got, want, size, "gradient")
+
+
+@pytest.mark.parametrize("M,n", [(384000, 2), (270000, 1), (150000, 700)])
+def test_slots_by_the_thousand(sw, orc, M, n):
+    """More slots than the plan holds in shared memory, in place and adapter by adapter; the plan's work is linear
+    in them."""
+    import torch
+    pr = Problem(sw, orc, M, 8, 64, "group", 32, 8, n, "mixed")
+    ref, U = pr.forward()
+    mag, Um = pr.forward(True)
+    y, u = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+    assert sw.device_status() == 0
+    check_sum(y, ref, mag, "Y")
+    check_sum(u, U, Um, "U")
+    dX, dA, dB = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, u, pr.scaling, torch.float32)
+    assert sw.device_status() == 0
+    check_dx(pr, dX)
+    for got, want, size in zip((dA, dB), pr.backward()[2:], pr.backward(True)[2:]):
+        check_sum(got, want, size, "gradient")

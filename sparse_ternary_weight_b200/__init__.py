@@ -511,6 +511,20 @@ def _same_device(device, *ts):
             raise ValueError("tensors must be on one CUDA device")
 
 
+def _planes(P, device):
+    """Refuses planes that are not what P's shape and granularity say: the kernels index them by those."""
+    import torch
+    words = P.N * (P.K // 32)
+    scales = lib().sherry_num_scales(P.N, P.K, P.granularity, P.group) if P.N else 0  # (below 0: the call reports why)
+    for t, dtypes, count, name in ((P.idx, (torch.int32, torch.uint32), words, "idx"), (P.sgn, (torch.uint8,), words, "sgn"),
+                                   (P.scales, (torch.float32,), scales, "scales")):
+        if t.device != device:
+            raise ValueError("tensors must be on one CUDA device")
+        if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < count or (name != "scales" and t.numel() != count):
+            raise ValueError(f"{name} of a packed [{P.N}, {P.K}] weight must be {count} contiguous elements of "
+                             f"{' or '.join(str(d) for d in dtypes)}")
+
+
 def _activations(X, K, what="X"):
     import torch
     _require_cuda(X)
@@ -523,7 +537,8 @@ def _adapters(X, P, A, B, ids, scaling):
     """Checked and contiguous (A, B, ids, scaling, n_adapters, rank)."""
     import torch
     _require_cuda(A, B, ids, scaling)
-    _same_device(X.device, P.idx, A, B, ids, scaling)
+    _planes(P, X.device)
+    _same_device(X.device, A, B, ids, scaling)
     if A.dtype != torch.bfloat16 or A.dim() != 3 or A.shape[2] != P.K:
         raise ValueError("A must be bf16 [n_adapters, rank, K]")
     n, R = A.shape[0], A.shape[1]
@@ -588,7 +603,7 @@ def linear_backward(dY, P: PackedWeight, out=None):
     """Input gradient of the packed linear: dX [M,K] = dY [M,N] (T alpha), bf16."""
     import torch
     dY = _activations(dY, P.N, "dY")
-    _same_device(dY.device, P.idx)
+    _planes(P, dY.device)
     M = dY.shape[0]
     out = _result(out, (M, P.K), torch.bfloat16, dY.device)
     with _on(dY.device):
@@ -852,7 +867,7 @@ def linear_logprobs(X, P: PackedWeight, targets=None, top: int = 0) -> TokenLogp
     vocabulary), a chunk of tokens at a time, so that only a chunk's logits exist."""
     import torch
     X = _activations(X, P.K)
-    _same_device(X.device, P.idx)
+    _planes(P, X.device)
     M = X.shape[0]
     if not 1 <= P.N <= _abi.MAX_VOCAB:
         raise ValueError(f"a head has 1 to {_abi.MAX_VOCAB} rows")

@@ -158,17 +158,18 @@ struct Lora {
     int64_t M, N, K, n, R;
     int gran, group;
 
+    // a plane of any shape; its elements are counted in read
+    static at::Tensor plane(Args& a, int i, at::ScalarType type) {
+        if (!THPVariable_Check(a.v[i])) return a.ok = false, at::Tensor();
+        return a.dense(i, type, THPVariable_Unpack(a.v[i]).dim());
+    }
+
     bool read(Args& a, int x, int i, int j) {
         X = a.dense(x, at::kBFloat16, 2);
         if (!a.ok) return false;
-        // planes are the library's own; their form was checked when they were made
-        for (int k = i; k < i + 3; ++k)
-            if (!THPVariable_Check(a.v[k]) || !THPVariable_Unpack(a.v[k]).is_cuda() ||
-                THPVariable_Unpack(a.v[k]).get_device() != a.dev)
-                return false;
-        idx = THPVariable_Unpack(a.v[i]);
-        sgn = THPVariable_Unpack(a.v[i + 1]);
-        scales = THPVariable_Unpack(a.v[i + 2]);
+        idx = plane(a, i, at::kInt);
+        sgn = plane(a, i + 1, at::kByte);
+        scales = plane(a, i + 2, at::kFloat);
         N = a.integer(i + 3);
         K = a.integer(i + 4);
         gran = (int)a.integer(i + 5);
@@ -181,6 +182,9 @@ struct Lora {
         M = X.size(0);
         n = A.size(0);
         R = A.size(1);
+        // the kernels index the planes by the shape and the granularity
+        const int64_t count = sherry_num_scales(N, K, gran, group);
+        if (count < 0 || idx.numel() != N * (K / 32) || sgn.numel() != idx.numel() || scales.numel() < count) return false;
         return N > 0 && M > 0 && X.size(1) == K && A.size(2) == K && is(B, {n, N, R}) && is(ids, {M}) &&
                is(scaling, {n}) && n >= 1 && n <= SHERRY_MAX_ADAPTERS && R >= 8 && R <= SHERRY_MAX_RANK && R % 8 == 0;
     }

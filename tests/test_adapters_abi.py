@@ -128,3 +128,31 @@ def test_scratch_goes_by_the_tokens(L):
     assert fwd(100, 1024) <= base + 2 * slots + 64 * 1024
     assert bwd(100, 1024) <= bwd(100, 1) + 2 * 3 * slots + 64 * 1024
     assert fwd(100, 1024) - fwd(100, 512) <= 8 * 1024  # the plan's counts alone
+
+
+def test_planes_are_what_the_weight_says():
+    """A packed weight whose planes are of another type, length or layout is refused, not read as it lies."""
+    import dataclasses
+
+    import torch
+    import sparse_ternary_weight_b200 as sw
+    cpu = torch.device("cpu")
+    P = sw.PackedWeight(torch.zeros(8, 2, dtype=torch.int32), torch.zeros(8, 2, dtype=torch.uint8), torch.zeros(16), 8, 64,
+                        _abi.PER_GROUP, 32)
+    sw._planes(P, cpu)
+    sw._planes(dataclasses.replace(P, granularity=_abi.PER_TENSOR), cpu)  # more scales than are read
+    sw._planes(dataclasses.replace(P, idx=P.idx.view(torch.uint32)), cpu)
+    for kw in bad_planes(P):
+        with pytest.raises(ValueError):
+            sw._planes(dataclasses.replace(P, **kw), cpu)
+    with pytest.raises(ValueError):
+        sw._planes(P, torch.device("meta"))
+
+
+def bad_planes(P):
+    """What is wrong with a plane of P, one thing at a time."""
+    import torch
+    two = lambda t: torch.stack([t, t], -1)[..., 0]  # noqa: E731  (every other element)
+    return [dict(idx=P.idx[:-1]), dict(idx=P.idx.long()), dict(idx=two(P.idx)), dict(idx=P.idx.t()), dict(sgn=P.sgn[:, :1]),
+            dict(sgn=P.sgn.int()), dict(sgn=two(P.sgn)), dict(scales=P.scales[:-1]), dict(scales=P.scales.double()),
+            dict(scales=P.scales.to(torch.bfloat16)), dict(scales=two(P.scales)), dict(N=P.N + 1), dict(N=P.N - 1)]

@@ -155,3 +155,22 @@ def test_slots_by_the_thousand(sw, orc, M, n):
     check_dx(pr, dX)
     for got, want, size in zip((dA, dB), pr.backward()[2:], pr.backward(True)[2:]):
         check_sum(got, want, size, "gradient")
+
+
+def test_planes_of_another_form_are_refused(sw, orc):
+    """By every call that takes a packed weight here, and before anything is launched."""
+    import dataclasses
+
+    import torch
+    from tests.test_adapters_abi import bad_planes
+    pr = Problem(sw, orc, 4, 64, 256, "group", 32, 16, 3)
+    _, U = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+    for kw in [*bad_planes(pr.P), dict(idx=pr.P.idx.cpu()), dict(sgn=pr.P.sgn.cpu()), dict(scales=pr.P.scales.cpu())]:
+        P = dataclasses.replace(pr.P, **kw)
+        G, B = (pr.G, pr.B) if P.N == 64 else (torch.zeros(4, P.N, dtype=torch.bfloat16, device="cuda"),
+                                               torch.zeros(3, P.N, 16, dtype=torch.bfloat16, device="cuda"))
+        for call in (lambda: sw.linear_lora(pr.X, P, pr.A, B, pr.ids, pr.scaling), lambda: sw.linear_backward(G, P),
+                     lambda: sw.linear_lora_backward(G, pr.X, P, pr.A, B, pr.ids, U, pr.scaling),
+                     lambda: sw.linear_logprobs(pr.X, P)):
+            with pytest.raises(ValueError):
+                call()

@@ -458,14 +458,20 @@ def unpack(P: PackedWeight, out=None):
 
 # ---- adapters and the input gradient -------------------------------------------------------------------
 
+_KEPT_BYTES = 4 << 20
+
+
 def _stream_workspace(nbytes: int, device) -> "object":
-    """A zero-filled linear workspace of this stream of ``device``.  Calls on different
-    streams may overlap, so each stream keeps its own; under graph capture each call
-    gets a buffer of its graph's own (zeroed by the graph), since a graph may be
-    replayed beside other graphs and eager calls."""
+    """A linear workspace (tickets zero) for a call on the current stream of ``device``.
+    Calls on different streams may overlap, so each stream keeps its own of up to 4 MB, which
+    saves a decode step the zeroing.  A larger one, mostly a chunk's logits or an fp32 Y, is the
+    call's own and goes back to the allocator; so is one under graph capture, since a graph may
+    be replayed beside other graphs and eager calls."""
     import torch
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    if nbytes > _KEPT_BYTES or torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf[:_abi.TICKET_BYTES].zero_()
+        return buf
     key = (device, "linear", _stream(device))
     seen = lib().sherry_timeout_count()
     if seen != _ws_timeouts[0]:

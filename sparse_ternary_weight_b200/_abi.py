@@ -18,6 +18,7 @@ MAX_K = 262144
 MAX_BATCH = 256
 MAX_RANK, MAX_ADAPTERS, MAX_TOP, MAX_VOCAB = 128, 1024, 32, 16777216
 NOALLOC_SCRATCH_BYTES = 16 << 20
+TICKET_BYTES = 256 << 10  # at the start of a linear workspace: zero before a call, left zero by it
 TEQUILA_ONES, TEQUILA_SIGN = 0, 1
 
 vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t

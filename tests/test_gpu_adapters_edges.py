@@ -174,3 +174,43 @@ def test_planes_of_another_form_are_refused(sw, orc):
                      lambda: sw.linear_logprobs(pr.X, P)):
             with pytest.raises(ValueError):
                 call()
+
+
+@pytest.mark.parametrize("what", ["head", "plain route"])
+def test_large_scratch_is_given_back(sw, what):
+    """A chunk's logits, and the fp32 Y under a bf16 one, do not outlive the call; their tickets are zeroed in
+    memory that held anything before, in eager calls and in replayed ones."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    N, K = (140000, 128) if what == "head" else (20000, 96)
+    P = sw.quantize_pack(0.05 * torch.randn((N, K), generator=gen, device="cuda"), "per_group", 32)
+    X = torch.randn((300, K), generator=gen, device="cuda").to(torch.bfloat16)
+    A = torch.randn((2, 8, K), generator=gen, device="cuda").to(torch.bfloat16)
+    B = torch.randn((2, N, 8), generator=gen, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(-1, 2, (300,), generator=gen, device="cuda", dtype=torch.int32)
+
+    def call():
+        if what == "head":
+            r = sw.linear_logprobs(X, P, ids, top=2)
+            return [r.logp, r.entropy, r.top_ids]
+        return [sw.linear_lora(X, P, A, B, ids, None, torch.bfloat16)]
+
+    with torch.cuda.stream(torch.cuda.Stream()):
+        before = torch.cuda.memory_allocated()
+        want = call()
+        kept = torch.cuda.memory_allocated() - before - sum(t.numel() * t.element_size() for t in want)
+        assert kept <= 5 << 20, kept
+        for value in (255, 1):
+            litter(value)
+            assert all(torch.equal(p, q) for p, q in zip(call(), want))
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert sw.device_status() == 0

@@ -338,7 +338,8 @@ size_t sherry_linear_lora_backward_workspace_bytes(int64_t M, int64_t N, int64_t
  *            element; read once.  1 <= V <= SHERRY_MAX_VOCAB
  *   targets  int32 [M], or NULL (then logp NULL)
  * -inf (a banned token) has p = 0.  A row of -inf only: logp -inf, entropy 0, stats
- * (-inf, 0), the lowest indices.  A row with NaN or +inf: NaN everywhere, top_ids -1.
+ * (-inf, 0), the lowest indices.  A row with NaN or +inf: NaN everywhere, top_ids -1
+ * (logp 0 all the same where the target is left out).
  * No workspace. */
 int sherry_token_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
                           int top, float* logp, float* entropy, float* stats, float* top_logp, int32_t* top_ids,
@@ -349,7 +350,8 @@ int sherry_token_logprobs(const void* logits, int dtype, int64_t M, int64_t V, i
  *   dlogp    fp32 [M], or NULL (0); dentropy  fp32 [M], or NULL (0)
  *   dlogits  [M][V] in the logits' type, rows ldd >= V apart; may be logits itself with
  *            ldd = ld, otherwise must not overlap it
- * Exactly 0 where p is 0 (the target apart) and in rows of -inf only. */
+ * Exactly 0 where p is 0 (the target apart), in rows of -inf only, and in rows whose
+ * target is left out (or targets NULL) and h is 0 or absent, whatever they hold. */
 int sherry_token_logprobs_backward(const void* logits, int dtype, int64_t M, int64_t V, int64_t ld,
                                    const int32_t* targets, const float* stats, const float* entropy,
                                    const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,

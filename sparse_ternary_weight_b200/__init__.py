@@ -768,7 +768,7 @@ def token_logprobs(logits, targets=None, top: int = 0) -> TokenLogprobs:
     """Log probabilities of one given token per row, the entropy, and the ``top`` likeliest
     tokens (ties to the lowest id) of logits [M,V] (fp32 or bf16; rows may be slices of
     a padded buffer), in one pass.  targets is int32 or int64 [M]; a value outside
-    [0, V) is left out (log p 0, no gradient).  -inf logits have p = 0; a row of -inf
+    [0, V) is left out (log p 0, and no gradient even where the row holds NaN).  -inf logits have p = 0; a row of -inf
     only gives -inf and entropy 0, one with NaN or +inf gives NaN and ids -1."""
     r = _done(_calls().token_logprobs(logits, targets, top), "token_logprobs")
     if r is not None:

@@ -595,6 +595,20 @@ __global__ void __launch_bounds__(TH) k_logprobs_bwd(const LpBwdParams P) {
     const float g = (t < 0 || dead) ? 0.0f : P.dlogp[rowi];
     const float h = P.dentropy ? P.dentropy[rowi] : 0.0f;
     const float H = P.dentropy ? P.entropy[rowi] : 0.0f;
+    if (t < 0 && h == 0.0f) {  // left out: zeros, whatever the row holds (padding may hold NaN)
+#pragma unroll
+        for (int u = 0; u < kLpBwdVecs; ++u) {
+            const int v = vb + u * TH, e0 = off + N * v;
+            if (v >= nv) break;
+            if (e0 >= 0 && e0 + N <= V) {
+                __stcs(reinterpret_cast<uint4*>(out + e0), make_uint4(0u, 0u, 0u, 0u));
+            } else {
+                for (int j = 0; j < N; ++j)
+                    if (e0 + j >= 0 && e0 + j < V) out[e0 + j] = LpVec<T>::round(0.0f);
+            }
+        }
+        return;
+    }
     // -p (g + h (log p + H)), two elements an instruction
     const float k = -fmaf(h, H, g);
     const uint64_t m2 = pair(-m, -m), l2 = pair(-lsum, -lsum), h2 = pair(-h, -h), k2 = pair(k, k), L2 = pair(kLog2e, kLog2e);

@@ -214,3 +214,39 @@ def test_large_scratch_is_given_back(sw, what):
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, want))
     assert sw.device_status() == 0
+
+
+@pytest.mark.parametrize("V,pad", [(1003, 0), (4097, 3), (50257, 64)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rows_left_out_pass_nothing_on(sw, V, pad, dt):
+    """Padding rows (target -1) may hold NaN and infinities: log p 0, and a gradient of exact zeros, not NaN."""
+    import torch
+    T = torch.float32 if dt == "f32" else torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn((6, V + pad), generator=gen, device="cuda").to(T)[:, :V]
+    t = torch.tensor([1, -1, 2, -1, V, 5], dtype=torch.int32, device="cuda")
+    left = torch.tensor([1, 3, 4], device="cuda")
+    g = torch.rand(6, generator=gen, device="cuda") + 0.5
+    r = sw.token_logprobs(z, t)
+    want = sw.token_logprobs_backward(z, t, r.stats, r.entropy, g)
+    assert not want[left].any()
+    z[1] = float("nan")
+    z[3, ::3] = float("inf")
+    z[4, 17] = float("nan")
+    r = sw.token_logprobs(z, t)
+    assert not r.logp[left].any() and bool(torch.isnan(r.entropy[left]).all())
+    zero = torch.zeros(6, device="cuda")
+    for got in (sw.token_logprobs_backward(z, t, r.stats, r.entropy, g), sw.token_logprobs_backward(z, t, r.stats, None, g),
+                sw.token_logprobs_backward(z, t, r.stats, r.entropy, g, zero),
+                sw.token_logprobs_backward(z, t, r.stats, r.entropy, g, out=torch.full_like(z, 7.0))):
+        assert torch.equal(got, want)
+    x = z.clone().requires_grad_()
+    (sw.token_logprobs_train(x, t)[0] * g).sum().backward()
+    # (a copy without the padding: its rows are aligned otherwise, so their sums have another order; the same bits
+    # as the explicit calls on that copy)
+    rx = sw.token_logprobs(x.detach(), t)
+    assert torch.equal(x.grad, sw.token_logprobs_backward(x.detach(), t, rx.stats, None, g)) and not x.grad[left].any()
+    # with an entropy gradient of its own the row counts, and shows its NaN
+    h = zero.clone()
+    h[1] = 1.0
+    assert bool(torch.isnan(sw.token_logprobs_backward(z, t, r.stats, r.entropy, g, h)[1]).all())

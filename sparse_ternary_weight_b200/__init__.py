@@ -664,9 +664,10 @@ def linear_lora_backward(dY, X, P: PackedWeight, A, B, ids, U, scaling=None, gra
 def _refuse_capture(what, explicit):
     """Autograd's accumulation of a leaf's gradient runs on the stream where an earlier
     graph of the same leaf was built; under capture that ends the capture, and the
-    process with it.  So the differentiable forms are not captured."""
+    process with it.  So the differentiable forms are not captured, neither forward nor
+    the backward pass of an eager call."""
     import torch
-    if torch.cuda.is_initialized() and torch.is_grad_enabled() and torch.cuda.is_current_stream_capturing():
+    if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
         raise RuntimeError(f"{what} cannot be captured into a CUDA graph: capture {explicit}")
 
 
@@ -687,9 +688,9 @@ def _lora_function():
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dY):
+            _refuse_capture("the backward pass of linear_lora_train", "linear_lora_backward")
             X, A, B, ids, scaling, U = ctx.saved_tensors
             need = ctx.needs_input_grad[:3]
-            # an fp32 gradient is rounded to the bf16 that the tensor cores multiply
             dX, dA, dB = linear_lora_backward(dY.to(torch.bfloat16), X, ctx.packed, A, B, ids, U, scaling, need=need)
             return dX, dA, dB, None, None, None, None
 
@@ -701,9 +702,12 @@ _LORA = None
 
 def linear_lora_train(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None):
     """Differentiable :func:`linear_lora`: gradients reach X, A and B (bf16, as the
-    tensors); the packed weight is frozen."""
+    tensors); the packed weight is frozen and ``scaling`` a constant.  An fp32 gradient
+    of Y is rounded to the bf16 that the tensor cores multiply."""
     global _LORA
-    _refuse_capture("linear_lora_train", "linear_lora and linear_lora_backward")
+    import torch
+    if torch.is_grad_enabled():
+        _refuse_capture("linear_lora_train", "linear_lora and linear_lora_backward")
     if _LORA is None:
         _LORA = _lora_function()
     return _LORA.apply(X, A, B, P, ids, scaling, out_dtype)
@@ -847,6 +851,7 @@ def _logprobs_function():
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dlogp, dentropy):
+            _refuse_capture("the backward pass of token_logprobs_train", "token_logprobs_backward")
             if dlogp is None and dentropy is None:
                 return None, None
             logits, targets, stats, entropy = ctx.saved_tensors
@@ -862,7 +867,9 @@ def token_logprobs_train(logits, targets):
     """Differentiable (log p(target), entropy) of every row; the loss of a model is, say,
     ``-logp.mean()``."""
     global _LOGPROBS
-    _refuse_capture("token_logprobs_train", "token_logprobs and token_logprobs_backward")
+    import torch
+    if torch.is_grad_enabled():
+        _refuse_capture("token_logprobs_train", "token_logprobs and token_logprobs_backward")
     if _LOGPROBS is None:
         _LOGPROBS = _logprobs_function()
     return _LOGPROBS.apply(logits, targets)

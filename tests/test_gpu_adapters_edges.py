@@ -250,3 +250,27 @@ def test_rows_left_out_pass_nothing_on(sw, V, pad, dt):
     h = zero.clone()
     h[1] = 1.0
     assert bool(torch.isnan(sw.token_logprobs_backward(z, t, r.stats, r.entropy, g, h)[1]).all())
+
+
+@pytest.mark.parametrize("what", ["adapters", "log probabilities"])
+def test_the_backward_pass_of_an_eager_call_is_not_captured(sw, orc, what):
+    """Refused as the capture of the whole step is; the graph that was built stays usable."""
+    import torch
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        pr = Problem(sw, orc, 6, 64, 256, "group", 128, 8, 2)
+        leaf = (pr.A if what == "adapters" else pr.G).clone().requires_grad_()
+        if what == "adapters":
+            y = sw.linear_lora_train(pr.X, pr.P, leaf, pr.B, pr.ids, pr.scaling)
+        else:
+            y = sw.token_logprobs_train(leaf, pr.ids)[0]
+        dy = torch.ones_like(y)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(RuntimeError, match="captured"):
+            with torch.cuda.graph(graph, stream=s):
+                y.backward(dy, retain_graph=True)
+        assert leaf.grad is None
+        y.backward(dy)
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(leaf.grad).all()) and bool(leaf.grad.any())

@@ -592,8 +592,6 @@ def linear_lora(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None, out
     M = X.shape[0]
     out = _result(out, (M, P.N), out_dtype, X.device)
     U = torch.empty((M, R), dtype=torch.float32, device=X.device) if return_u else None
-    if return_u and P.N == 0:
-        U.zero_()
     with _on(X.device):
         L = lib()
         wsb = L.sherry_linear_lora_workspace_bytes(M, P.N, P.K, P.granularity, P.group, n, R, yd)

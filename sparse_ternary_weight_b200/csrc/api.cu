@@ -659,10 +659,20 @@ int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const
     if ((st = check_linear_desc(d, M))) return st;
     if (y_dtype != SHERRY_F32 && y_dtype != SHERRY_BF16) return SHERRY_ERR_DTYPE;
     if (M > 0 && N > 0 && (!A || !B || !ids)) return SHERRY_ERR_NULL;
+    if (M > 0 && U && (!X || !A || !ids)) return SHERRY_ERR_NULL;
     if (!aligned(A, 16) || !aligned(B, 16) || !aligned(ids, 4) || !aligned(scaling, 4) || !aligned(U, 16))
         return SHERRY_ERR_ALIGN;
-    if (M == 0 || N == 0) return SHERRY_OK;
     const ProbShape s{N, K, granularity, group};
+    if (N == 0 && U) {  // no outputs, but U does not depend on them
+        constexpr int64_t kRows = 32768;  // (tokens are the grid's second axis)
+        for (int64_t m = 0; m < M && !st; m += kRows) {
+            d.X = X + m * K;
+            st = lora_down_few_launch(s, d, std::min(kRows, M - m), A, rank, ids + m, scaling, n_adapters, U + m * rank,
+                                      static_cast<cudaStream_t>(stream));
+        }
+        return st;
+    }
+    if (M == 0 || N == 0) return SHERRY_OK;
     const LoraWs w = lora_ws(s, M, n_adapters, rank, y_dtype);
     if ((st = check_ws(workspace, workspace_bytes, w.total))) return st;
     char* ws = static_cast<char*>(workspace);

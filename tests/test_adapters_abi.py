@@ -156,3 +156,10 @@ def bad_planes(P):
     return [dict(idx=P.idx[:-1]), dict(idx=P.idx.long()), dict(idx=two(P.idx)), dict(idx=P.idx.t()), dict(sgn=P.sgn[:, :1]),
             dict(sgn=P.sgn.int()), dict(sgn=two(P.sgn)), dict(scales=P.scales[:-1]), dict(scales=P.scales.double()),
             dict(scales=P.scales.to(torch.bfloat16)), dict(scales=two(P.scales)), dict(N=P.N + 1), dict(N=P.N - 1)]
+
+
+def test_u_without_outputs_needs_its_inputs(L):
+    f = lambda **kw: L.sherry_linear_lora(*lora_args(**{**dict(N=0, U=FAKE, idx=None, sgn=None, sc=None, B=None, Y=None), **kw}))  # noqa: E731
+    for k in ("X", "A", "ids"):
+        assert f(**{k: None}) == _abi.ERR_NULL, k
+    assert f(U=FAKE + 4) == _abi.ERR_ALIGN and f(M=0, X=None, A=None, ids=None) == _abi.OK

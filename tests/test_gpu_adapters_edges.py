@@ -274,3 +274,15 @@ def test_the_backward_pass_of_an_eager_call_is_not_captured(sw, orc, what):
         y.backward(dy)
         torch.cuda.synchronize()
         assert bool(torch.isfinite(leaf.grad).all()) and bool(leaf.grad.any())
+
+
+@pytest.mark.parametrize("M", [1, 5, 33000])
+def test_u_of_a_weight_without_rows(sw, orc, M):
+    """U = s_a X A_a^T does not depend on the weight's rows: it is the same beside none."""
+    import torch
+    pr = Problem(sw, orc, M, 8, 64, "group", 32, 8, 3, "mixed")
+    none = sw.PackedWeight(pr.P.idx[:0], pr.P.sgn[:0], pr.P.scales[:0], 0, 64, pr.P.granularity, 32)
+    litter(255)
+    y, u = sw.linear_lora(pr.X, none, pr.A, pr.B[:, :0], pr.ids, pr.scaling, return_u=True)
+    assert sw.device_status() == 0 and y.shape == (M, 0)
+    check_sum(u, pr.forward()[1], pr.forward(True)[1], "U")

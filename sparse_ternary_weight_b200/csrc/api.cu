@@ -690,7 +690,7 @@ int sherry_linear_lora(const uint16_t* X, int64_t M, int64_t N, int64_t K, const
         down.G = X;
         if (w.xp) {
             const LoraRows rows{X, reinterpret_cast<uint16_t*>(ws + w.xp), K, K, 0};
-            if ((st = lora_rows_launch(&rows, 1, M, plan, cs))) return st;
+            if ((st = lora_rows_launch(&rows, 1, M, plan, sms, cs))) return st;
             down.Gp = rows.dst;
         }
         down.ldg = down.C = K;
@@ -780,7 +780,7 @@ int sherry_linear_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, 
     const uint16_t* G = dY;
     if (ld != N) {
         const LoraRows rows{dY, reinterpret_cast<uint16_t*>(ws + w.g), N, ld, 1};
-        if ((st = lora_rows_launch(&rows, 1, M, LoraPlan{}, cs))) return st;
+        if ((st = lora_rows_launch(&rows, 1, M, LoraPlan{}, device_sms(), cs))) return st;
         G = rows.dst;
     }
     const ProbShape s{N, K, granularity, group};
@@ -830,7 +830,7 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     uint16_t* xp = reinterpret_cast<uint16_t*>(ws + w.xp);
     if (ld != N || plan.may_permute) rows[copies++] = LoraRows{dY, g, N, ld, ld != N};
     if (dA && plan.may_permute) rows[copies++] = LoraRows{X, xp, K, K, 0};
-    if (copies && (st = lora_rows_launch(rows, copies, M, plan, cs))) return st;
+    if (copies && (st = lora_rows_launch(rows, copies, M, plan, sms, cs))) return st;
     const uint16_t* G = ld != N ? g : dY;
     const uint16_t* Gp = plan.may_permute ? g : nullptr;
     const LoraImage imgp{reinterpret_cast<uint16_t*>(ws + w.imgp), lora_rp(rank), terms};

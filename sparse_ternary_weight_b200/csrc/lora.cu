@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_lora_rows(const RowsParams P) 
     }
 }
 
-int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan& plan, cudaStream_t stream) {
+int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan& plan, int sms, cudaStream_t stream) {
     RowsParams P{};
     P.M = M;
     P.count = count;
@@ -335,7 +335,7 @@ int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan&
         always = always || jobs[j].always;
     }
     // copies that are seldom made have few CTAs to start and end for nothing (331 x 2050 x 8192: 46 -> 43 us)
-    const unsigned grid = (unsigned)std::min<int64_t>((pieces + kRowsThreads - 1) / kRowsThreads, always ? 148 * 8 : 148 * 2);
+    const unsigned grid = (unsigned)std::min<int64_t>((pieces + kRowsThreads - 1) / kRowsThreads, (always ? 8 : 2) * (int64_t)sms);
     auto kernel = pieces < (int64_t)1 << 29 ? k_lora_rows<uint32_t> : k_lora_rows<uint64_t>;
     return launch_after(kernel, grid, kRowsThreads, 0, stream, 1, plan.head != nullptr, P);
 }

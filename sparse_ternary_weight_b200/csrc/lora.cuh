@@ -113,7 +113,7 @@ struct LoraRows {
     int64_t N, ld;
     int always;
 };
-int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan& plan, cudaStream_t stream);
+int lora_rows_launch(const LoraRows* jobs, int count, int64_t M, const LoraPlan& plan, int sms, cudaStream_t stream);
 
 // V[m][r] = scaling[a] * sum_c G[m][c] W_a(r, c), a the token's adapter, as fp32 rows (zero for tokens
 // of none) and / or as an image; and the image of rows V2 that are there already.

@@ -493,7 +493,11 @@ def _calls():
     which the wrappers then convert or refuse themselves, and an int for a status."""
     if _native[0] is None:
         lib()  # a missing library is reported in its own words
-        from . import _binding as module
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing or was built for another torch; build it with "
+                               "`python -m sparse_ternary_weight_b200.build`") from e
         _native[0] = module
     return _native[0]
 

@@ -245,7 +245,7 @@ PyObject* linear_lora_backward(PyObject*, PyObject* const* args, Py_ssize_t narg
 #define SHERRY_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SHERRY_METHOD(token_logprobs), SHERRY_METHOD(token_logprobs_backward), SHERRY_METHOD(linear_lora),
                          SHERRY_METHOD(linear_lora_backward), {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

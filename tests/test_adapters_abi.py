@@ -163,3 +163,16 @@ def test_u_without_outputs_needs_its_inputs(L):
     for k in ("X", "A", "ids"):
         assert f(**{k: None}) == _abi.ERR_NULL, k
     assert f(U=FAKE + 4) == _abi.ERR_ALIGN and f(M=0, X=None, A=None, ids=None) == _abi.OK
+
+
+def test_a_missing_binding_is_reported(monkeypatch):
+    """In its own words, as a missing library is: there is no other form of the calls to fall back to."""
+    import sys
+
+    import torch
+    import sparse_ternary_weight_b200 as sw
+    monkeypatch.setattr(sw, "_native", [None])
+    monkeypatch.setitem(sys.modules, "sparse_ternary_weight_b200._binding", None)
+    monkeypatch.delattr(sw, "_binding", raising=False)
+    with pytest.raises(RuntimeError, match="sparse_ternary_weight_b200.build"):
+        sw.token_logprobs(torch.zeros(2, 8))

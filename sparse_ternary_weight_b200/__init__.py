@@ -543,6 +543,13 @@ def _activations(X, K, what="X"):
     return X.contiguous()
 
 
+def _output_gradient(dY, N):
+    """dY as the kernels take it: rows of a batch whose rows are not a multiple of 16 bytes may start
+    anywhere (a slice, a split's share of a gradient), and are then copied."""
+    dY = _activations(dY, N, "dY")
+    return dY.clone() if dY.data_ptr() % 16 else dY
+
+
 def _adapters(X, P, A, B, ids, scaling):
     """Checked and contiguous (A, B, ids, scaling, n_adapters, rank)."""
     import torch
@@ -610,7 +617,7 @@ def linear_lora(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None, out
 def linear_backward(dY, P: PackedWeight, out=None):
     """Input gradient of the packed linear: dX [M,K] = dY [M,N] (T alpha), bf16."""
     import torch
-    dY = _activations(dY, P.N, "dY")
+    dY = _output_gradient(dY, P.N)
     _planes(P, dY.device)
     M = dY.shape[0]
     out = _result(out, (M, P.K), torch.bfloat16, dY.device)
@@ -637,7 +644,7 @@ def linear_lora_backward(dY, X, P: PackedWeight, A, B, ids, U, scaling=None, gra
               "linear_lora_backward")
     if r is not None:
         return r
-    dY = _activations(dY, P.N, "dY")
+    dY = _output_gradient(dY, P.N)
     X = _activations(X, P.K)
     M = X.shape[0]
     if dY.shape[0] != M:

@@ -224,7 +224,7 @@ PyObject* linear_lora_backward(PyObject*, PyObject* const* args, Py_ssize_t narg
         if (!l.read(a, 1, 2, 9)) Py_RETURN_NONE;
         const at::Tensor dY = a.dense(0, at::kBFloat16, 2), U = a.dense(13, at::kFloat, 2, true);
         const int gd = (int)a.integer(14), need = (int)a.integer(15);
-        if (!a.ok || !is(dY, {l.M, l.N}) || !is(U, {l.M, l.R}) || ((need & 4) && !U.defined())) Py_RETURN_NONE;
+        if (!a.ok || !is(dY, {l.M, l.N}) || reinterpret_cast<uintptr_t>(ptr(dY)) % 16 != 0 || !is(U, {l.M, l.R}) || ((need & 4) && !U.defined())) Py_RETURN_NONE;
         const at::ScalarType type = gd == SHERRY_BF16 ? at::kBFloat16 : at::kFloat;
         at::Tensor dX, dA, dB, ws;
         if (need & 1) dX = a.empty({l.M, l.K}, at::kBFloat16);

@@ -286,3 +286,29 @@ def test_u_of_a_weight_without_rows(sw, orc, M):
     y, u = sw.linear_lora(pr.X, none, pr.A, pr.B[:, :0], pr.ids, pr.scaling, return_u=True)
     assert sw.device_status() == 0 and y.shape == (M, 0)
     check_sum(u, pr.forward()[1], pr.forward(True)[1], "U")
+
+
+@pytest.mark.parametrize("N", [129, 130, 132, 136])
+def test_gradients_of_a_slice_of_a_batch(sw, orc, N):
+    """Rows of dY that start off a 16-byte boundary, as any row of an odd length does."""
+    import torch
+    pr = Problem(sw, orc, 40, N, 256, "group", 128, 16, 3, "mixed")
+    _, U = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, return_u=True)
+    want = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, U, pr.scaling)
+    plain = sw.linear_backward(pr.G, pr.P)
+    for first in (1, 2, 3):
+        rows = torch.full((first + 40, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+        rows[first:] = pr.G
+        G = rows[first:]
+        assert G.is_contiguous()
+        got = sw.linear_lora_backward(G, pr.X, pr.P, pr.A, pr.B, pr.ids, U, pr.scaling)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        assert torch.equal(sw.linear_backward(G, pr.P), plain)
+    # under autograd: two calls' outputs put together
+    A = pr.A.clone().requires_grad_()
+    part = lambda a, b: sw.linear_lora_train(pr.X[a:b], pr.P, A, pr.B, pr.ids[a:b], pr.scaling, torch.bfloat16)  # noqa: E731
+    torch.cat([part(0, 3), part(3, 40)]).backward(pr.G)
+    both = [sw.linear_lora_backward(pr.G[a:b], pr.X[a:b], pr.P, pr.A, pr.B, pr.ids[a:b], U[a:b], pr.scaling)[1]
+            for a, b in ((0, 3), (3, 40))]
+    # (the order of the two is autograd's: a sum of two bf16 numbers does not depend on it)
+    assert torch.equal(A.grad, both[0] + both[1])

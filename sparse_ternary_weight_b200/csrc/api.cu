@@ -841,7 +841,7 @@ int sherry_linear_lora_backward(const uint16_t* dY, const uint16_t* X, int64_t M
     if (dX) {
         down.A = A;
         down.K = K;
-        down.beside_ctas = dgrad_ctas(M, N, K, n_adapters, rank, sms);
+        down.beside_ctas = dgrad_ctas(s, M, n_adapters, rank, sms);
     }
     if (dX || dA) {
         down.G = G;

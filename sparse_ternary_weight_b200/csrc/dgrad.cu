@@ -547,41 +547,46 @@ static int lora_stages(int64_t M, int n_adapters, int R) {
 }
 
 struct GPlan {
-    int tm, mtiles, ktiles, splits;
+    int tm, mtiles, ktiles, splits, nstages;
 };
+// bf16 terms of alpha
+static int alpha_terms(const ProbShape& s) { return s.granularity == SHERRY_PER_TENSOR ? 1 : 2; }
 
 // Two 128-token MMAs per CTA once that still gives every SM a tile (the decoded operand is then used
-// twice); rows split over CTAs where there are fewer tiles than SMs, at least 256 each.  (256-token tiles
-// with split rows instead: 256 x 2048 x 2048 15 -> 20 us, 2171 x 2444 x 1920 43 -> 41 + 8 for the partial sums.)
-// lstages: stages of a token tile's adapters (at a time when its slots are not known)
-static GPlan dgrad_plan(int64_t M, int64_t N, int64_t K, int lstages, int sms) {
+// twice); rows split over CTAs where there are fewer tiles than SMs, at least 4 stages each, or beside adapters
+// 256 rows, since their gradients take the SMs that are left (group scales, 128 / 256 rows at least, in us: 280 x 616 x
+// 2048 plain 14.4 / 16.5, with adapters 33 / 30; 64 x 2048 x 2048 16.4 / 16.5 and 31 / 27.5).  (With one term, 256-token
+// tiles with split rows instead: 256 x 2048 x 2048 15 -> 20 us, 2171 x 2444 x 1920 43 -> 41 + 8 for the partial sums.)
+// lstages: 64-row stages that a token tile's adapters are worth (at a time when its slots are not known)
+static GPlan dgrad_plan(int64_t M, int64_t N, int64_t K, int terms, int lstages, int sms) {
     GPlan g;
     g.ktiles = (int)((K + kGK - 1) / kGK);
     g.tm = ((M + 255) / 256) * g.ktiles * 10 >= (int64_t)sms * 7 ? 2 : 1;
     g.mtiles = (int)((M + 128 * g.tm - 1) / (128 * g.tm));
     const int64_t tiles = (int64_t)g.mtiles * g.ktiles;
-    const int64_t parts = (N + 63) / 64;
+    g.nstages = (int)((N * terms + kGN - 1) / kGN);
     g.splits = 1;
     if (g.tm == 1 && tiles * 2 <= sms)
-        g.splits = (int)std::max<int64_t>(1, std::min<int64_t>({sms / tiles, (parts + lstages) / 4, parts}));
+        g.splits = (int)std::max<int64_t>(1, std::min<int64_t>({sms / tiles, (g.nstages + lstages * terms) / (lstages ? 4 * terms : 4), g.nstages}));
     return g;
 }
 
 size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int n_adapters, int R, int sms) {
-    const GPlan g = dgrad_plan(M, N, K, lora_stages(M, n_adapters, R), sms);
-    return g.splits > 1 ? (size_t)g.splits * (size_t)(M * K) * sizeof(float) : 0;
+    int splits = 1;  // the more of either form's
+    for (int terms : {1, 2}) splits = std::max(splits, dgrad_plan(M, N, K, terms, lora_stages(M, n_adapters, R), sms).splits);
+    return splits > 1 ? (size_t)splits * (size_t)(M * K) * sizeof(float) : 0;
 }
 
-int64_t dgrad_ctas(int64_t M, int64_t N, int64_t K, int n_adapters, int R, int sms) {
-    const GPlan g = dgrad_plan(M, N, K, lora_stages(M, n_adapters, R), sms);
+int64_t dgrad_ctas(const ProbShape& s, int64_t M, int n_adapters, int R, int sms) {
+    const GPlan g = dgrad_plan(M, s.N, s.K, alpha_terms(s), lora_stages(M, n_adapters, R), sms);
     return std::min<int64_t>((int64_t)g.mtiles * g.ktiles * g.splits, sms);
 }
 
 int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, const float* scales, const uint16_t* dY,
                  int64_t ldy, int64_t M, uint16_t* dX, const LoraGradArgs* lora, void* workspace, int sms,
                  cudaStream_t stream) {
-    const GPlan g = dgrad_plan(M, s.N, s.K, lora ? lora_stages(M, lora->n_adapters, lora->R) : 0, sms);
-    const int terms = s.granularity == SHERRY_PER_TENSOR ? 1 : 2;  // of alpha
+    const int terms = alpha_terms(s);
+    const GPlan g = dgrad_plan(M, s.N, s.K, terms, lora ? lora_stages(M, lora->n_adapters, lora->R) : 0, sms);
     CUtensorMap map;
     int st = encode_2d(&map, dY, ldy, M, 128, kGN / terms);
     if (st) return st;
@@ -601,7 +606,7 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
     P.mtiles = g.mtiles;
     P.ktiles = g.ktiles;
     P.splits = g.splits;
-    P.nstages = (int)((s.N * terms + kGN - 1) / kGN);
+    P.nstages = g.nstages;
     CUtensorMap ypmap = map, pmap = map, amap = map;
     if (lora) {
         P.plan = lora->plan;
@@ -638,7 +643,7 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
 
 int dgrad_join_launch(const ProbShape& s, const float* scales, int64_t M, uint16_t* dX, const void* workspace,
                       int n_adapters, int R, int sms, cudaStream_t stream) {
-    const GPlan g = dgrad_plan(M, s.N, s.K, lora_stages(M, n_adapters, R), sms);
+    const GPlan g = dgrad_plan(M, s.N, s.K, alpha_terms(s), lora_stages(M, n_adapters, R), sms);
     if (g.splits == 1) return SHERRY_OK;
     const int64_t total = M * s.K;
     return launch_after(k_dgrad_join, (unsigned)((total / 4 + 255) / 256), 256, 0, stream, 1, true,

@@ -87,7 +87,7 @@ struct LoraGradArgs {
     int R, n_adapters;
     LoraPlan plan;
 };
-int64_t dgrad_ctas(int64_t M, int64_t N, int64_t K, int n_adapters, int R, int sms);  // 0 adapters: the plain gradient
+int64_t dgrad_ctas(const ProbShape& s, int64_t M, int n_adapters, int R, int sms);  // 0 adapters: the plain gradient
 // dX = dY (T alpha) (+ P A_a): dY bf16 rows ldy apart (a multiple of 8), lora null for the plain gradient (dgrad.cu)
 size_t dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int n_adapters, int R, int sms);
 int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, const float* scales, const uint16_t* dY,

@@ -28,9 +28,13 @@
 //   warps 0..7   epilogue: TMEM -> registers -> dX (bf16) or, where n is split over
 //                CTAs, fp32 partial sums that k_dgrad_join adds in order
 //   warps 8..23  decode, two groups that take the stages in turn: a stage's waits, lookups and
-//                fences are a chain of some 1500 cycles (4096 x 8192 x 2048: 116 -> 107 us)
+//                fences are a chain of some 1500 cycles (one term, 4096 x 8192 x 2048: 116 -> 107 us)
 //   warp 24      TMA, warp 25 MMA issue
 // n is split where there are fewer tiles than SMs.
+//
+// Bound by the tensor cores: at 4096 x 8192 x 2048 with adapters of rank 32 the tensor pipe is
+// 89% busy on the 128 SMs that have a tile.  Without adapters 174 us for two terms (the
+// operations of both at the measured rate: 165), 111 for a per-tensor scale (83).
 #include "common.cuh"
 #include "lora.cuh"
 #include "lut.cuh"
@@ -200,7 +204,7 @@ k_dgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtens
         };
         // A CTA with one item has its stages to itself once the last product is done: results go through them, so
         // that a store covers whole lines of a row and not 16 bytes of 32 rows
-        // (256 x 2048 x 2048: 15.4 -> 13.7 us)
+        // (one term, 256 x 2048 x 2048: 15.4 -> 13.5 us)
         const bool staged = items <= (int)gridDim.x;
         const int pitch = kGK * (P.splits == 1 ? 2 : 4) + 16;  // bytes
         const int c0 = TM == 2 ? 0 : half * COLS;

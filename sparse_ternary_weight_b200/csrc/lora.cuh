@@ -97,7 +97,7 @@ int dgrad_launch(const ProbShape& s, const uint32_t* idx, const uint8_t* sgn, co
 int dgrad_join_launch(const ProbShape& s, const float* scales, int64_t M, uint16_t* dX, const void* workspace,
                       int n_adapters, int R, int sms, cudaStream_t stream);
 
-// bytes of a plan, and the plan laid out in `mem` (256-byte aligned); false where it is too large
+// bytes of a plan, and the plan laid out in `mem` (256-byte aligned)
 size_t lora_plan_bytes(int64_t M, int n_adapters);
 LoraPlan lora_plan_in(void* mem, int64_t M, int n_adapters);
 int lora_plan_launch(const int32_t* ids, int64_t M, int n_adapters, const LoraPlan& plan, cudaStream_t stream);

@@ -11,9 +11,11 @@
 // are fp32, promoted with alpha, and the warps' are joined in order.  The second
 // launch starts beside the first and waits for U only then.
 //
-// Bound by latency: at 16 tokens x 8192 x 2048 the packed planes are 2.6 MB (0.4 us of
-// HBM) and the lookups 1 us of shared memory.  tcgen05's tiles of 128 rows would leave
-// most SMs without one; rows of 16 give every SM three CTAs.
+// Bound by latency: at 16 tokens x 8192 x 2048 no pipe is full (LSU 57%, a third of that
+// bank conflicts between the rows that one load touches; issue slots 28%, DRAM 6%); the
+// warps wait for loads 39% of their time, sixteen of them per SM (128 registers a thread), and 512
+// CTAs are 1.7 waves.  10 us a call.  (At 1 x 8192 x 8192 the LSU is 80% busy.)  tcgen05's tiles of
+// 128 rows would leave most SMs without one; rows of 16 give every SM three CTAs or more.
 #include "lora.cuh"
 #include "lut.cuh"
 #include "tc.cuh"

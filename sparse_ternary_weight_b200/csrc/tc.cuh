@@ -87,6 +87,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 
 // Launches that overlap their predecessor's end (launch_after): everything before pdl_wait touches
 // nothing that a kernel before it writes; after it, all of the stream's earlier work is complete.
+//
+// The adapters' kernels take their TMEM before they wait, and none waits for columns held by one that waits
+// for it: of two that overlap in a stream one is a k_lora_down, and what fits beside one of those in an SM's shared
+// memory never wants more than the 512 columns with it.  (k_lora_down has 85 KB or more for up to 128 columns;
+// k_prefill, k_dgrad and k_lora_grad have 192 or more for 512, k_lora_grad 80 for 256, 64 for 128, 48 for fewer.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -154,11 +159,6 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a, uint64_
         "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])                      \
         : "memory")
 
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }

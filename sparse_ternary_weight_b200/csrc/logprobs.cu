@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(TH, 1024 / TH) k_logprobs(const LpParams P) {
     if (rank == 0) {
         // log S relative to the true maximum: S was summed relative to ref = rn(m L)
         const bool dead = bmax == -INFINITY, bad = !(s1 < INFINITY);
-        float lsum = logf(s1) + (edge ? 0.0f : fmaf(-bmax, kLog2e, ref) * kLn2);
+        // (S holds a 1, so its logarithm is not below 0: rounding must not make a probability above 1)
+        float lsum = fmaxf(logf(s1) + (edge ? 0.0f : fmaf(-bmax, kLog2e, ref) * kLn2), 0.0f);
         if (dead) lsum = 0.0f;
         if (bad) lsum = NAN;
         if (tid == 0) {

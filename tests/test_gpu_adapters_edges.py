@@ -312,3 +312,24 @@ def test_gradients_of_a_slice_of_a_batch(sw, orc, N):
             for a, b in ((0, 3), (3, 40))]
     # (the order of the two is autograd's: a sum of two bf16 numbers does not depend on it)
     assert torch.equal(A.grad, both[0] + both[1])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_no_probability_above_one(sw, dt):
+    """Rows that leave one token, or one far above the rest: log S >= 0 and log p <= 0, near 0 for
+    maxima of every size.  Up to 1e8 the rounding of m log2(e) is at most 4 (half a step at 2^27), so S = 2^y with
+    |y| <= 4: the exponential is off by 2^-22 of itself, its logarithm (up to 2.8) by one step, 2^-22, and the
+    product that takes y ln 2 back out by two half steps of 2.8 and ln 2's own, 3 x 2^-23: 2^-20 in all."""
+    import torch
+    T = torch.float32 if dt == "f32" else torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    size = 10.0 ** torch.linspace(-6, 7.9, 3000, device="cuda")
+    z = torch.full((3000, 40), float("-inf"), dtype=T, device="cuda")
+    lead = torch.where(torch.rand(3000, generator=gen, device="cuda") < 0.5, -size, size).to(T)
+    t = torch.randint(0, 40, (3000,), generator=gen, device="cuda", dtype=torch.int32)
+    z.scatter_(1, t.long()[:, None], lead[:, None])
+    z[::3] = torch.where(torch.isinf(z[::3]), (lead[::3, None].float() - 200 - 2 * lead[::3, None].float().abs()).to(T), z[::3])
+    for x, y in ((z, t), (z[:1], t[:1]), (lead[:, None].contiguous(), torch.zeros_like(t))):
+        r = sw.token_logprobs(x, y, top=1)
+        assert bool((r.stats[:, 1] >= 0).all()) and bool((r.logp <= 0).all()) and bool((r.top_logp <= 0).all())
+        assert float(r.logp.min()) >= -2.0 ** -20 and float(r.entropy.max()) <= 2.0 ** -20 and float(r.entropy.min()) >= 0

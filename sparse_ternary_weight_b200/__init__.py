@@ -574,12 +574,16 @@ def _adapters(X, P, A, B, ids, scaling):
     return (A.contiguous(), B.contiguous(), ids.contiguous(), None if scaling is None else scaling.contiguous(), n, R)
 
 
-def _result(out, shape, dtype, device):
+def _result(out, shape, dtype, device, *inputs):
+    """``out`` checked, or a new tensor; the kernels read ``inputs`` while they write it."""
     import torch
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape) or not out.is_contiguous() or out.device != device:
         raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    for t in inputs:
+        if t is not None and out.numel() and t.numel() and _spans_overlap(out.view(1, -1), t.view(1, -1)):
+            raise ValueError("out must not overlap what the call reads")
     return out
 
 
@@ -601,7 +605,7 @@ def linear_lora(X, P: PackedWeight, A, B, ids, scaling=None, out_dtype=None, out
     X = _activations(X, P.K)
     A, B, ids, scaling, n, R = _adapters(X, P, A, B, ids, scaling)
     M = X.shape[0]
-    out = _result(out, (M, P.N), out_dtype, X.device)
+    out = _result(out, (M, P.N), out_dtype, X.device, X, A, B, ids, scaling, P.idx, P.sgn, P.scales)
     U = torch.empty((M, R), dtype=torch.float32, device=X.device) if return_u else None
     with _on(X.device):
         L = lib()
@@ -620,7 +624,7 @@ def linear_backward(dY, P: PackedWeight, out=None):
     dY = _output_gradient(dY, P.N)
     _planes(P, dY.device)
     M = dY.shape[0]
-    out = _result(out, (M, P.K), torch.bfloat16, dY.device)
+    out = _result(out, (M, P.K), torch.bfloat16, dY.device, dY, P.idx, P.sgn, P.scales)
     with _on(dY.device):
         L = lib()
         wsb = L.sherry_linear_backward_workspace_bytes(M, P.N, P.K)

@@ -333,3 +333,24 @@ def test_no_probability_above_one(sw, dt):
         r = sw.token_logprobs(x, y, top=1)
         assert bool((r.stats[:, 1] >= 0).all()) and bool((r.logp <= 0).all()) and bool((r.top_logp <= 0).all())
         assert float(r.logp.min()) >= -2.0 ** -20 and float(r.entropy.max()) <= 2.0 ** -20 and float(r.entropy.min()) >= 0
+
+
+def test_results_into_what_is_read_are_refused(sw, orc):
+    """A square layer's input has its output's shape: writing over it would feed other tiles half of it."""
+    import torch
+    pr = Problem(sw, orc, 300, 256, 256, "group", 128, 16, 3, "mixed")
+    bf = torch.bfloat16
+    buf = torch.zeros(310, 256, dtype=bf, device="cuda")
+    buf[:300] = pr.X
+    X = buf[:300]
+    for out in (X, buf[10:], buf[5:305]):
+        with pytest.raises(ValueError, match="overlap"):
+            sw.linear_lora(X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, bf, out=out)
+        with pytest.raises(ValueError, match="overlap"):
+            sw.linear_backward(X, pr.P, out=out)
+    two = torch.zeros(600, 256, dtype=bf, device="cuda")
+    two[:300] = pr.X
+    want = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, bf)
+    assert torch.equal(sw.linear_lora(two[:300], pr.P, pr.A, pr.B, pr.ids, pr.scaling, bf, out=two[300:]), want)
+    empty = torch.empty(0, 256, dtype=bf, device="cuda")
+    assert sw.linear_backward(empty, pr.P, out=empty) is empty

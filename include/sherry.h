@@ -265,8 +265,8 @@ float sherry_arenas_lambda(int64_t step, int64_t total, float lambda0);
  * dX[m][k] = sum_n dY[m][n] t[n][k] alpha(n,k), bf16, for training whatever lies
  * below a frozen packed weight ("Sherry, Tequila and Fairies in Python" section
  * 1.1: the layer is F.linear(x, w), whose gradient in x is dY w).
- *   dY       bf16 [M][N] row-major; read only
- *   dX       bf16 [M][K]; fully overwritten
+ *   dY       bf16 [M][N] row-major, 16-byte aligned; read only
+ *   dX       bf16 [M][K]; fully overwritten; must not overlap dY
  *   workspace  sherry_linear_backward_workspace_bytes(M, N, K) bytes of scratch
  *            (no tickets; need not be zero)
  * Accumulated in fp32 and rounded once.  alpha varies along the sum, so it enters the
@@ -289,7 +289,7 @@ size_t sherry_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   scaling  fp32 [n_adapters], or NULL for 1
  *   U        fp32 [M][rank] (16-byte aligned), optional (NULL): written, zero for
  *            tokens of no adapter; the backward pass wants it
- *   Y        as sherry_linear
+ *   Y        as sherry_linear; like U it must not overlap what is read
  *   workspace  sherry_linear_lora_workspace_bytes(...) bytes, 256-byte aligned; where
  *            sherry_linear_lora_needs_tickets says so a linear workspace (its first 256
  *            KiB zero before first use, left zero by every call), otherwise any scratch

@@ -354,3 +354,32 @@ def test_results_into_what_is_read_are_refused(sw, orc):
     assert torch.equal(sw.linear_lora(two[:300], pr.P, pr.A, pr.B, pr.ids, pr.scaling, bf, out=two[300:]), want)
     empty = torch.empty(0, 256, dtype=bf, device="cuda")
     assert sw.linear_backward(empty, pr.P, out=empty) is empty
+
+
+@pytest.mark.parametrize("R,dt", [(128, "f32"), (64, "f32"), (16, "bf16")])
+def test_calls_at_once_on_two_streams(sw, orc, R, dt):
+    """Forward and backward of two problems side by side, with and without dX, again and again: kernels of both
+    share SMs, and each stream's results are those of the calls alone."""
+    import torch
+    T = torch.float32 if dt == "f32" else torch.bfloat16
+    prs = [Problem(sw, orc, 300, 384, 1024, "group", 128, R, 3, "mixed"), Problem(sw, orc, 900, 640, 512, "channel", 0, R, 9, "mixed")]
+
+    def step(pr):
+        y, u = sw.linear_lora(pr.X, pr.P, pr.A, pr.B, pr.ids, pr.scaling, T, return_u=True)
+        a = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, u, pr.scaling, T, need=(False, True, True))
+        b = sw.linear_lora_backward(pr.G, pr.X, pr.P, pr.A, pr.B, pr.ids, u, pr.scaling, T)
+        return [y, u, *a[1:], *b]
+
+    want = [step(pr) for pr in prs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(step(prs[i]))
+    torch.cuda.synchronize()
+    assert sw.device_status() == 0
+    for i in range(2):
+        for outs in got[i]:
+            assert all(torch.equal(p, q) for p, q in zip(outs, want[i]))

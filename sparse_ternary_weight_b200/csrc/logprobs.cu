@@ -28,7 +28,7 @@
 // thread joins two aligned vectors of the input into one of the output.  Both go past
 // the caches as streams.
 //
-// What bounds them, 2048 x 128256 bf16: the gradient HBM (159 us, as long as a copy of the same bytes takes).
+// What bounds them, 2048 x 128256 bf16: the gradient HBM (159 to 164 us, as long as a copy of the same bytes takes).
 // The forward 98 us without alternatives (a read at the copy's rate: 81) and 116 with 8: the pass loads an
 // iteration's vectors only when it has used the last (37% of the warps' time is waiting for loads; DRAM 59%, the
 // exponentials' pipe 57%), and a row's listing and ranking follow behind barriers.  One row: 5 us, and
